@@ -33,7 +33,8 @@ EXPORTS = ["cs_version", "cs_status_string", "cs_last_error", "cs_workspace_size
            "cs_select", "cs_sparse_ffn", "cs_exact_ffn", "cs_union_mask", "cs_decode_stack",
            "cs_stack_release", "cs_sparse_ffn_noalloc", "cs_decode_layer", "cs_permute_rows",
            "cs_hot_order", "cs_fit_scratch_size", "cs_fit_predictor", "cs_sparse_attention",
-           "cs_decode_attention"]
+           "cs_decode_attention", "cs_qcache_workspace_size", "cs_qcache_append", "cs_qcache_read",
+           "cs_qcache_attention", "cs_qcache_evict", "cs_qcache_trim"]
 
 
 class CsError(RuntimeError):
@@ -61,6 +62,17 @@ class _Attn(C.Structure):
 
 class _Sel(C.Structure):
     _fields_ = [("mode", C.c_int), ("k", C.c_int), ("tau", C.c_float), ("hot", C.c_int)]
+
+
+class _QCache(C.Structure):
+    _fields_ = [("batch", C.c_int), ("n_heads", C.c_int), ("d_head", C.c_int), ("capacity", C.c_int),
+                ("ld_batch", C.c_int64), ("ld_head", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("weight", C.c_void_p), ("pos", C.c_void_p)]
+
+
+class _Rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("dtype", C.c_int), ("ld_batch", C.c_int64), ("ld_token", C.c_int64),
+                ("ld_head", C.c_int64)]
 
 
 def library_path() -> str:
@@ -105,11 +117,20 @@ def lib():
             L.cs_fit_scratch_size.argtypes = [I, I, I, I]
             L.cs_fit_scratch_size.restype = S
             L.cs_fit_predictor.argtypes = [C.POINTER(_Layer), C.POINTER(_Pred), P, I, C.c_double, P, S, P]
+            QC, HR = C.POINTER(_QCache), C.POINTER(_Rows)
+            L.cs_qcache_workspace_size.argtypes = [I] * 6
+            L.cs_qcache_workspace_size.restype = S
+            L.cs_qcache_append.argtypes = [QC, HR, HR, I, P, P, P, P, P, S, P]
+            L.cs_qcache_read.argtypes = [QC, HR, HR, I, P, P, P, S, P]
+            L.cs_qcache_attention.argtypes = [QC, HR, I, I, P, P, P, C.c_float, C.c_float, P, HR, P, S, P]
+            L.cs_qcache_evict.argtypes = [QC, P, I, I, P, I, I, P, P, S, P]
+            L.cs_qcache_trim.argtypes = [QC, P, I, P, I, I, QC, P, S, P]
             for name in ("cs_workspace_init", "cs_get_device_error", "cs_pack_transpose",
                          "cs_predict", "cs_select", "cs_sparse_ffn", "cs_exact_ffn",
                          "cs_union_mask", "cs_decode_stack", "cs_stack_release",
                          "cs_sparse_ffn_noalloc", "cs_decode_layer", "cs_permute_rows", "cs_hot_order",
-                         "cs_fit_predictor", "cs_sparse_attention", "cs_decode_attention"):
+                         "cs_fit_predictor", "cs_sparse_attention", "cs_decode_attention", "cs_qcache_append",
+                         "cs_qcache_read", "cs_qcache_attention", "cs_qcache_evict", "cs_qcache_trim"):
                 getattr(L, name).restype = I
             _lib = L
     return _lib
@@ -363,6 +384,175 @@ def cs_fit_predictor(layer: FfnLayer, pred: Predictor, X, lam, stream=None):
     ptr = (buf.data_ptr() + 255) & ~255
     _check(lib().cs_fit_predictor(C.byref(layer.c), C.byref(pred.c), _ptr(X), N, float(lam), ptr, n,
                                   _stream(stream)))
+
+
+QCACHE_GROUP = 64   # channels that share one scale and offset
+
+
+class QCache:
+    """A KV cache held in 4 bits (see include/cs.h): k and v uint8 [batch,
+    n_heads, capacity, d_head / 2], k_scale and v_scale fp16 [batch, n_heads,
+    capacity, d_head / 64, 2], weight fp32 and pos int32 [batch, n_heads,
+    capacity] (either may be None).  The tensors may be views, as long as their
+    slots are contiguous and all step alike over sequences and heads.  For
+    cs_qcache_evict alone, weight (and pos) are enough."""
+
+    def __init__(self, k, v, k_scale, v_scale, weight=None, pos=None):
+        self.k, self.v, self.k_scale, self.v_scale, self.weight, self.pos = k, v, k_scale, v_scale, weight, pos
+        codes = (k, v, k_scale, v_scale)
+        if any(t is None for t in codes) != all(t is None for t in codes):
+            raise ValueError("k, v, k_scale and v_scale go together")
+        some = next((t for t in (k, weight, pos) if t is not None), None)
+        if some is None or some.dim() < 3:
+            raise ValueError("a cache has codes, or at least weights")
+        self.batch, self.n_heads, self.capacity = some.shape[:3]
+        self.d_head = 0 if k is None else 2 * k.shape[3]
+        lead, groups = tuple(some.shape[:3]), self.d_head // QCACHE_GROUP
+        ld = None
+        for t, dtype, tail in ((k, torch.uint8, (self.d_head // 2,)), (v, torch.uint8, (self.d_head // 2,)),
+                               (k_scale, torch.float16, (groups, 2)), (v_scale, torch.float16, (groups, 2)),
+                               (weight, torch.float32, ()), (pos, torch.int32, ())):
+            if t is None:
+                continue
+            if t.dtype != dtype or tuple(t.shape) != lead + tail:
+                raise ValueError(f"expected a {dtype} tensor of shape {lead + tail}, got {t.dtype} {tuple(t.shape)}")
+            ld = self._slots(t, tail, ld)
+        self.ld_batch, self.ld_head = ld
+        self.c = _QCache(self.batch, self.n_heads, self.d_head, self.capacity, self.ld_batch, self.ld_head, _ptr(k),
+                         _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), _ptr(pos))
+
+    def _slots(self, t, tail, ld=None):
+        """The slots from one sequence and one head of t to the next, which have to be `ld` if that is given."""
+        row = 1
+        for n, st in zip(reversed(tail), reversed(t.stride()[3:])):
+            if st != row and n > 1:
+                raise ValueError("a slot's values must be contiguous")
+            row *= n
+        if self.capacity > 1 and t.stride(2) != row:
+            raise ValueError("a head's slots must be contiguous")
+        dense = (self.n_heads * self.capacity, self.capacity)
+        got = []
+        for i, n in ((0, self.batch), (1, self.n_heads)):
+            if n > 1 and t.stride(i) % row:
+                raise ValueError("a cache tensor must step by whole slots")
+            got.append(t.stride(i) // row if n > 1 else dense[i])
+        if ld is not None and tuple(got) != tuple(ld):
+            raise ValueError("a cache's tensors must step alike over sequences and heads")
+        return tuple(got)
+
+    @classmethod
+    def empty(cls, batch, n_heads, capacity, d_head, device="cuda"):
+        """A cache of its own, with weights and positions, all slots empty."""
+        lead = (int(batch), int(n_heads), int(capacity))
+        z = lambda dtype, *tail: torch.zeros(lead + tail, dtype=dtype, device=device)  # noqa: E731
+        groups = d_head // QCACHE_GROUP
+        return cls(z(torch.uint8, d_head // 2), z(torch.uint8, d_head // 2), z(torch.float16, groups, 2),
+                   z(torch.float16, groups, 2), z(torch.float32), z(torch.int32).fill_(-1))
+
+
+class QCacheWorkspace:
+    """Device workspace of the cs_qcache_* calls on caches of this one's sizes,
+    with up to n_heads query heads and n_q query tokens per sequence."""
+
+    def __init__(self, cache: QCache, n_heads=None, n_q=1, device=None, stream=None):
+        heads = cache.n_heads if n_heads is None else int(n_heads)
+        n = lib().cs_qcache_workspace_size(cache.batch, cache.n_heads, cache.capacity, cache.d_head or QCACHE_GROUP,
+                                           heads, int(n_q))
+        if n == 0:
+            raise ValueError("no cs_qcache call takes these sizes")
+        self.nbytes = n
+        some = cache.k if cache.k is not None else cache.weight
+        self.buf = torch.empty(n + 256, dtype=torch.uint8, device=device or some.device)
+        self.ptr = (self.buf.data_ptr() + 255) & ~255
+        _check(lib().cs_workspace_init(self.ptr, self.nbytes, _stream(stream)))
+
+
+def _rows(t, batch, heads, d_head, what):
+    """cs_head_rows of a [batch, tokens, heads, d_head] tensor with contiguous rows."""
+    if t.dim() != 4 or t.shape[0] != batch or t.shape[2] != heads or t.shape[3] != d_head or t.stride(3) != 1:
+        raise ValueError(f"{what}: expected [{batch}, tokens, {heads}, {d_head}] with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.dtype not in _TORCH_DT:
+        raise ValueError(f"{what}: dtype {t.dtype} is not fp32, fp16 or bf16")
+    return _Rows(_ptr(t), _dt(t), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _ints(t, shape, what):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous int32 tensor of shape {tuple(shape)}")
+    return _ptr(t)
+
+
+def cs_qcache_append(cache: QCache, k, v, ws: QCacheWorkspace, start=None, slots=None, n_new=None, pos=None,
+                     stream=None):
+    """Quantise the new rows k and v [batch, n, n_heads, d_head] into slots
+    start[b] + t, or slots[b, h, t] (see include/cs.h)."""
+    B, H = cache.batch, cache.n_heads
+    kr, vr = _rows(k, B, H, cache.d_head, "k"), _rows(v, B, H, cache.d_head, "v")
+    n = k.shape[1]
+    if v.shape[1] != n:
+        raise ValueError("k and v differ in their number of tokens")
+    _check(lib().cs_qcache_append(C.byref(cache.c), C.byref(kr), C.byref(vr), n, _ints(start, (B,), "start"),
+                                  _ints(slots, (B, H, n), "slots"), _ints(n_new, (B,), "n_new"),
+                                  _ints(pos, (B,), "pos"), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def cs_qcache_read(cache: QCache, k, v, ws: QCacheWorkspace, start=None, slots=None, stream=None):
+    """The values of slots start[b] + t, or slots[b, h, t], into k and v
+    [batch, n, n_heads, d_head] (see include/cs.h)."""
+    B, H = cache.batch, cache.n_heads
+    kr, vr = _rows(k, B, H, cache.d_head, "k"), _rows(v, B, H, cache.d_head, "v")
+    n = k.shape[1]
+    if v.shape[1] != n:
+        raise ValueError("k and v differ in their number of tokens")
+    _check(lib().cs_qcache_read(C.byref(cache.c), C.byref(kr), C.byref(vr), n, _ints(start, (B,), "start"),
+                                _ints(slots, (B, H, n), "slots"), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def cs_qcache_attention(cache: QCache, q, length, out, ws: QCacheWorkspace, q_pos=None, mask=None, scale=0.0,
+                        weight=None, decay=1.0, stream=None):
+    """Attention of q [batch, n_q, n_heads, d_head] over the first length[b]
+    slots into out (see include/cs.h).  mask: int32 or uint32 [batch,
+    ceil(n_heads / 32)], the query heads to compute (cs_select's mask).
+    weight: gathers decay * cache.weight + this step's attention per slot; a
+    tensor that steps like cache.weight, often cache.weight itself."""
+    B = cache.batch
+    if q.dim() != 4 or q.shape != out.shape:
+        raise ValueError("q and out must be [batch, n_q, n_heads, d_head] tensors of one shape")
+    heads = q.shape[2]
+    qr, orr = _rows(q, B, heads, cache.d_head, "q"), _rows(out, B, heads, cache.d_head, "out")
+    if mask is not None and (mask.element_size() != 4 or mask.is_floating_point() or not mask.is_contiguous()
+                             or tuple(mask.shape) != (B, -(-heads // 32))):
+        raise ValueError("mask: expected contiguous 32-bit words [batch, ceil(n_heads / 32)]")
+    if weight is not None:
+        if weight.dtype != torch.float32 or tuple(weight.shape) != (B, cache.n_heads, cache.capacity):
+            raise ValueError("weight: expected fp32 [batch, n_heads, capacity]")
+        cache._slots(weight, (), (cache.ld_batch, cache.ld_head))
+    _check(lib().cs_qcache_attention(C.byref(cache.c), C.byref(qr), heads, q.shape[1], _ints(length, (B,), "length"),
+                                     _ints(q_pos, (B,), "q_pos"), _ptr(mask), float(scale), float(decay),
+                                     _ptr(weight), C.byref(orr), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def cs_qcache_evict(cache: QCache, length, limit, slots, ws: QCacheWorkspace, next_pos=None, sinks=0, recent=0,
+                    stream=None):
+    """slots [batch, n_heads, n] = where the next n tokens go when at most
+    `limit` slots may be in use (see include/cs.h)."""
+    B = cache.batch
+    if slots.dim() != 3:
+        raise ValueError("slots: expected int32 [batch, n_heads, n]")
+    n = slots.shape[2]
+    _check(lib().cs_qcache_evict(C.byref(cache.c), _ints(length, (B,), "length"), int(limit), n,
+                                 _ints(next_pos, (B,), "next_pos"), int(sinks), int(recent),
+                                 _ints(slots, (B, cache.n_heads, n), "slots"), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def cs_qcache_trim(cache: QCache, length, keep, dst: QCache, ws: QCacheWorkspace, next_pos=None, sinks=0, recent=0,
+                   stream=None):
+    """Copy each head's `keep` heaviest slots to the front of dst (see
+    include/cs.h)."""
+    _check(lib().cs_qcache_trim(C.byref(cache.c), _ints(length, (cache.batch,), "length"), int(keep),
+                                _ints(next_pos, (cache.batch,), "next_pos"), int(sinks), int(recent),
+                                C.byref(dst.c), ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def cs_stack_release():

@@ -395,6 +395,144 @@ size_t cs_fit_scratch_size(int d, int f, int r, int N);
 cs_status cs_fit_predictor(const cs_ffn_layer *layer, cs_predictor *pred, const float *X, int N, double lambda,
                            void *scratch, size_t scratch_bytes, cs_stream_t stream);
 
+/*
+ * A KV cache held in 4 bits, for serving many sequences with a bounded number
+ * of slots each.  For `batch` sequences and `n_heads` key/value heads it has
+ * `capacity` slots; a slot holds one key row and one value row of d_head
+ * channels.  A row is cut into groups of 64 channels, and a group keeps
+ *     scale = fp16((max - min) * fp32(1 / 15)),  offset = fp16(min)
+ * and one code per channel, the nearest of 0 .. 15 to (x - offset) / scale
+ * (halves to even; 0 where scale is 0), which stands for offset + scale * code.
+ * Rows are clamped to +-65504 first and NaN counts as 0, so a written slot
+ * never holds an infinity or NaN.
+ *   k, v:             [batch, n_heads, capacity, d_head / 2] bytes; byte i
+ *                     holds channel 2i in its low half and 2i + 1 in its high.
+ *   k_scale, v_scale: [batch, n_heads, capacity, d_head / 64, 2] fp16, a
+ *                     group's scale, then its offset.
+ *   weight:           [batch, n_heads, capacity] fp32 or NULL: the attention
+ *                     weight that the slot has gathered (eviction's measure).
+ *   pos:              [batch, n_heads, capacity] int32 or NULL: the position
+ *                     of the slot's token; negative marks an empty slot.
+ *   ld_batch, ld_head: slots from one sequence (head) to the next, the same
+ *                     for all six arrays; 0 means dense.
+ * d_head is 64, 128, 192 or 256; batch <= 4096; k and v 16-byte aligned, the
+ * others 4-byte.  Which slots of a sequence are in use is the caller's to
+ * keep: calls take the number per sequence (slots 0 .. length - 1), one
+ * number for all heads, and none of them changes it.  One cache object stands
+ * for one layer.
+ */
+typedef struct cs_qcache {
+    int batch, n_heads, d_head, capacity;
+    int64_t ld_batch, ld_head;
+    uint8_t *k, *v;
+    void *k_scale, *v_scale;
+    float *weight;
+    int32_t *pos;
+} cs_qcache;
+
+/*
+ * Rows of d_head contiguous elements outside a cache: element (b, t, h, c) of
+ * a [batch, tokens, heads, d_head] array is data[b * ld_batch + t * ld_token +
+ * h * ld_head + c], strides in elements, data aligned to one element (rows on
+ * 16-byte boundaries are read and written fastest).
+ */
+typedef struct cs_head_rows {
+    void *data;
+    cs_dtype dtype;
+    int64_t ld_batch, ld_token, ld_head;
+} cs_head_rows;
+
+/*
+ * Workspace bytes of the cs_qcache_* calls below on a cache of these sizes,
+ * with up to n_heads query heads (a multiple of kv_heads) and n_q query tokens
+ * per sequence; 0 for sizes that no call takes.  Initialise it once with
+ * cs_workspace_init; cs_get_device_error reads its error word.
+ */
+size_t cs_qcache_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n_q);
+
+/*
+ * Quantises n new tokens per sequence into the cache.  Token t of sequence b
+ * goes to slot slots[b, h, t] of head h ([batch, n_heads, n] int32 device, as
+ * cs_qcache_evict gives them), or to slot start[b] + t of every head ([batch]
+ * int32 device): exactly one of the two is given.
+ *   k, v: the new rows, n_heads heads, one dtype.
+ *   n_new: [batch] int32 device or NULL: how many of the n tokens sequence b
+ *      has (clamped to [0, n], CS_DEVERR_COUNT).
+ *   pos: [batch] int32 device, the position of sequence b's first new token;
+ *      required if and only if the cache has positions.
+ * A written slot's weight becomes 0.  A slot of -1 skips its row; any other
+ * slot outside [0, capacity) skips it and sets CS_DEVERR_INDEX.  Slots given
+ * twice in one call hold one of the rows' bytes each (unspecified).
+ */
+cs_status cs_qcache_append(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n,
+                           const int32_t *start, const int32_t *slots, const int32_t *n_new, const int32_t *pos,
+                           void *ws, size_t ws_bytes, cs_stream_t stream);
+
+/*
+ * The values that slots stand for, offset + scale * code, rounded once to the
+ * output's dtype.  Slots are given as in cs_qcache_append; one outside
+ * [0, capacity) gives a zero row (and sets CS_DEVERR_INDEX unless it is -1).
+ */
+cs_status cs_qcache_read(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n,
+                         const int32_t *start, const int32_t *slots, void *ws, size_t ws_bytes,
+                         cs_stream_t stream);
+
+/*
+ * Attention of n_q query tokens per sequence over the slots in use.  Query
+ * head h reads cache head g = h / (n_heads / cache->n_heads):
+ *     s_i = scale q . k_i,  p = softmax(s),  out = sum_i p_i v_i,
+ * over the slots i < length[b] (clamped to [0, capacity], CS_DEVERR_COUNT).
+ *   q, out: n_q tokens of n_heads heads, of one dtype.
+ *   q_pos: [batch] int32 device or NULL.  Given (the cache then needs
+ *      positions), token t sees only slots with 0 <= pos <= q_pos[b] + t.
+ *   mask: [batch, ceil(n_heads / 32)] uint32 device or NULL: the query heads
+ *      to compute, as cs_select writes them ([P1] first section: a small,
+ *      input-dependent set of heads).  Cache heads that no chosen head reads
+ *      are not read.
+ *   scale: the factor on q . k; 0 means 1 / sqrt(d_head).
+ *   weight: device fp32 or NULL, laid out like cache->weight (and allowed to
+ *      be it): weight[i] = decay * cache->weight[i] + the sum of p_i over the
+ *      head's group and the n_q tokens, for i < length[b]; other slots are not
+ *      written.  decay == 0 reads no old weights.
+ * A row that sees no slot, and a head that is not chosen, gives zeros and
+ * adds no weight.  Sums and softmax statistics are fp32; with the same
+ * arguments the results are the same bit for bit.
+ */
+cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int n_heads, int n_q,
+                              const int32_t *length, const int32_t *q_pos, const uint32_t *mask, float scale,
+                              float decay, float *weight, const cs_head_rows *out, void *ws, size_t ws_bytes,
+                              cs_stream_t stream);
+
+/*
+ * The slots that the next n tokens of every sequence take, per head, when at
+ * most `limit` slots may be in use: first the slots given up among the
+ * length[b] used ones (as many as the free ones fall short of n), then free
+ * ones from length[b] on, all ascending.  Given up are the first of this
+ * order: empty slots (pos < 0); then by weight, least first; then protected
+ * slots, least weight first.  Equal weights go by the lower slot, -0 equals
+ * +0, and NaN is below every number.  Protected are the tokens at positions
+ * below `sinks` and at next_pos[b] - recent or later.  Needs weights only
+ * (and positions, if the cache has them): k, v and the scales may be NULL.
+ *   next_pos: [batch] int32 device: the position of the next token; may be
+ *      NULL when recent is 0.  sinks and recent need positions.
+ *   slots: [batch, n_heads, n] int32 device (output).  1 <= n <= limit <=
+ *      capacity.
+ * After the tokens are in (cs_qcache_append with these slots), the number of
+ * slots in use is min(length[b] + n, limit).
+ */
+cs_status cs_qcache_evict(const cs_qcache *cache, const int32_t *length, int limit, int n, const int32_t *next_pos,
+                          int sinks, int recent, int32_t *slots, void *ws, size_t ws_bytes, cs_stream_t stream);
+
+/*
+ * Copies each head's last `keep` slots of the order above (the heaviest and
+ * the protected ones; all, if length[b] <= keep) to slots 0, 1, ... of dst, in
+ * ascending order of their slots, with weights and positions.  dst has the
+ * same batch, n_heads and d_head, at least `keep` slots, weights and positions
+ * if src has them, and memory of its own; its other slots are not written.
+ */
+cs_status cs_qcache_trim(const cs_qcache *src, const int32_t *length, int keep, const int32_t *next_pos, int sinks,
+                         int recent, const cs_qcache *dst, void *ws, size_t ws_bytes, cs_stream_t stream);
+
 /* Drops every cached stack and layer graph (waits for nothing; call when idle). */
 cs_status cs_stack_release(void);
 
