@@ -193,8 +193,12 @@ __global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
     __shared__ int hist[256];
     __shared__ int wsum[32];
     __shared__ int pick[2];
+    __shared__ int used_s;
     const int cap = a.keep >= 0 ? a.c.cap : a.limit;
-    const int used = q_length(a.length, b, cap, a.err);
+    // one thread reads it: the barriers below need one answer, whatever else writes there meanwhile
+    if (tid == 0) used_s = q_length(a.length, b, cap, a.err);
+    __syncthreads();
+    const int used = used_s;
     const int e = a.keep >= 0 ? max(0, used - a.keep) : max(0, a.n - (cap - used));
     const int64_t slot0 = a.c.slot0(b, h);
     const float *w = a.c.weight + slot0;
@@ -236,8 +240,10 @@ __global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
             want -= pick[1];
         }
     }
-    // `want` of the slots equal to (c, key) go, the first ones
-    int32_t *out = a.out + ((int64_t)b * a.c.heads + h) * (a.keep >= 0 ? a.keep : a.n);
+    // `want` of the slots equal to (c, key) go, the first ones; weights that another kernel changes meanwhile
+    // must not lead past the list
+    const int room = a.keep >= 0 ? a.keep : a.n;
+    int32_t *out = a.out + ((int64_t)b * a.c.heads + h) * room;
     int equal = 0, put = 0;
     for (int i0 = 0; i0 < used; i0 += kEvictThreads) {
         const int i = i0 + tid;
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
         if (a.keep >= 0) take = i < used && !take;
         const int at = put + block_excl_scan(take, wsum, &n);
         put += n;
-        if (take) out[at] = i;
+        if (take && at < room) out[at] = i;
     }
     if (a.keep < 0)
         for (int i = e + tid; i < a.n; i += kEvictThreads) out[i] = used + i - e;
@@ -272,7 +278,9 @@ __global__ void __launch_bounds__(256) qtrim_kernel(QEvictCall a, QCacheK dst) {
     const int t = (int)(item / words);
     int w = (int)(item % words);
     if (t >= min(a.keep, q_length(a.length, b, a.c.cap, nullptr))) return;
-    const int64_t from = a.c.slot0(b, h) + ld_dep(a.out + ((int64_t)b * a.c.heads + h) * a.keep + t);
+    const int slot = ld_dep(a.out + ((int64_t)b * a.c.heads + h) * a.keep + t);
+    if (slot < 0 || slot >= a.c.cap) return;
+    const int64_t from = a.c.slot0(b, h) + slot;
     const int64_t to = dst.slot0(b, h) + t;
     auto word = [](void *p, int64_t slot, int per, int i) { return reinterpret_cast<uint32_t *>(p) + slot * per + i; };
     if (w < cw) { *word(dst.k, to, cw, w) = ld_dep(word(a.c.k, from, cw, w)); return; }
@@ -450,6 +458,10 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
     CS_CHECK(n_q >= 0, "%s: n_q=%d is negative", who, n_q);
     if ((int64_t)n_heads / cache->n_heads * n_q > kQMaxRows) {
         set_error("%s: %d query rows per cache head, above %d", who, n_heads / cache->n_heads * n_q, kQMaxRows);
+        return CS_ERR_UNSUPPORTED;
+    }
+    if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16) >= INT32_MAX) {
+        set_error("%s: batch x n_heads x capacity is too large", who);
         return CS_ERR_UNSUPPORTED;
     }
     CS_CHECK(length && aligned(length, 4), "%s: length is null or misaligned", who);
