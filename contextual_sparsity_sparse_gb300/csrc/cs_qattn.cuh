@@ -1,0 +1,1014 @@
+// Attention over the 4-bit KV cache: the kernels, a translation unit per
+// d_head (cs_qattn64.cu ...); cs_qattn.cu holds the host side.
+//
+// Per query row r (a query head of a cache head's group, at one query token):
+//     x_i = q_r . k_i (q scaled),   p_i = 2^((x_i - m) c1),   out = sum p_i v_i / sum p_i.
+// With k = z + s n and v = z + s n per group of 64 channels (n = 0 .. 15):
+//     q . k = sum_g s_g (q . (n - 8))_g + (z_g + 8 s_g) (sum q)_g
+//     sum_i p_i v_i = sum_i (p_i s_i) (n_i - 8) + sum_i p_i (z_i + 8 s_i)
+// so the codes go into matrix products as they are and the scales meet only
+// sums (keys) or probabilities (values).
+//
+// Two kernels.  In the first the slots of all sequences and heads, cut into
+// units of UT slots, are one long axis that is split evenly over the CTAs,
+// whatever the lengths: a CTA may take the end of one head's slots, some whole
+// heads, and the start of another.  Its warps take the units of a head in
+// turn, each with its own running maximum and sums, fed by its own ring of
+// asynchronous copies, which runs on across heads; at a head's end the warps'
+// sums are joined.  A head that lies in one CTA is finished there; else the CTA
+// leaves a partial record, and the second kernel joins the records and
+// finishes (with the same split, every CTA a share of the record sums).
+// Starting and joining a head costs a CTA about as long as kHeadCost units, so
+// a head is that much longer on the axis.
+//
+// Products.  mma.sync m16n8k16 in fp16 with fp32 sums: the query rows are the
+// 8 columns, so a batch-1 head wastes little, and the codes are the A operand
+// straight from their packed words.  For the keys, 16 slots x 16 channels: a
+// nibble ANDed out of a word is an fp16 subnormal n 2^-24 (or, four bits up,
+// n 2^-20), exact in the product; the factor 16 goes into q, and the sums start
+// at -8 (sum q).  For the values, 16 channels x 16 slots: two slots' words are
+// interleaved by byte permutes, n is ORed into 1024 + n and 1032 subtracted.
+// The tensor-memory path of the newer matrix instructions needs 128 rows and
+// operands in shared memory; with at most 16 query rows per head the products
+// are not what bounds this kernel, the instructions around them are.
+//
+// Precision.  q is scaled by a power of two and split into two fp16 parts (22
+// bits; the second is zero for 16-bit inputs).  p s is scaled so that the
+// largest stays below 2^15 and split likewise; for bf16 outputs one part is
+// enough (2^-12 beside the output's 2^-9).  With at most 4 rows the two parts
+// sit in the same 8 columns.  All sums and the softmax statistics are fp32.
+#pragma once
+
+#include "cs_qcache.cuh"
+
+namespace cs {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kHeadCost = 8;
+
+struct QAttnK {
+    QAttnArgs a;
+    int group, rows;     // query heads per cache head; rows of this pass
+    int row0;            // its first row: row r is head r % group of the group, token r / group
+    int grid;            // CTAs of both kernels
+    float *part;         // [grid, 2] records: per column its maximum, sum and c1, then the sums of p v
+    float *logit;        // [grid, 2, area / RP, RP] x, for the weights
+    int64_t area;        // floats of one CTA's half of logit
+    float c2, sign;      // |scale| log2(e), and the scale's sign
+};
+
+// Query columns per pass and how they sit in the 8 columns of a product.
+enum QMode { PACK4 = 0, ONE8 = 1, TWO8 = 2 };
+
+// The launchers of one d_head (mode, whether p s and q have second parts).
+template <int D>
+cudaError_t run_qattn(QAttnK k, int mode, bool lo, int64_t cost, cudaStream_t s);
+
+#ifdef CS_QATTN_KERNELS
+
+namespace {
+
+template <int D, int MODE>
+struct Cfg {
+    static constexpr int NT = MODE == TWO8 ? 2 : 1;          // tiles of 8 columns
+    static constexpr int RP = MODE == PACK4 ? 4 : 8 * NT;    // query rows
+    static constexpr int PARTS = MODE == PACK4 ? 1 : 2;      // q's two parts: same or separate products
+    static constexpr int G = D / kQGroup;
+    static constexpr int UT = D <= 128 ? 32 : 16;            // slots per unit
+    static constexpr int SUB = UT / 16;
+    static constexpr int RB = D / 2;                         // bytes of a row
+    static constexpr int STAGE = UT * (2 * RB + 8 * G + 4);  // one unit: keys, values, their scales, positions
+    static constexpr int MINB = D * NT <= 128 ? 2 : 1;       // CTAs per SM
+    static constexpr int ST = D == 64 ? 4 : MINB == 2 ? 2 : 3;
+    static constexpr int RS = D + 4;                         // floats of a joined column (conflict-free)
+    static constexpr int QF = NT * PARTS * (D / 32) * 32;    // uint4 fragments of q, two products each
+    static constexpr int RED = kWarps * 4 * RS;              // floats: four columns of every warp
+    static constexpr int CS = 3 + G;                         // floats of a column: c1, last position, on, sums of q
+    static constexpr int STAT = kWarps * RP * 2 + 3 * RP;    // floats: the warps' bases and sums, then the joined ones
+    static constexpr int REC = RP * (D + 3);                 // floats of a record
+    static constexpr size_t smem_fixed = (size_t)kWarps * ST * STAGE + QF * 16 + (RED + RP * CS + STAT) * 4;
+};
+
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if (N == 16) asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_or0(uint32_t dst, const void *src, bool on) {
+    if (N == 16) asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ T lds(const char *p) { return *reinterpret_cast<const T *>(p); }
+// A slot's G scale words.
+template <int G>
+__device__ __forceinline__ void lds_scales(const char *p, uint32_t (&w)[G]) {
+    if (G == 2) {
+        const uint2 v = lds<uint2>(p);
+        w[0] = v.x;
+        w[1 % G] = v.y;
+    } else if (G == 4) {
+        const uint4 v = lds<uint4>(p);
+        w[0] = v.x;
+        w[1 % G] = v.y;
+        w[2 % G] = v.z;
+        w[3 % G] = v.w;
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) w[g] = lds<uint32_t>(p + 4 * g);
+    }
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (x & mask) | or
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t o) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(o));
+    return r;
+}
+__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Where a 16-byte chunk of a unit's row lies: pairs of chunks (the 32 bytes of a
+// group) are permuted so that the four slots of which a half warp reads the
+// keys, or a warp the values, lie in different banks.  Rows of 32 and 96 bytes
+// need nothing.
+template <int D>
+__device__ __forceinline__ int swizzle(int tok) { return D == 128 ? tok & 2 : D == 256 ? (tok & 3) << 1 : 0; }
+// The slot within 16 that is row i of a product.  Of any four in the above, no
+// two are alike modulo 4; slot_of_row(i + 1) = slot_of_row(i) ^ 2 for even i.
+__device__ __forceinline__ int slot_of_row(int i) {
+    return (i & 8) | (i & 4) | (((i & 1) ^ ((i >> 2) & 1)) << 1) | ((i >> 1) & 1);
+}
+
+// ------------------------------------------------------------ the split axis
+
+// Whether a cache head has a chosen query head.
+__device__ __forceinline__ bool kv_on(const QAttnK &k, int b, int h) {
+    if (!k.a.mask) return true;
+    const uint32_t *m = k.a.mask + (int64_t)b * ((k.a.heads + 31) / 32);
+    for (int j = h * k.group; j < (h + 1) * k.group;) {
+        const int bit = j & 31, n = min(32 - bit, (h + 1) * k.group - j);
+        const uint32_t w = ld_dep(m + (j >> 5)) >> bit;
+        if (n == 32 ? w : w & ((1u << n) - 1u)) return true;
+        j += n;
+    }
+    return false;
+}
+
+__device__ __forceinline__ bool row_on(const QAttnK &k, int b, int h, int r) {
+    if (r >= k.rows) return false;
+    if (!k.a.mask) return true;
+    const int j = h * k.group + (k.row0 + r) % k.group;
+    return ld_dep(k.a.mask + (int64_t)b * ((k.a.heads + 31) / 32) + (j >> 5)) >> (j & 31) & 1u;
+}
+
+// The cache head that is the sequence's n-th with a chosen query head.
+__device__ __forceinline__ int chosen_head(const QAttnK &k, int b, int n) {
+    if (!k.a.mask) return n;
+    int h = 0;
+    for (; h < k.a.c.heads - 1; ++h)
+        if (kv_on(k, b, h) && n-- == 0) break;
+    return h;
+}
+
+// In shared memory per sequence: its length, and where it starts on the axis (one more at the end).
+struct Axis {
+    int *len, *pre;
+    int per;          // a CTA's length of the axis
+    int begin, end;   // this CTA's part
+
+    template <int UT>
+    __device__ __forceinline__ int take(const QAttnK &k, int b, bool flag) {
+        const int n = q_length(k.a.length, b, k.a.c.cap, flag ? k.a.err : nullptr);
+        int heads = k.a.c.heads;
+        if (k.a.mask) {
+            heads = 0;
+            for (int h = 0; h < k.a.c.heads; ++h) heads += kv_on(k, b, h);
+        }
+        len[b] = n;
+        return n ? ((n + UT - 1) / UT + kHeadCost) * heads : 0;
+    }
+
+    template <int UT>
+    __device__ void build(const QAttnK &k, int *smem, int *wsum, bool flag) {
+        len = smem;
+        pre = smem + k.a.c.batch;
+        const int B = k.a.c.batch;
+        int total;
+        if (B <= 32) {
+            // every warp writes the same values, so no warp waits for another
+            const int lane = threadIdx.x & 31;
+            const int v = lane < B ? take<UT>(k, lane, flag) : 0;
+            int inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(kFull, inc, o);
+                if (lane >= o) inc += n;
+            }
+            total = __shfl_sync(kFull, inc, 31);
+            if (lane < B) pre[lane] = inc - v;
+            if (lane == 0) pre[B] = total;
+            __syncwarp();
+        } else {
+            const int each = (B + kThreads - 1) / kThreads;
+            const int b0 = min(B, (int)threadIdx.x * each), b1 = min(B, b0 + each);
+            int sum = 0;
+            for (int b = b0; b < b1; ++b) {
+                const int v = take<UT>(k, b, flag);
+                pre[b] = v;   // not yet summed
+                sum += v;
+            }
+            int at = block_excl_scan(sum, wsum, &total);
+            for (int b = b0; b < b1; ++b) {
+                const int v = pre[b];
+                pre[b] = at;
+                at += v;
+            }
+            if (threadIdx.x == 0) pre[B] = total;
+            __syncthreads();
+        }
+        // a warp without a unit saves nothing, so a CTA takes at least one for each
+        per = max((total + k.grid - 1) / k.grid, kWarps + kHeadCost);
+        begin = (int)min((int64_t)total, (int64_t)blockIdx.x * per);
+        end = (int)min((int64_t)total, (int64_t)begin + per);
+    }
+};
+
+// A CTA's share of one head's units.
+struct Seg {
+    int b, h;         // sequence, and which of its chosen heads
+    int u0, u1;       // units [u0, u1) ...
+    int nu;           // ... of nu
+    int first;        // the first unit's place on the axis
+
+    __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == nu; }
+    __device__ __forceinline__ int next() const { return first + nu; }
+    template <int UT>
+    __device__ __forceinline__ void seek(const Axis &x, int at, int from_b) {
+        b = from_b;
+        while (x.pre[b + 1] <= at) ++b;
+        nu = (x.len[b] + UT - 1) / UT;
+        const int rel = at - x.pre[b];
+        h = rel / (nu + kHeadCost);
+        first = x.pre[b] + h * (nu + kHeadCost) + kHeadCost;
+        u0 = max(0, at - first);
+        u1 = max(u0, min(nu, x.end - first));   // none, if this CTA's part ends before them
+    }
+};
+
+__device__ __forceinline__ int first_seq(const Axis &x, int B, int at) {
+    int lo = 0, hi = B;   // the last b with pre[b] <= at; empty ones before it are passed over by seek
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (x.pre[mid] <= at) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int64_t out_at(const QAttnK &k, int b, int head, int row) {
+    const int r = k.row0 + row;
+    return b * k.a.out.ldb + r / k.group * k.a.out.ldt + (int64_t)(head * k.group + r % k.group) * k.a.out.ldh;
+}
+
+// The weights of n slots from slot0 on, from the x that were left at lg: RP / 4
+// threads to a slot, each four columns.  base, c1, inv: per column.
+template <int RP>
+__device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, int64_t slot0, const float *base, const float *c1,
+                                      const float *inv) {
+    constexpr int L = RP / 4;
+    const int c = threadIdx.x % L * 4;
+    float bb[4], cc[4], ii[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bb[i] = base[c + i];
+        cc[i] = c1[c + i];
+        ii[i] = inv[c + i];
+    }
+    // four slots' loads at a time, ahead of the stores (which the compiler may not move loads over); whole warps go
+    // round, so that the shuffles have all their lanes
+    constexpr int U = 4, STEP = kThreads / L;
+    for (int t0 = 0; t0 < n; t0 += U * STEP) {
+        float4 x[U];
+        float old[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = t0 + i * STEP + threadIdx.x / L;
+            x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            old[i] = 0.f;
+            if (t < n) {
+                x[i] = ld_dep(reinterpret_cast<const float4 *>(lg + (int64_t)t * RP + c));
+                if (c == 0 && k.a.decay != 0.f) old[i] = ld_dep(k.a.c.weight + slot0 + t);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = t0 + i * STEP + threadIdx.x / L;
+            float w = exp2_approx((x[i].x - bb[0]) * cc[0]) * ii[0];
+            w = fmaf(exp2_approx((x[i].y - bb[1]) * cc[1]), ii[1], w);
+            w = fmaf(exp2_approx((x[i].z - bb[2]) * cc[2]), ii[2], w);
+            w = fmaf(exp2_approx((x[i].w - bb[3]) * cc[3]), ii[3], w);
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) w += __shfl_xor_sync(kFull, w, o);
+            if (t < n && c == 0) k.a.weight[slot0 + t] = fmaf(k.a.decay, old[i], w);
+        }
+    }
+}
+
+// ------------------------------------------------------------- first kernel
+
+template <int D, int MODE>
+struct Tile {
+    using C = Cfg<D, MODE>;
+    float o[C::G * 4][C::NT][4];     // channels 8 (lane / 4) + 2 t (+ 1) of group g in o[4 g + t], columns 2 (lane % 4) (+ 1)
+    float z[C::G][C::NT][2];         // sums of p (z + 8 s), this lane's slots
+    float l[C::NT][2];               // sums of p, this lane's slots
+    float m[C::NT][2];               // largest x so far
+    float ms[C::NT][2];              // the same, 0 for -inf
+    int e;                           // exponent field of the largest value scale so far; the sums hold p 2^(29 - e)
+    float es;                        // the least scale with a larger one
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n) {
+#pragma unroll
+            for (int t = 0; t < C::G * 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[t][n][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[n][i] = -INFINITY;
+                ms[n][i] = 0.f;
+                l[n][i] = 0.f;
+#pragma unroll
+                for (int g = 0; g < C::G; ++g) z[g][n][i] = 0.f;
+            }
+        }
+        e = 1;
+        es = 1.220703125e-4f;   // 2^-13
+    }
+};
+
+// Starts the copies of one unit of a head, n slots or more, into a stage of the warp's ring.
+template <int D, int MODE>
+__device__ __forceinline__ void fetch(const QAttnK &k, uint32_t stage, int64_t slot0, int n) {
+    using C = Cfg<D, MODE>;
+    constexpr int CH = C::RB / 16, N = C::UT * CH;
+    // a slot's scales go in one piece, or (12 bytes) word by word
+    constexpr int SP = C::G == 3 ? 4 : 4 * C::G, SN = C::UT * C::G * 4 / SP;
+    const int lane = threadIdx.x & 31;
+    const QCacheK &c = k.a.c;
+    const uint8_t *kp = c.k + slot0 * C::RB + lane * 16, *vp = c.v + slot0 * C::RB + lane * 16;
+    const char *ks = reinterpret_cast<const char *>(c.ks + slot0 * C::G) + lane * SP;
+    const char *vs = reinterpret_cast<const char *>(c.vs + slot0 * C::G) + lane * SP;
+    const uint32_t sc = stage + 2 * C::UT * C::RB + lane * SP;
+    if (n >= C::UT) {
+#pragma unroll
+        for (int i = 0; i < N; i += 32) {
+            const int tok = (i + lane) / CH;
+            const uint32_t at = stage + tok * C::RB + (((i + lane) % CH ^ swizzle<D>(tok)) << 4);
+            cp_async<16>(at, kp + i * 16);
+            cp_async<16>(at + C::UT * C::RB, vp + i * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < SN; i += 32)
+            if (SN % 32 == 0 || i + lane < SN) {
+                cp_async<SP>(sc + i * SP, ks + i * SP);
+                cp_async<SP>(sc + C::UT * C::G * 4 + i * SP, vs + i * SP);
+            }
+    } else {
+        // what lies past the head's slots is not read; zeros stand in the ring
+        for (int i = 0; i < N; i += 32) {
+            const int tok = (i + lane) / CH;
+            const uint32_t at = stage + tok * C::RB + (((i + lane) % CH ^ swizzle<D>(tok)) << 4);
+            const bool on = tok < n;
+            cp_async_or0<16>(at, on ? kp + i * 16 : c.k, on);
+            cp_async_or0<16>(at + C::UT * C::RB, on ? vp + i * 16 : c.v, on);
+        }
+        for (int i = 0; i < SN; i += 32)
+            if (i + lane < SN) {
+                const bool on = (i + lane) * SP < n * C::G * 4;
+                cp_async_or0<SP>(sc + i * SP, on ? ks + i * SP : reinterpret_cast<const char *>(c.ks), on);
+                cp_async_or0<SP>(sc + C::UT * C::G * 4 + i * SP, on ? vs + i * SP : reinterpret_cast<const char *>(c.vs), on);
+            }
+    }
+    if (k.a.q_pos && lane < C::UT)
+        cp_async_or0<4>(stage + C::UT * (2 * C::RB + C::G * 8) + lane * 4, lane < n ? c.pos + slot0 + lane : c.pos, lane < n);
+}
+
+// LO: p s has a second fp16 part (always so in PACK4).
+template <int D, int MODE, bool LO>
+__global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAttnK k) {
+    using C = Cfg<D, MODE>;
+    extern __shared__ __align__(16) char smem[];
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * C::ST * C::STAGE);
+    float *red = reinterpret_cast<float *>(qf + C::QF);
+    float *cols = red + C::RED;
+    float *stat = cols + C::RP * C::CS;
+    int *axis_mem = reinterpret_cast<int *>(stat + C::STAT);
+    __shared__ int wsum[32];
+    __shared__ int wexp[kWarps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
+    const QCacheK &c = k.a.c;
+    pdl_wait();
+    pdl_launch_dependents();
+    Axis ax{};
+    ax.build<C::UT>(k, axis_mem, wsum, blockIdx.x == 0);
+    if (ax.begin >= ax.end) return;
+
+    const char *ring = smem + warp * C::ST * C::STAGE;
+    const uint32_t ring_at = smem_addr(ring);
+    const bool by_pos = k.a.q_pos != nullptr, weighing = k.a.weight != nullptr;
+
+    // the fetching side runs ahead of the computing side, on across heads
+    Seg s{};
+    s.template seek<C::UT>(ax, ax.begin, first_seq(ax, c.batch, ax.begin));
+    Seg f = s;
+    int fu = f.u0 + warp, fstage = 0;
+    int fhead = chosen_head(k, f.b, f.h);
+    bool more = true;
+    auto fetch_next = [&]() {
+        while (more && fu >= f.u1) {
+            if (f.next() >= ax.end) {
+                more = false;
+            } else {
+                f.template seek<C::UT>(ax, f.next(), f.b);
+                fu = f.u0 + warp;
+                fhead = chosen_head(k, f.b, f.h);
+            }
+        }
+        if (more) {
+            fetch<D, MODE>(k, ring_at + fstage * C::STAGE, c.slot0(f.b, fhead) + (int64_t)fu * C::UT, ax.len[f.b] - fu * C::UT);
+            fu += kWarps;
+        }
+        fstage = fstage + 1 == C::ST ? 0 : fstage + 1;
+        cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::ST - 1; ++i) fetch_next();
+
+    // what this lane reads of a unit, from the start of a stage
+    const int tok0 = slot_of_row(r), vtok = slot_of_row(2 * j);
+    int kat[C::G], vat[2][C::G];   // of sub-unit 0; 8 rows and sub-units further, only the row differs
+#pragma unroll
+    for (int g = 0; g < C::G; ++g) {
+        kat[g] = tok0 * C::RB + (((2 * g) ^ swizzle<D>(tok0)) << 4) + j * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int tok = vtok ^ (2 * i);
+            vat[i][g] = C::UT * C::RB + tok * C::RB + (((2 * g) ^ swizzle<D>(tok)) << 4) + r * 4;
+        }
+    }
+
+    int stage = 0;
+    Tile<D, MODE> T;
+    for (;;) {
+        if (s.u0 >= s.u1) break;   // only a CTA's last head can have no unit in its part
+        const int head = chosen_head(k, s.b, s.h);
+        // ---- this head's query rows as fragments, a warp to a row
+        {
+            __half *qh = reinterpret_cast<__half *>(qf);
+            for (int row = warp; row < C::RP; row += kWarps) {
+                const bool on = row_on(k, s.b, head, row);
+                const int t = (k.row0 + row) / k.group;
+                const int64_t src = s.b * k.a.q.ldb + t * k.a.q.ldt + (int64_t)(head * k.group + (k.row0 + row) % k.group) * k.a.q.ldh;
+                float q[D / 32];
+                float big = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    q[i] = on ? k.sign * q_load1(k.a.q, src + i * 32 + lane) : 0.f;
+                    big = fmaxf(big, fabsf(q[i]));
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+                // the power of two that takes the largest to [2^14, 2^15); infinities stay what they are
+                const int eb = (int)(__float_as_uint(big) >> 23);
+                const int up = big > 0.f && eb < 255 ? min(141 - eb, 127) : 0;
+                const float f1 = __uint_as_float((uint32_t)(127 + up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    // channel 32 i + lane of the row is nibble `nib` of word `w` of lane jj's two words of its group
+                    const int jj = (i & 1) * 2 + (lane >> 4), w = (i & ~1) + ((lane >> 3) & 1), nib = lane & 7;
+                    q[i] = q[i] * f1 * f2;
+                    const float v = nib & 1 ? q[i] * 0.0625f : q[i];
+                    const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+                    const int col = row & 7, nt = row >> 3;
+                    auto put = [&](int tile, int cc, __half h) {
+                        qh[((tile * (D / 32) + w) * 32 + cc * 4 + jj) * 8 + ((nib & 3) >> 1) * 4 + (nib & 1) * 2 + (nib >> 2)] = h;
+                    };
+                    put(nt * C::PARTS, col, hi);
+                    if (C::PARTS == 1) put(0, col + 4, lo);
+                    else put(nt * 2 + 1, col, lo);
+                }
+                float sum[C::G];
+#pragma unroll
+                for (int g = 0; g < C::G; ++g) sum[g] = warp_sum(q[2 * g] + q[2 * g + 1]);
+                if (lane == 0) {
+                    float *cc = cols + row * C::CS;
+                    // takes the products back; kept where x c1 stays in fp32's range (beyond, one slot takes all as well)
+                    cc[0] = fminf(fmaxf(k.c2 * exp2f((float)(24 - up)), 1.2e-38f), 1.2e30f);
+                    cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + s.b) + t : INT_MAX);
+                    cc[2] = on ? 1.f : 0.f;
+#pragma unroll
+                    for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * 5.9604644775390625e-8f;   // 2^-24, as the products
+                }
+            }
+        }
+        __syncthreads();
+        const bool two = LO && C::PARTS == 2 && k.a.q.dt == CS_F32;
+        float c1[C::NT][2], zq[C::NT][2][C::G];
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float *cc = cols + (MODE == PACK4 ? (j & 1) * 2 + i : n * 8 + j * 2 + i) * C::CS;
+                c1[n][i] = cc[0];
+#pragma unroll
+                for (int g = 0; g < C::G; ++g) zq[n][i][g] = MODE == PACK4 && j >= 2 ? 0.f : cc[3 + g];
+            }
+        T.clear();
+        const int len = ax.len[s.b];
+        float *lg = k.logit + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * k.area;
+
+        for (int u = s.u0 + warp; u < s.u1; u += kWarps) {
+            __syncwarp();
+            fetch_next();
+            cp_async_wait<C::ST - 1>();
+            __syncwarp();
+            const char *ub = ring + stage * C::STAGE, *sb = ub + 2 * C::UT * C::RB;
+            stage = stage + 1 == C::ST ? 0 : stage + 1;
+
+            // ---- x = sum_g s_g (q . (n - 8))_g + (z_g + 8 s_g) (sum q)_g
+            float x[C::SUB][C::NT][4];
+            uint32_t ks[C::SUB][2][C::G];
+#pragma unroll
+            for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) lds_scales<C::G>(sb + (sub * 16 + 8 * i + tok0) * C::G * 4, ks[sub][i]);
+#pragma unroll
+            for (int g = 0; g < C::G; ++g) {
+                float acc[C::SUB][C::NT][4];
+#pragma unroll
+                for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float a0 = -8.f * zq[n][q][g];
+#pragma unroll
+                        for (int sub = 0; sub < C::SUB; ++sub) acc[sub][n][q] = acc[sub][n][2 + q] = a0;
+                    }
+                uint2 kw[C::SUB][2];
+#pragma unroll
+                for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) kw[sub][i] = lds<uint2>(ub + kat[g] + (sub * 16 + 8 * i) * C::RB);
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int n = 0; n < C::NT; ++n) {
+                        const uint4 *qa = qf + (n * C::PARTS * (D / 32) + 2 * g + w) * 32 + lane;
+                        const uint4 b = *qa;
+                        uint4 b2 = make_uint4(0, 0, 0, 0);
+                        if (two) b2 = qa[(D / 32) * 32];
+#pragma unroll
+                        for (int step = 0; step < 2; ++step)
+#pragma unroll
+                            for (int sub = 0; sub < C::SUB; ++sub) {
+                                uint32_t a[4];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    uint32_t v = w ? kw[sub][i].y : kw[sub][i].x;
+                                    if (step) v >>= 8;
+                                    a[i] = v & 0x000f000fu;
+                                    a[i + 2] = v & 0x00f000f0u;
+                                }
+                                mma16816(acc[sub][n], a, step ? b.z : b.x, step ? b.w : b.y);
+                                if (two) mma16816(acc[sub][n], a, step ? b2.z : b2.x, step ? b2.w : b2.y);
+                            }
+                    }
+#pragma unroll
+                for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float sc, zo;
+                        half2x(ks[sub][i][g], sc, zo);
+                        zo = fmaf(8.f, sc, zo);
+#pragma unroll
+                        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const float v = g == 0 ? zo * zq[n][q][g] : fmaf(zo, zq[n][q][g], x[sub][n][2 * i + q]);
+                                x[sub][n][2 * i + q] = fmaf(acc[sub][n][2 * i + q], sc, v);
+                            }
+                    }
+            }
+            if (MODE == PACK4) {
+#pragma unroll
+                for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[sub][0][i] += __shfl_xor_sync(kFull, x[sub][0][i], 2);
+            }
+            uint32_t vs[C::SUB][2][C::G];
+#pragma unroll
+            for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    lds_scales<C::G>(sb + C::UT * C::G * 4 + (sub * 16 + 8 * i + tok0) * C::G * 4, vs[sub][i]);
+            // ---- what is not seen is -inf, and the value scales of slots that no row sees count as 0
+            if (by_pos || (u + 1) * C::UT > len) {
+                const int newest = by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + k.rows - 1) / k.group : 0;
+#pragma unroll
+                for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = sub * 16 + 8 * i + tok0;
+                        int p = 0;
+                        bool there = u * C::UT + tok < len;
+                        if (by_pos) {
+                            p = lds<int>(sb + C::UT * C::G * 8 + tok * 4);
+                            there = there && p >= 0 && p <= newest;
+                        }
+#pragma unroll
+                        for (int g = 0; g < C::G; ++g) vs[sub][i][g] = there ? vs[sub][i][g] : 0u;
+#pragma unroll
+                        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int col = MODE == PACK4 ? (j & 1) * 2 + q : n * 8 + j * 2 + q;
+                                if (!there || p > __float_as_int(cols[col * C::CS + 1])) x[sub][n][2 * i + q] = -INFINITY;
+                            }
+                    }
+            }
+            if (weighing && (MODE != PACK4 || j < 2)) {
+                float *to = lg + ((u - s.u0) * C::UT + tok0) * (int64_t)C::RP + 2 * j;
+#pragma unroll
+                for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < C::NT; ++n)
+                            *reinterpret_cast<float2 *>(to + (sub * 16 + 8 * i) * C::RP + n * 8) =
+                                make_float2(x[sub][n][2 * i], x[sub][n][2 * i + 1]);
+            }
+            // ---- the running maxima
+            float mx[C::NT][2];
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    mx[n][q] = fmaxf(x[0][n][q], x[0][n][2 + q]);
+                    if (C::SUB == 2) mx[n][q] = fmaxf(mx[n][q], fmaxf(x[C::SUB - 1][n][q], x[C::SUB - 1][n][2 + q]));
+                    grow |= mx[n][q] > T.m[n][q];
+                }
+            float vsc[C::SUB][2][C::G], top = 0.f;
+#pragma unroll
+            for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int g = 0; g < C::G; ++g) {
+                        vsc[sub][i][g] = __half2float(__ushort_as_half((unsigned short)(vs[sub][i][g] & 0xffffu)));
+                        top = fmaxf(top, vsc[sub][i][g]);
+                    }
+            grow |= top >= T.es;
+            if (__any_sync(kFull, grow)) {
+                // an fp32 exponent field of 113 (2^-14) is fp16's 1
+                const int e = max(T.e, (int)(__reduce_max_sync(kFull, __float_as_uint(top)) >> 23) - 112);
+                const float de = (float)(T.e - e);
+                T.e = e;
+                T.es = __uint_as_float((uint32_t)(113 + e) << 23);
+#pragma unroll
+                for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float m = fmaxf(mx[n][q], T.m[n][q]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                        // nothing but zeros, or NaN, came before the first finite x
+                        const float al = T.m[n][q] == -INFINITY ? 0.f : exp2_approx(fmaf(T.m[n][q] - m, c1[n][q], de));
+                        T.m[n][q] = m;
+                        T.ms[n][q] = m == -INFINITY ? 0.f : m;
+                        T.l[n][q] *= al;
+#pragma unroll
+                        for (int g = 0; g < C::G; ++g) T.z[g][n][q] *= al;
+#pragma unroll
+                        for (int t = 0; t < C::G * 4; ++t) {
+                            T.o[t][n][q] *= al;
+                            T.o[t][n][2 + q] *= al;
+                        }
+                    }
+            }
+            // ---- p, its sums, and p s as fragments
+            const float up = (float)(29 - T.e);
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int sub = 0; sub < C::SUB; ++sub)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float &v = x[sub][n][2 * i + q];
+                            v = exp2_approx(fmaf(v - T.ms[n][q], c1[n][q], up));
+                            T.l[n][q] += v;
+                        }
+#pragma unroll
+            for (int g = 0; g < C::G; ++g)
+#pragma unroll
+                for (int sub = 0; sub < C::SUB; ++sub) {
+                    uint32_t ph[C::NT][2], pl[C::NT][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float sc = vsc[sub][i][g];
+                        const float zo = fmaf(8.f, sc, __half2float(__ushort_as_half((unsigned short)(vs[sub][i][g] >> 16))));
+#pragma unroll
+                        for (int n = 0; n < C::NT; ++n) {
+                            const float p0 = x[sub][n][2 * i], p1 = x[sub][n][2 * i + 1];
+                            T.z[g][n][0] = fmaf(p0, zo, T.z[g][n][0]);
+                            T.z[g][n][1] = fmaf(p1, zo, T.z[g][n][1]);
+                            const float a0 = p0 * sc, a1 = p1 * sc;
+                            const uint32_t h = pack_h2(a0, a1);
+                            uint32_t lo = 0;
+                            if (LO) {
+                                float h0, h1;
+                                half2x(h, h0, h1);
+                                lo = pack_h2(a0 - h0, a1 - h1);
+                            }
+                            if (MODE == PACK4) {
+                                ph[n][i] = transpose8x8(j >= 2 ? lo : h);
+                            } else {
+                                ph[n][i] = transpose8x8(h);
+                                if (LO) pl[n][i] = transpose8x8(lo);
+                            }
+                        }
+                    }
+                    // the values' words: rows of a product are channels, its columns the slots' order of the keys' rows
+                    uint32_t vw[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vw[i] = lds<uint32_t>(ub + vat[i & 1][g] + (sub * 16 + 8 * (i >> 1)) * C::RB);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t a = __byte_perm(vw[0], vw[1], half ? 0x7632 : 0x5410);
+                        const uint32_t b = __byte_perm(vw[2], vw[3], half ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t av = t ? a >> 8 : a, bv = t ? b >> 8 : b;
+                            uint32_t fr[4];
+                            fr[0] = hsub2u(and_or(av, 0x000f000fu, 0x64006400u), 0x64086408u);
+                            fr[1] = hsub2u(and_or(av, 0x00f000f0u, 0x64006400u), 0x64806480u);
+                            fr[2] = hsub2u(and_or(bv, 0x000f000fu, 0x64006400u), 0x64086408u);
+                            fr[3] = hsub2u(and_or(bv, 0x00f000f0u, 0x64006400u), 0x64806480u);
+#pragma unroll
+                            for (int n = 0; n < C::NT; ++n) {
+                                mma16816(T.o[g * 4 + half * 2 + t][n], fr, ph[n][0], ph[n][1]);
+                                if (MODE != PACK4 && LO) mma16816(T.o[g * 4 + half * 2 + t][n], fr, pl[n][0], pl[n][1]);
+                            }
+                        }
+                    }
+                }
+        }
+
+        // ---- the warps' sums become one
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    T.l[n][q] += __shfl_xor_sync(kFull, T.l[n][q], o);
+#pragma unroll
+                    for (int g = 0; g < C::G; ++g) T.z[g][n][q] += __shfl_xor_sync(kFull, T.z[g][n][q], o);
+                }
+                if (r == 0 && (MODE != PACK4 || j < 2)) {
+                    const int col = n * 8 + 2 * j + q;
+                    stat[warp * C::RP + col] = T.m[n][q];
+                    stat[(kWarps + warp) * C::RP + col] = T.l[n][q];
+                }
+            }
+        if (lane == 0) wexp[warp] = T.e;
+        __syncthreads();
+        float *base = stat + 2 * kWarps * C::RP, *sum = base + C::RP, *cc1 = sum + C::RP;
+        if (tid < C::RP) {
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w * C::RP + tid]);
+            const float at = m == -INFINITY ? 0.f : m, c = cols[tid * C::CS];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2f(fmaf(stat[w * C::RP + tid] - at, c, (float)(wexp[w] - 29)));
+                stat[w * C::RP + tid] = f;
+                l = fmaf(f, stat[(kWarps + w) * C::RP + tid], l);
+            }
+            base[tid] = m;
+            // a row that is not asked for has no sum
+            sum[tid] = cols[tid * C::CS + 2] != 0.f ? l : 0.f;
+            cc1[tid] = c;
+        }
+        const bool whole = s.whole();
+        float *rec = k.part + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * C::REC;
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n) {
+#pragma unroll
+            for (int hf = 0; hf < (MODE == PACK4 ? 1 : 2); ++hf) {   // columns 4 hf .. 4 hf + 3 of the tile
+                float *mine = red + warp * 4 * C::RS;
+#pragma unroll
+                for (int t = 0; t < C::G * 4; ++t) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = T.o[t][n][i];
+                        if (MODE == PACK4) v[i] += __shfl_xor_sync(kFull, v[i], 2);
+                    }
+                    if (j >> 1 == hf) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            *reinterpret_cast<float2 *>(mine + (2 * (j & 1) + q) * C::RS + t * 16 + r * 2) =
+                                make_float2(v[q] + T.z[t / 4][n][q], fmaf(v[2 + q], 0.0625f, T.z[t / 4][n][q]));
+                    }
+                }
+                __syncthreads();
+                for (int i = tid; i < 4 * D; i += kThreads) {
+                    const int col = i / D, e = i % D, row = n * 8 + hf * 4 + col;
+                    float v = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) v = fmaf(stat[w * C::RP + row], red[(w * 4 + col) * C::RS + e], v);
+                    const int ch = (e >> 6) * 64 + ((e >> 1) & 7) * 8 + ((e >> 4) & 3) * 2 + (e & 1);
+                    if (!whole) {
+                        rec[3 * C::RP + row * D + ch] = v;
+                    } else if (row < k.rows) {
+                        const float l = sum[row];
+                        q_store1(k.a.out, out_at(k, s.b, head, row) + ch, l == 0.f ? 0.f : v / l);
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        if (!whole) {
+            if (tid < 3 * C::RP) rec[tid] = base[tid];   // maximum, sum and c1 lie side by side
+        } else if (weighing) {
+            if (tid < C::RP) {
+                base[tid] = base[tid] == -INFINITY ? 0.f : base[tid];
+                sum[tid] = sum[tid] == 0.f ? 0.f : 1.f / sum[tid];
+            }
+            __syncthreads();
+            weigh<C::RP>(k, lg, len, c.slot0(s.b, head), base, cc1, sum);
+        }
+        if (s.next() >= ax.end) break;
+        s.template seek<C::UT>(ax, s.next(), s.b);
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------ second kernel
+
+// Finishes the heads that lie in more than one CTA, and writes what no CTA came
+// by: zero rows (and decayed weights) of empty sequences and heads not chosen.
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads) qattn_join_kernel(QAttnK k) {
+    using C = Cfg<D, MODE>;
+    extern __shared__ __align__(16) int axis_mem[];
+    __shared__ int wsum[32];
+    __shared__ float base[C::RP], inv[C::RP], cc1[C::RP];
+    __shared__ float red[kThreads];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const QCacheK &c = k.a.c;
+    float *factor = reinterpret_cast<float *>(axis_mem + 2 * c.batch + 1);   // [records, RP]
+    pdl_wait();
+    pdl_launch_dependents();
+    Axis ax{};
+    ax.build<C::UT>(k, axis_mem, wsum, false);
+    if (ax.begin < ax.end) {
+        Seg s{};
+        s.template seek<C::UT>(ax, ax.begin, first_seq(ax, c.batch, ax.begin));
+        for (;;) {
+            if (s.u0 < s.u1 && !s.whole()) {
+                const int head = chosen_head(k, s.b, s.h);
+                const int p0 = s.first / ax.per, n = (s.first + s.nu - 1) / ax.per - p0 + 1;
+                auto rec = [&](int p) { return k.part + ((int64_t)(p0 + p) * 2 + (p == 0)) * C::REC; };
+                // a warp to a column: its base and sum over the n records
+                for (int row = warp; row < C::RP; row += kWarps) {
+                    float m = -INFINITY, l = 0.f;
+                    for (int p = lane; p < n; p += 32) m = fmaxf(m, ld_dep(rec(p) + row));
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                    if (m == -INFINITY) m = 0.f;
+                    const float c = ld_dep(rec(0) + 2 * C::RP + row);
+                    for (int p = lane; p < n; p += 32) {
+                        const float f = exp2f((ld_dep(rec(p) + row) - m) * c);
+                        factor[p * C::RP + row] = f;
+                        l = fmaf(f, ld_dep(rec(p) + C::RP + row), l);
+                    }
+                    l = warp_sum(l);
+                    if (lane == 0) {
+                        base[row] = m;
+                        inv[row] = l == 0.f ? 0.f : 1.f / l;
+                        cc1[row] = c;
+                    }
+                }
+                __syncthreads();
+                // this CTA's share of the output values: many records are added up by 8 warps, few by one thread
+                const int mine = blockIdx.x - p0, total = k.rows * D;
+                const int e0 = (int)((int64_t)total * mine / n), e1 = (int)((int64_t)total * (mine + 1) / n);
+                if (n > kWarps) {
+                    for (int i0 = e0; i0 < e1; i0 += 32) {
+                        const int i = i0 + lane;
+                        float v = 0.f;
+                        if (i < e1) {
+#pragma unroll 4
+                            for (int p = warp; p < n; p += kWarps) v = fmaf(factor[p * C::RP + i / D], ld_dep(rec(p) + 3 * C::RP + i), v);
+                        }
+                        red[tid] = v;
+                        __syncthreads();
+                        if (warp == 0 && i < e1) {
+                            v = 0.f;
+#pragma unroll
+                            for (int w = 0; w < kWarps; ++w) v += red[w * 32 + lane];
+                            q_store1(k.a.out, out_at(k, s.b, head, i / D) + i % D, v * inv[i / D]);
+                        }
+                        __syncthreads();
+                    }
+                } else {
+                    for (int i = e0 + tid; i < e1; i += kThreads) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int p = 0; p < kWarps; ++p)
+                            if (p < n) v = fmaf(factor[p * C::RP + i / D], ld_dep(rec(p) + 3 * C::RP + i), v);
+                        q_store1(k.a.out, out_at(k, s.b, head, i / D) + i % D, v * inv[i / D]);
+                    }
+                }
+                if (k.a.weight) {
+                    const int t0 = s.u0 * C::UT, t1 = min(ax.len[s.b], s.u1 * C::UT);
+                    weigh<C::RP>(k, k.logit + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * k.area, t1 - t0, c.slot0(s.b, head) + t0, base,
+                                 cc1, inv);
+                }
+                __syncthreads();
+            }
+            if (s.next() >= ax.end) break;
+            s.template seek<C::UT>(ax, s.next(), s.b);
+        }
+    }
+    for (int64_t i = blockIdx.x; i < (int64_t)c.batch * c.heads; i += gridDim.x) {
+        const int b = (int)(i / c.heads), h = (int)(i % c.heads);
+        if (ax.len[b] > 0 && kv_on(k, b, h)) continue;
+        for (int e = tid; e < k.rows * D; e += kThreads) q_store1(k.a.out, out_at(k, b, h, e / D) + e % D, 0.f);
+        if (k.a.weight)
+            for (int e = tid; e < ax.len[b]; e += kThreads) {
+                const int64_t slot = c.slot0(b, h) + e;
+                k.a.weight[slot] = k.a.decay == 0.f ? 0.f : k.a.decay * ld_dep(c.weight + slot);
+            }
+    }
+}
+
+template <int D, int MODE, bool LO>
+cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
+    using C = Cfg<D, MODE>;
+    const size_t axis = (2 * (size_t)k.a.c.batch + 1) * sizeof(int), smem = C::smem_fixed + axis;
+    static_assert(C::smem_fixed + (2 * kQMaxBatch + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
+    int64_t grid = (int64_t)k.a.sms * (smem <= 112 * 1024 ? C::MINB : 1);
+    if (grid < 1) grid = 1;
+    const int64_t most = (cost + kWarps + kHeadCost - 1) / (kWarps + kHeadCost);
+    k.grid = (int)(most < grid ? most : grid);
+    const size_t join = axis + (size_t)k.grid * C::RP * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && join > 48 * 1024)
+        e = cudaFuncSetAttribute(qattn_join_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join);
+    if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, LO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
+    if (e == cudaSuccess) e = launch(qattn_join_kernel<D, MODE>, dim3(k.grid), dim3(kThreads), join, s, pdl_enabled(), k);
+    return e;
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t run_qattn(QAttnK k, int mode, bool lo, int64_t cost, cudaStream_t s) {
+    if (mode == PACK4) return run<D, PACK4, true>(k, cost, s);
+    if (mode == ONE8) return lo ? run<D, ONE8, true>(k, cost, s) : run<D, ONE8, false>(k, cost, s);
+    return lo ? run<D, TWO8, true>(k, cost, s) : run<D, TWO8, false>(k, cost, s);
+}
+
+#endif  // CS_QATTN_KERNELS
+
+}  // namespace cs

@@ -1,0 +1,5 @@
+// Attention over the 4-bit KV cache, rows of 64 channels.
+#define CS_QATTN_KERNELS
+#include "cs_qattn.cuh"
+
+template cudaError_t cs::run_qattn<64>(cs::QAttnK, int, bool, int64_t, cudaStream_t);

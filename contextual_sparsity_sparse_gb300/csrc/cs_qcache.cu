@@ -327,8 +327,9 @@ cs_status check_cache(const cs_qcache *q, bool codes, const char *who, QCacheK *
             return CS_ERR_UNSUPPORTED;
         }
         CS_CHECK(q->k && q->v && q->k_scale && q->v_scale, "%s: the cache's k, v, k_scale and v_scale are required", who);
-        CS_CHECK(aligned(q->k, 16) && aligned(q->v, 16) && aligned(q->k_scale, 4) && aligned(q->v_scale, 4),
-                 "%s: k and v must be 16-byte aligned, their scales 4-byte", who);
+        const int groups = q->d_head / kQGroup, piece = 4 * (groups & -groups);   // a slot's scales are copied in such pieces
+        CS_CHECK(aligned(q->k, 16) && aligned(q->v, 16) && aligned(q->k_scale, piece) && aligned(q->v_scale, piece),
+                 "%s: k and v must be 16-byte aligned, their scales %d-byte", who, piece);
     }
     CS_CHECK(aligned(q->weight, 4) && aligned(q->pos, 4), "%s: weight and pos must be 4-byte aligned", who);
     *out = QCacheK{q->k, q->v, static_cast<uint32_t *>(q->k_scale), static_cast<uint32_t *>(q->v_scale), q->weight, q->pos,
@@ -460,7 +461,7 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
         set_error("%s: %d query rows per cache head, above %d", who, n_heads / cache->n_heads * n_q, kQMaxRows);
         return CS_ERR_UNSUPPORTED;
     }
-    if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16) >= INT32_MAX) {
+    if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16 + 16) >= INT32_MAX) {
         set_error("%s: batch x n_heads x capacity is too large", who);
         return CS_ERR_UNSUPPORTED;
     }

@@ -416,7 +416,7 @@ cs_status cs_fit_predictor(const cs_ffn_layer *layer, cs_predictor *pred, const 
  *   ld_batch, ld_head: slots from one sequence (head) to the next, the same
  *                     for all six arrays; 0 means dense.
  * d_head is 64, 128, 192 or 256; batch <= 4096; k and v 16-byte aligned, the
- * others 4-byte.  Which slots of a sequence are in use is the caller's to
+ * scales 4-byte (d_head 128: 8, 256: 16), weight and pos 4-byte.  Which slots of a sequence are in use is the caller's to
  * keep: calls take the number per sequence (slots 0 .. length - 1), one
  * number for all heads, and none of them changes it.  One cache object stands
  * for one layer.
