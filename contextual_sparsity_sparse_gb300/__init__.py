@@ -152,7 +152,8 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle itself: building a torch.cuda.Stream around it costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
 
@@ -469,18 +470,26 @@ class QCacheWorkspace:
 
 def _rows(t, batch, heads, d_head, what):
     """cs_head_rows of a [batch, tokens, heads, d_head] tensor with contiguous rows."""
-    if t.dim() != 4 or t.shape[0] != batch or t.shape[2] != heads or t.shape[3] != d_head or t.stride(3) != 1:
+    shape, st = t.shape, t.stride()
+    if len(st) != 4 or shape[0] != batch or shape[2] != heads or shape[3] != d_head or st[3] != 1:
         raise ValueError(f"{what}: expected [{batch}, tokens, {heads}, {d_head}] with contiguous rows, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-    if t.dtype not in _TORCH_DT:
+                         f"{tuple(shape)} with strides {st}")
+    dt = _TORCH_DT.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{what}: dtype {t.dtype} is not fp32, fp16 or bf16")
-    return _Rows(_ptr(t), _dt(t), t.stride(0), t.stride(1), t.stride(2))
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return _Rows(t.data_ptr(), dt, st[0], st[1], st[2])
 
 
 def _ints(t, shape, what):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
-        raise ValueError(f"{what}: expected a contiguous int32 tensor of shape {tuple(shape)}")
-    return _ptr(t)
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous int32 tensor of shape {shape}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
 
 
 def cs_qcache_append(cache: QCache, k, v, ws: QCacheWorkspace, start=None, slots=None, n_new=None, pos=None,

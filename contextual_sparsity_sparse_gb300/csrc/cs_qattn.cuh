@@ -45,7 +45,7 @@ namespace cs {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kHeadCost = 8;
+constexpr int kHeadCost = 24;
 
 struct QAttnK {
     QAttnArgs a;
@@ -250,7 +250,7 @@ struct Axis {
             __syncthreads();
         }
         // a warp without a unit saves nothing, so a CTA takes at least one for each
-        per = max((total + k.grid - 1) / k.grid, kWarps + kHeadCost);
+        per = max((total + k.grid - 1) / k.grid, kWarps);
         begin = (int)min((int64_t)total, (int64_t)blockIdx.x * per);
         end = (int)min((int64_t)total, (int64_t)begin + per);
     }
@@ -307,33 +307,42 @@ __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, i
         cc[i] = c1[c + i];
         ii[i] = inv[c + i];
     }
-    // four slots' loads at a time, ahead of the stores (which the compiler may not move loads over); whole warps go
-    // round, so that the shuffles have all their lanes
-    constexpr int U = 4, STEP = kThreads / L;
-    for (int t0 = 0; t0 < n; t0 += U * STEP) {
+    // whole warps go round, so that the shuffles have all their lanes; the next round's loads are under way while
+    // this one is worked on and stored
+    constexpr int U = 8, STEP = kThreads / L;
+    struct Round {
         float4 x[U];
         float old[U];
+    };
+    auto load = [&](Round &d, int t0) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int t = t0 + i * STEP + threadIdx.x / L;
-            x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            old[i] = 0.f;
+            d.x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            d.old[i] = 0.f;
             if (t < n) {
-                x[i] = ld_dep(reinterpret_cast<const float4 *>(lg + (int64_t)t * RP + c));
-                if (c == 0 && k.a.decay != 0.f) old[i] = ld_dep(k.a.c.weight + slot0 + t);
+                d.x[i] = ld_dep(reinterpret_cast<const float4 *>(lg + (int64_t)t * RP + c));
+                if (c == 0 && k.a.decay != 0.f) d.old[i] = ld_dep(k.a.c.weight + slot0 + t);
             }
         }
+    };
+    Round now, next;
+    load(now, 0);
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += U * STEP) {
+        load(next, t0 + U * STEP);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int t = t0 + i * STEP + threadIdx.x / L;
-            float w = exp2_approx((x[i].x - bb[0]) * cc[0]) * ii[0];
-            w = fmaf(exp2_approx((x[i].y - bb[1]) * cc[1]), ii[1], w);
-            w = fmaf(exp2_approx((x[i].z - bb[2]) * cc[2]), ii[2], w);
-            w = fmaf(exp2_approx((x[i].w - bb[3]) * cc[3]), ii[3], w);
+            float w = exp2_approx((now.x[i].x - bb[0]) * cc[0]) * ii[0];
+            w = fmaf(exp2_approx((now.x[i].y - bb[1]) * cc[1]), ii[1], w);
+            w = fmaf(exp2_approx((now.x[i].z - bb[2]) * cc[2]), ii[2], w);
+            w = fmaf(exp2_approx((now.x[i].w - bb[3]) * cc[3]), ii[3], w);
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) w += __shfl_xor_sync(kFull, w, o);
-            if (t < n && c == 0) k.a.weight[slot0 + t] = fmaf(k.a.decay, old[i], w);
+            if (t < n && c == 0) k.a.weight[slot0 + t] = fmaf(k.a.decay, now.old[i], w);
         }
+        now = next;
     }
 }
 
@@ -430,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
     int *axis_mem = reinterpret_cast<int *>(stat + C::STAT);
     __shared__ int wsum[32];
     __shared__ int wexp[kWarps];
+    __shared__ int64_t outs[C::RP];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
     const QCacheK &c = k.a.c;
@@ -485,23 +495,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
 
     int stage = 0;
     Tile<D, MODE> T;
+    // a warp's query rows (rows warp, warp + 8) of a head, fetched ahead of their use
+    constexpr int QR = (C::RP + kWarps - 1) / kWarps;
+    float qv[QR][D / 32];
+    auto fetch_q = [&](int b, int h) {
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+            const int row = warp + i * kWarps, t = (k.row0 + row) / k.group;
+            const bool on = row < C::RP && row_on(k, b, h, row);
+            const int64_t src = b * k.a.q.ldb + t * k.a.q.ldt + (int64_t)(h * k.group + (k.row0 + row) % k.group) * k.a.q.ldh;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) qv[i][e] = on ? k.sign * q_load1(k.a.q, src + e * 32 + lane) : 0.f;
+        }
+    };
+    if (s.u0 >= s.u1) return;   // only the last head of a CTA's part can have no unit in it
+    int head = chosen_head(k, s.b, s.h);
+    fetch_q(s.b, head);
     for (;;) {
-        if (s.u0 >= s.u1) break;   // only a CTA's last head can have no unit in its part
-        const int head = chosen_head(k, s.b, s.h);
         // ---- this head's query rows as fragments, a warp to a row
         {
             __half *qh = reinterpret_cast<__half *>(qf);
-            for (int row = warp; row < C::RP; row += kWarps) {
-                const bool on = row_on(k, s.b, head, row);
-                const int t = (k.row0 + row) / k.group;
-                const int64_t src = s.b * k.a.q.ldb + t * k.a.q.ldt + (int64_t)(head * k.group + (k.row0 + row) % k.group) * k.a.q.ldh;
-                float q[D / 32];
+#pragma unroll
+            for (int qi = 0; qi < QR; ++qi) {
+                const int row = warp + qi * kWarps;
+                if (row >= C::RP) break;
+                float (&q)[D / 32] = qv[qi];
                 float big = 0.f;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    q[i] = on ? k.sign * q_load1(k.a.q, src + i * 32 + lane) : 0.f;
-                    big = fmaxf(big, fabsf(q[i]));
-                }
+                for (int i = 0; i < D / 32; ++i) big = fmaxf(big, fabsf(q[i]));
 #pragma unroll
                 for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
                 // the power of two that takes the largest to [2^14, 2^15); infinities stay what they are
@@ -528,9 +549,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 for (int g = 0; g < C::G; ++g) sum[g] = warp_sum(q[2 * g] + q[2 * g + 1]);
                 if (lane == 0) {
                     float *cc = cols + row * C::CS;
+                    const bool on = row_on(k, s.b, head, row);
+                    outs[row] = out_at(k, s.b, head, row);
                     // takes the products back; kept where x c1 stays in fp32's range (beyond, one slot takes all as well)
                     cc[0] = fminf(fmaxf(k.c2 * exp2f((float)(24 - up)), 1.2e-38f), 1.2e30f);
-                    cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + s.b) + t : INT_MAX);
+                    cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + row) / k.group : INT_MAX);
                     cc[2] = on ? 1.f : 0.f;
 #pragma unroll
                     for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * 5.9604644775390625e-8f;   // 2^-24, as the products
@@ -791,6 +814,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 }
         }
 
+        // ---- the next head's query rows, on their way while this one is finished
+        Seg nx = s;
+        int nhead = head;
+        bool last = s.next() >= ax.end;
+        if (!last) {
+            nx.template seek<C::UT>(ax, s.next(), s.b);
+            last = nx.u0 >= nx.u1;
+            if (!last) {
+                nhead = chosen_head(k, nx.b, nx.h);
+                fetch_q(nx.b, nhead);
+            }
+        }
         // ---- the warps' sums become one
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
@@ -860,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                         rec[3 * C::RP + row * D + ch] = v;
                     } else if (row < k.rows) {
                         const float l = sum[row];
-                        q_store1(k.a.out, out_at(k, s.b, head, row) + ch, l == 0.f ? 0.f : v / l);
+                        q_store1(k.a.out, outs[row] + ch, l == 0.f ? 0.f : v / l);
                     }
                 }
                 __syncthreads();
@@ -876,8 +911,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
             __syncthreads();
             weigh<C::RP>(k, lg, len, c.slot0(s.b, head), base, cc1, sum);
         }
-        if (s.next() >= ax.end) break;
-        s.template seek<C::UT>(ax, s.next(), s.b);
+        if (last) break;
+        s = nx;
+        head = nhead;
         __syncthreads();
     }
 }
@@ -989,7 +1025,7 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     static_assert(C::smem_fixed + (2 * kQMaxBatch + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
     int64_t grid = (int64_t)k.a.sms * (smem <= 112 * 1024 ? C::MINB : 1);
     if (grid < 1) grid = 1;
-    const int64_t most = (cost + kWarps + kHeadCost - 1) / (kWarps + kHeadCost);
+    const int64_t most = (cost + kWarps - 1) / kWarps;
     k.grid = (int)(most < grid ? most : grid);
     const size_t join = axis + (size_t)k.grid * C::RP * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -4,7 +4,11 @@
 // Contextual sparsity keeps what a token needs and leaves the rest; a serving
 // process does the same with its cache: the slots that gathered the least
 // attention are given up, and the rows that stay are held in 4 bits.
+#include <cooperative_groups.h>
+
 #include "cs_qcache.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace cs {
 
@@ -18,6 +22,7 @@ struct QRowsCall {
     int n;
     const int32_t *start, *slots, *n_new, *pos;
     uint32_t *err;
+    uint32_t mul, shift;     // x / n = (x mul) >> shift for x < 2^31
 };
 
 // The slot of token t of sequence b in head h, or -1; a slot out of range is flagged.
@@ -70,93 +75,171 @@ __device__ __forceinline__ void store8(const QRowsK &r, int64_t i, const float (
     }
 }
 
-// One thread quantises 8 channels; the 8 threads of a group find its bounds
-// together.  Consecutive groups of threads take consecutive channels, then
-// tokens, of one head, so that the codes are written in long runs.  The code is
-// the nearest of (x - offset) / scale in exact arithmetic: an fp32 quotient is
-// off by less than 1e-5 where it matters (below 16), so only one within 1e-4
-// of a half is divided again in 64 bits.
-__global__ void __launch_bounds__(256) qappend_kernel(QRowsCall a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int per = a.c.d / 8, h = blockIdx.y, b = blockIdx.z;
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = item / per;            // (token, k or v)
-    const int c8 = (int)(item % per) * 8;
-    const int t = (int)(row >> 1), isv = (int)(row & 1);
-    int n = a.n;
-    if (a.n_new) {
-        const int m = ld_dep(a.n_new + b);
-        if (m < 0 || m > n) atomicOr(a.err, CS_DEVERR_COUNT);
-        n = m < 0 ? 0 : m < n ? m : n;
-    }
-    const bool on = t < n;
-    const int slot = on ? slot_of(a, b, h, t) : -1;
-    const QRowsK &r = isv ? a.v : a.k;
-    float x[8];
-    float lo = INFINITY, hi = -INFINITY;
-    if (on) {
-        load8(r, b * r.ldb + t * r.ldt + h * r.ldh + c8, x);
+// A row's part that one thread has: 8 channels, D / 8 threads to a row.  A CTA
+// takes kRowSteps x 256 / (D / 8) of a sequence's rows, which are numbered with
+// the token running fastest, then the head, so that codes are written (and read)
+// in long runs.  All of a thread's loads are issued before it works on any.
+constexpr int kRowThreads = 256, kRowSteps = 2;
+template <int D>
+struct RowPart {
+    static constexpr int PER = D / 8, ROWS = kRowThreads / PER;
+    int c8, t[kRowSteps], h[kRowSteps], slot[kRowSteps];   // slot -1: no such row, or none for it
+    bool row[kRowSteps];
+
+    // limit: how many of the n tokens the sequence has
+    __device__ __forceinline__ RowPart(const QRowsCall &a, int b, int limit) {
+        const int r = threadIdx.x / PER;
+        c8 = threadIdx.x % PER * 8;
+        const uint32_t rows = (uint32_t)a.n * a.c.heads;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = x[e] != x[e] ? 0.f : fminf(fmaxf(x[e], -65504.f), 65504.f);
-            lo = fminf(lo, x[e]);
-            hi = fmaxf(hi, x[e]);
+        for (int i = 0; i < kRowSteps; ++i) {
+            const uint32_t x = (blockIdx.x * kRowSteps + i) * (uint32_t)ROWS + r;
+            h[i] = (int)((uint64_t)x * a.mul >> a.shift);
+            t[i] = (int)(x - (uint32_t)h[i] * a.n);
+            row[i] = r < ROWS && x < rows && t[i] < limit;
+            slot[i] = row[i] ? slot_of(a, b, h[i], t[i]) : -1;
         }
     }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-    }
-    if (slot < 0) return;
-    const __half sh = __float2half_rn((hi - lo) * (1.f / 15.f)), zh = __float2half_rn(lo);
-    const float s = __half2float(sh), z = __half2float(zh), inv = 1.f / s;
-    uint32_t codes = 0;
+};
+
+// The 8 codes of channels x whose group lies in [lo, hi], beside the group's
+// scale and offset: the nearest of (x - z) / s in exact arithmetic.  An fp32
+// quotient below 16 is off by less than 1e-5, so only one within 1e-4 of a half
+// is divided again in 64 bits.  The group's threads go through this together.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float lo, float hi, __half &sh, __half &zh) {
+    sh = __float2half_rn((hi - lo) * (1.f / 15.f));
+    zh = __float2half_rn(lo);
+    const float s = __half2float(sh), z = __half2float(zh);
+    if (s == 0.f) return 0;
+    const float inv = 1.f / s;
+    // rounded scales and offsets can take the ends past 0 and 15
+    const bool past = (lo - z) * inv < -0.499f || (hi - z) * inv > 15.499f;
+    float n[8];
+    bool half = past;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        float n = 0.f;
-        if (s > 0.f) {
-            const float q = (x[e] - z) * inv;
-            n = rintf(q);
-            if (fabsf(fabsf(q - n) - 0.5f) < 1e-4f) n = (float)rint(((double)x[e] - (double)z) / (double)s);
-            n = fminf(fmaxf(n, 0.f), 15.f);
-        }
-        codes |= (uint32_t)n << (4 * e);
+        const float q = (x[e] - z) * inv;
+        n[e] = (q + 12582912.f) - 12582912.f;   // 1.5 2^23: rounds to the nearest integer, halves to even
+        half |= fabsf(q - n[e]) > 0.4999f;
     }
-    const int64_t at = a.c.slot0(b, h) + slot;
-    reinterpret_cast<uint32_t *>(isv ? a.c.v : a.c.k)[at * per + c8 / 8] = codes;
-    if (c8 % kQGroup == 0)
-        (isv ? a.c.vs : a.c.ks)[at * (a.c.d / kQGroup) + c8 / kQGroup] =
-            (uint32_t)__half_as_ushort(sh) | (uint32_t)__half_as_ushort(zh) << 16;
-    if (c8 == 0 && isv) {
-        if (a.c.weight) a.c.weight[at] = 0.f;
-        if (a.c.pos) a.c.pos[at] = ld_dep(a.pos + b) + t;
+    if (half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = (x[e] - z) * inv;
+            float r = rintf(q);
+            if (fabsf(fabsf(q - r) - 0.5f) < 1e-4f) r = (float)rint(((double)x[e] - (double)z) / (double)s);
+            n[e] = fminf(fmaxf(r, 0.f), 15.f);
+        }
+    }
+    const float a = fmaf(fmaf(fmaf(n[3], 16.f, n[2]), 16.f, n[1]), 16.f, n[0]);
+    const float b = fmaf(fmaf(fmaf(n[7], 16.f, n[6]), 16.f, n[5]), 16.f, n[4]);
+    return (uint32_t)a | (uint32_t)b << 16;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) qappend_kernel(QRowsCall a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.y;
+    int limit = a.n;
+    if (a.n_new) {
+        limit = ld_dep(a.n_new + b);
+        if (limit < 0 || limit > a.n) {
+            atomicOr(a.err, CS_DEVERR_COUNT);
+            limit = limit < 0 ? 0 : a.n;
+        }
+    }
+    const RowPart<D> p(a, b, limit);
+    float x[kRowSteps][2][8];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][v][e] = 0.f;
+            const QRowsK &r = v ? a.v : a.k;
+            if (p.slot[i] >= 0) load8(r, b * r.ldb + p.t[i] * r.ldt + p.h[i] * r.ldh + p.c8, x[i][v]);
+        }
+    const int first = a.pos ? ld_dep(a.pos + b) : 0;
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const int64_t at = p.slot[i] >= 0 ? a.c.slot0(b, p.h[i]) + p.slot[i] : 0;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            float lo = INFINITY, hi = -INFINITY;
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                odd |= !(fabsf(x[i][v][e]) <= 65504.f);
+                lo = fminf(lo, x[i][v][e]);
+                hi = fmaxf(hi, x[i][v][e]);
+            }
+            if (odd) {
+                lo = INFINITY;
+                hi = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float &y = x[i][v][e];
+                    y = y != y ? 0.f : fminf(fmaxf(y, -65504.f), 65504.f);
+                    lo = fminf(lo, y);
+                    hi = fmaxf(hi, y);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+            }
+            if (p.slot[i] < 0) continue;
+            __half sh, zh;
+            const uint32_t codes = quantise8(x[i][v], lo, hi, sh, zh);
+            reinterpret_cast<uint32_t *>(v ? a.c.v : a.c.k)[at * (D / 8) + p.c8 / 8] = codes;
+            if (p.c8 % kQGroup == 0)
+                (v ? a.c.vs : a.c.ks)[at * (D / kQGroup) + p.c8 / kQGroup] =
+                    (uint32_t)__half_as_ushort(sh) | (uint32_t)__half_as_ushort(zh) << 16;
+        }
+        if (p.slot[i] >= 0 && p.c8 == 0) {
+            if (a.c.weight) a.c.weight[at] = 0.f;
+            if (a.c.pos) a.c.pos[at] = first + p.t[i];
+        }
     }
 }
 
-// The same division of the work the other way round: one thread, 8 channels.
-__global__ void __launch_bounds__(256) qread_kernel(QRowsCall a) {
+template <int D>
+__global__ void __launch_bounds__(kRowThreads) qread_kernel(QRowsCall a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int per = a.c.d / 8, h = blockIdx.y, b = blockIdx.z;
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = item / per;
-    const int c8 = (int)(item % per) * 8;
-    const int t = (int)(row >> 1), isv = (int)(row & 1);
-    if (t >= a.n) return;
-    const int slot = slot_of(a, b, h, t);
-    float x[8] = {};
-    if (slot >= 0) {
-        const int64_t at = a.c.slot0(b, h) + slot;
-        const uint32_t codes = ld_dep(reinterpret_cast<const uint32_t *>(isv ? a.c.v : a.c.k) + at * per + c8 / 8);
-        float s, z;
-        half2x(ld_dep((isv ? a.c.vs : a.c.ks) + at * (a.c.d / kQGroup) + c8 / kQGroup), s, z);
+    const int b = blockIdx.y;
+    const RowPart<D> p(a, b, a.n);
+    uint32_t codes[kRowSteps][2], sz[kRowSteps][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaf(s, (float)(codes >> (4 * e) & 15u), z);
-    }
-    const QRowsK &r = isv ? a.v : a.k;
-    store8(r, b * r.ldb + t * r.ldt + h * r.ldh + c8, x);
+    for (int i = 0; i < kRowSteps; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            codes[i][v] = sz[i][v] = 0;
+            if (p.slot[i] < 0) continue;
+            const int64_t at = a.c.slot0(b, p.h[i]) + p.slot[i];
+            codes[i][v] = ld_dep(reinterpret_cast<const uint32_t *>(v ? a.c.v : a.c.k) + at * (D / 8) + p.c8 / 8);
+            sz[i][v] = ld_dep((v ? a.c.vs : a.c.ks) + at * (D / kQGroup) + p.c8 / kQGroup);
+        }
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            if (!p.row[i]) continue;
+            float s, z, x[8];
+            half2x(sz[i][v], s, z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // nibbles e and e + 4 as fp16 1024 + n, less 1024
+                const uint32_t w = (codes[i][v] >> (4 * e) & 0x000f000fu) | 0x64006400u;
+                const float2 n = __half22float2(__hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1024.f)));
+                x[e] = fmaf(s, n.x, z);
+                x[e + 4] = fmaf(s, n.y, z);
+            }
+            const QRowsK &r = v ? a.v : a.k;
+            store8(r, b * r.ldb + p.t[i] * r.ldt + p.h[i] * r.ldh + p.c8, x);
+        }
 }
 
 // --------------------------------------------------------------- evict, trim
@@ -172,7 +255,7 @@ struct QEvictCall {
     uint32_t *err;
 };
 
-constexpr int kEvictThreads = 512;
+constexpr int kLongThreads = 512;
 
 // A total order on weights as unsigned integers: NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -182,11 +265,22 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One CTA per (sequence, head).  The slots to give up are the first e of the
+// A slot's class by its token's position: 0 empty, 1 plain, 2 protected.
+struct SlotClass {
+    int sinks;
+    int64_t from;
+
+    __device__ __forceinline__ SlotClass(const QEvictCall &a, int b)
+        : sinks(a.sinks), from(a.recent > 0 ? (int64_t)ld_dep(a.next_pos + b) - a.recent : INT64_MAX) {}
+    __device__ __forceinline__ int operator()(int p) const { return p < 0 ? 0 : p < sinks || p >= from ? 2 : 1; }
+};
+
+// Rows too long for the registers of a cluster: one CTA per (sequence, head) goes
+// over the weights once per histogram.  The slots to give up are the first e of the
 // order (class, weight, slot), class 0 empty, 1 plain, 2 protected: the class
 // and then the weight's four bytes are found one histogram at a time, and a
 // last pass in slot order writes the chosen slots (or, for a trim, the others).
-__global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
+__global__ void __launch_bounds__(kLongThreads) qevict_long_kernel(QEvictCall a) {
     pdl_wait();
     pdl_launch_dependents();
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
@@ -202,27 +296,22 @@ __global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
     const int e = a.keep >= 0 ? max(0, used - a.keep) : max(0, a.n - (cap - used));
     const int64_t slot0 = a.c.slot0(b, h);
     const float *w = a.c.weight + slot0;
-    const int32_t *pos = a.c.pos ? a.c.pos + slot0 : nullptr;
-    const int64_t from = a.recent > 0 ? (int64_t)ld_dep(a.next_pos + b) - a.recent : INT64_MAX;
-    auto cls = [&](int i) {
-        if (!pos) return 1;
-        const int p = ld_dep(pos + i);
-        return p < 0 ? 0 : p < a.sinks || p >= from ? 2 : 1;
-    };
+    const SlotClass sc(a, b);
+    auto cls = [&](int i) { return a.c.pos ? sc(ld_dep(a.c.pos + slot0 + i)) : 1; };
     int want = e;            // still to take at or above the prefix found so far
     int c = -1;
     uint32_t key = 0;
     if (e > 0) {
-        for (int i = tid; i < 4; i += kEvictThreads) hist[i] = 0;
+        for (int i = tid; i < 4; i += kLongThreads) hist[i] = 0;
         __syncthreads();
-        for (int i = tid; i < used; i += kEvictThreads) atomicAdd(&hist[cls(i)], 1);
+        for (int i = tid; i < used; i += kLongThreads) atomicAdd(&hist[cls(i)], 1);
         __syncthreads();
         for (c = 0; c < 2 && want > hist[c]; ++c) want -= hist[c];
         for (int shift = 24; shift >= 0; shift -= 8) {
             __syncthreads();
-            for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
+            for (int i = tid; i < 256; i += kLongThreads) hist[i] = 0;
             __syncthreads();
-            for (int i = tid; i < used; i += kEvictThreads) {
+            for (int i = tid; i < used; i += kLongThreads) {
                 const uint32_t u = weight_key(ld_dep(w + i));
                 if (cls(i) == c && (shift == 24 || u >> (shift + 8) == key >> (shift + 8)))
                     atomicAdd(&hist[u >> shift & 255u], 1);
@@ -245,7 +334,7 @@ __global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
     const int room = a.keep >= 0 ? a.keep : a.n;
     int32_t *out = a.out + ((int64_t)b * a.c.heads + h) * room;
     int equal = 0, put = 0;
-    for (int i0 = 0; i0 < used; i0 += kEvictThreads) {
+    for (int i0 = 0; i0 < used; i0 += kLongThreads) {
         const int i = i0 + tid;
         bool lower = false, same = false;
         if (e > 0 && i < used) {
@@ -264,31 +353,285 @@ __global__ void __launch_bounds__(kEvictThreads) qevict_kernel(QEvictCall a) {
         if (take && at < room) out[at] = i;
     }
     if (a.keep < 0)
-        for (int i = e + tid; i < a.n; i += kEvictThreads) out[i] = used + i - e;
+        for (int i = e + tid; i < a.n; i += kLongThreads) out[i] = used + i - e;
 }
 
-// One thread copies 4 bytes of a slot: words 0 .. d / 4 - 1 are its codes, the
-// next 2 d / 64 its scales, then its weight and position.
+// A cluster of C CTAs of T threads per (sequence, head), K slots to a thread, all
+// in registers: a warp has 32 K consecutive slots.  The slots to give up are the
+// first e of the order (class, weight, slot): three histograms find the last
+// one's class and key (2 + 10, 11 and 11 bits), each CTA its own slots' counts,
+// which the cluster adds up a slice per CTA; then ballots number the chosen
+// slots, and the equal ones, in slot order.
+constexpr int kBins = 3 * 1024;
+
+template <int T>
+struct EvictShared {
+    int hist[kBins];
+    int red[kBins];
+    int wsum[32];
+    int tot[8];          // the slices' totals
+    int pick[2];         // the bin, and what comes before it
+    int lower[T / 32], same[T / 32];
+    int2 cta[8];         // the CTAs' chosen and equal slots
+    int used;
+};
+
+// The bin of the cluster's `want`-th value (from 1) among nb bins, and how many
+// lie in lower bins.
+template <int T>
+__device__ int2 find_bin(EvictShared<T> &sh, cg::cluster_group &cl, int nb, int want) {
+    const int C = (int)cl.num_blocks(), me = (int)cl.block_rank(), tid = threadIdx.x;
+    const int *counts = sh.hist;
+    int slice = nb, lo = 0, before = 0, owner = 0;
+    if (C > 1) {
+        slice = nb / C;
+        lo = me * slice;
+        cl.sync();
+        int sum = 0;
+        for (int i = tid; i < slice; i += T) {
+            int v = 0;
+            for (int r = 0; r < C; ++r) v += cl.map_shared_rank(sh.hist, r)[lo + i];
+            sh.red[i] = v;
+            sum += v;
+        }
+        int total;
+        block_excl_scan(sum, sh.wsum, &total);
+        if (tid < C) cl.map_shared_rank(sh.tot, tid)[me] = total;
+        cl.sync();
+        while (owner < C - 1 && want > before + sh.tot[owner]) before += sh.tot[owner++];
+        counts = sh.red;
+    } else {
+        __syncthreads();
+    }
+    if (me == owner) {
+        const int each = (slice + T - 1) / T;
+        const int i0 = min(slice, tid * each), i1 = min(slice, i0 + each);
+        int sum = 0;
+        for (int i = i0; i < i1; ++i) sum += counts[i];
+        int total;
+        int at = before + block_excl_scan(sum, sh.wsum, &total);
+        if (want > at && want <= at + sum)
+            for (int i = i0; i < i1; ++i) {
+                if (want <= at + counts[i]) {
+                    for (int r = 0; r < C; ++r) {
+                        int *to = C > 1 ? cl.map_shared_rank(sh.pick, r) : sh.pick;
+                        to[0] = lo + i;
+                        to[1] = at;
+                    }
+                    break;
+                }
+                at += counts[i];
+            }
+    }
+    if (C > 1) cl.sync();
+    else __syncthreads();
+    return make_int2(sh.pick[0], sh.pick[1]);
+}
+
+template <int T, int K>
+__global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
+    __shared__ EvictShared<T> sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
+    const int row = blockIdx.x / C, h = row % a.c.heads, b = row / a.c.heads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kBins; i += T) sh.hist[i] = 0;
+    if (C > 1) cl.sync();   // the others' shared memory is there
+    pdl_wait();
+    pdl_launch_dependents();
+    const int cap = a.keep >= 0 ? a.c.cap : a.limit;
+    // one thread reads it for the cluster: the barriers below need one answer, whatever else writes there meanwhile
+    if (me == 0 && tid == 0) {
+        const int n = q_length(a.length, b, cap, a.err);
+        for (int r = 0; r < C; ++r) *cl.map_shared_rank(&sh.used, r) = n;
+    }
+    const int64_t slot0 = a.c.slot0(b, h);
+    const SlotClass sc(a, b);
+    // slots past the length are loaded, too (they are the cache's), while it is on its way
+    const int first = (me * (T / 32) + warp) * 32 * K + lane;
+    uint32_t key[K], cls = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int slot = first + 32 * i;
+        key[i] = slot < cap ? __float_as_uint(ld_dep(a.c.weight + slot0 + slot)) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int slot = first + 32 * i;
+        const int c = a.c.pos ? sc(slot < cap ? ld_dep(a.c.pos + slot0 + slot) : 0) : 1;
+        cls |= (uint32_t)c << (2 * i);
+    }
+    if (C > 1) cl.sync();
+    else __syncthreads();
+    const int used = sh.used;
+    const int e = a.keep >= 0 ? max(0, used - a.keep) : max(0, a.n - (cap - used));
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        key[i] = weight_key(__uint_as_float(key[i]));
+        if (first + 32 * i >= used) cls |= 3u << (2 * i);
+    }
+    int want = e;
+    uint32_t pc = 0, pk = 0;   // the last one's class and key
+    if (e > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const uint32_t c = cls >> (2 * i) & 3u;
+            if (c < 3) atomicAdd(&sh.hist[c * 1024 + (key[i] >> 22)], 1);
+        }
+        int2 p = find_bin<T>(sh, cl, kBins, want);
+        pc = (uint32_t)p.x >> 10;
+        pk = (uint32_t)(p.x & 1023) << 22;
+        want -= p.y;
+#pragma unroll 1
+        for (int shift = 11; shift >= 0; shift -= 11) {
+            for (int i = tid; i < 2048; i += T) sh.hist[i] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if ((cls >> (2 * i) & 3u) == pc && (key[i] ^ pk) >> (shift + 11) == 0) atomicAdd(&sh.hist[key[i] >> shift & 2047u], 1);
+            p = find_bin<T>(sh, cl, 2048, want);
+            pk |= (uint32_t)p.x << shift;
+            want -= p.y;
+        }
+    }
+    // `want` of the slots equal to (pc, pk) go, the first ones
+    uint32_t lower = 0, same = 0;
+    int nl = 0, ns = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const uint32_t c = cls >> (2 * i) & 3u;
+        const bool in = e > 0 && c < 3;
+        const bool lo = in && (c < pc || (c == pc && key[i] < pk)), eq = in && c == pc && key[i] == pk;
+        lower |= (uint32_t)lo << i;
+        same |= (uint32_t)eq << i;
+        nl += __popc(__ballot_sync(kFull, lo));
+        ns += __popc(__ballot_sync(kFull, eq));
+    }
+    if (lane == 0) {
+        sh.lower[warp] = nl;
+        sh.same[warp] = ns;
+    }
+    __syncthreads();
+    int bl = 0, bs = 0, tl = 0, ts = 0;
+    for (int w = 0; w < T / 32; ++w) {
+        if (w < warp) {
+            bl += sh.lower[w];
+            bs += sh.same[w];
+        }
+        tl += sh.lower[w];
+        ts += sh.same[w];
+    }
+    if (C > 1) {
+        if (tid < C) cl.map_shared_rank(sh.cta, tid)[me] = make_int2(tl, ts);
+        cl.sync();
+        for (int r = 0; r < me; ++r) {
+            bl += sh.cta[r].x;
+            bs += sh.cta[r].y;
+        }
+    }
+    // weights that another kernel changes meanwhile must not lead past the list
+    const int room = a.keep >= 0 ? a.keep : a.n;
+    int32_t *out = a.out + ((int64_t)b * a.c.heads + h) * room;
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        const int slot = first + 32 * i;
+        const uint32_t wl = __ballot_sync(kFull, lower >> i & 1u), we = __ballot_sync(kFull, same >> i & 1u);
+        const int eqs = bs + __popc(we & below);
+        const bool gone = (lower >> i & 1u) || ((same >> i & 1u) && eqs < want);
+        const int at = bl + __popc(wl & below) + min(eqs, want);   // slots before this one that go
+        bl += __popc(wl);
+        bs += __popc(we);
+        if (a.keep >= 0) {
+            if (slot < used && !gone && slot - at < room) out[slot - at] = slot;
+        } else if (gone && at < room) {
+            out[at] = slot;
+        }
+    }
+    if (a.keep < 0 && me == 0)
+        for (int i = e + tid; i < a.n; i += T) out[i] = used + i - e;
+}
+
+// Copies the slots that stay.  A CTA takes kTrimSlots of a head's: their codes in
+// 16-byte pieces, then their scales, weights and positions word by word.
+constexpr int kTrimSlots = 64;
+template <int D>
 __global__ void __launch_bounds__(256) qtrim_kernel(QEvictCall a, QCacheK dst) {
     pdl_wait();
     pdl_launch_dependents();
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int cw = a.c.d / 8, sw = a.c.d / kQGroup, words = 2 * (cw + sw) + 2;
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int t = (int)(item / words);
-    int w = (int)(item % words);
-    if (t >= min(a.keep, q_length(a.length, b, a.c.cap, nullptr))) return;
-    const int slot = ld_dep(a.out + ((int64_t)b * a.c.heads + h) * a.keep + t);
-    if (slot < 0 || slot >= a.c.cap) return;
-    const int64_t from = a.c.slot0(b, h) + slot;
-    const int64_t to = dst.slot0(b, h) + t;
-    auto word = [](void *p, int64_t slot, int per, int i) { return reinterpret_cast<uint32_t *>(p) + slot * per + i; };
-    if (w < cw) { *word(dst.k, to, cw, w) = ld_dep(word(a.c.k, from, cw, w)); return; }
-    if ((w -= cw) < cw) { *word(dst.v, to, cw, w) = ld_dep(word(a.c.v, from, cw, w)); return; }
-    if ((w -= cw) < sw) { *word(dst.ks, to, sw, w) = ld_dep(word(a.c.ks, from, sw, w)); return; }
-    if ((w -= sw) < sw) { *word(dst.vs, to, sw, w) = ld_dep(word(a.c.vs, from, sw, w)); return; }
-    if ((w -= sw) == 0) dst.weight[to] = ld_dep(a.c.weight + from);
-    else if (dst.pos) dst.pos[to] = a.c.pos ? ld_dep(a.c.pos + from) : -1;
+    const int h = blockIdx.y, b = blockIdx.z, t0 = blockIdx.x * kTrimSlots;
+    __shared__ int slots[kTrimSlots];
+    const int n = min(kTrimSlots, min(a.keep, q_length(a.length, b, a.c.cap, nullptr)) - t0);
+    if (threadIdx.x < kTrimSlots) {
+        int s = -1;
+        if ((int)threadIdx.x < n) s = ld_dep(a.out + ((int64_t)b * a.c.heads + h) * a.keep + t0 + threadIdx.x);
+        slots[threadIdx.x] = s < a.c.cap ? s : -1;
+    }
+    __syncthreads();
+    const int64_t from = a.c.slot0(b, h), to = dst.slot0(b, h) + t0;
+    constexpr int CH = D / 32, STEPS = kTrimSlots * CH / 256 > 0 ? (kTrimSlots * CH + 255) / 256 : 1;
+    uint4 v[2][STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int x = i * 256 + threadIdx.x, t = x / CH, ch = x % CH;
+        const int s = t < kTrimSlots ? slots[t] : -1;
+        if (s < 0) continue;
+        v[0][i] = ld_dep(reinterpret_cast<const uint4 *>(a.c.k) + (from + s) * CH + ch);
+        v[1][i] = ld_dep(reinterpret_cast<const uint4 *>(a.c.v) + (from + s) * CH + ch);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int x = i * 256 + threadIdx.x, t = x / CH, ch = x % CH;
+        if (t >= kTrimSlots || slots[t] < 0) continue;
+        reinterpret_cast<uint4 *>(dst.k)[(to + t) * CH + ch] = v[0][i];
+        reinterpret_cast<uint4 *>(dst.v)[(to + t) * CH + ch] = v[1][i];
+    }
+    constexpr int G = D / kQGroup;
+    for (int x = threadIdx.x; x < kTrimSlots * G; x += 256) {
+        const int t = x / G, g = x % G, s = slots[t];
+        if (s < 0) continue;
+        const uint32_t ks = ld_dep(a.c.ks + (from + s) * G + g), vs = ld_dep(a.c.vs + (from + s) * G + g);
+        dst.ks[(to + t) * G + g] = ks;
+        dst.vs[(to + t) * G + g] = vs;
+    }
+    if (threadIdx.x < kTrimSlots && slots[threadIdx.x] >= 0) {
+        const int s = slots[threadIdx.x];
+        const float w = ld_dep(a.c.weight + from + s);
+        const int p = a.c.pos ? ld_dep(a.c.pos + from + s) : 0;
+        dst.weight[to + threadIdx.x] = w;
+        if (a.c.pos) dst.pos[to + threadIdx.x] = p;
+    }
+}
+
+// Launches the choice of slots for rows of up to `cap` slots.
+template <int T, int K>
+cudaError_t launch_evict(const QEvictCall &a, int ctas, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.c.heads * a.c.batch * ctas));
+    cfg.blockDim = dim3(T);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, qevict_kernel<T, K>, a);
+}
+
+cudaError_t choose_slots(const QEvictCall &a, cudaStream_t s) {
+    const int cap = a.keep >= 0 ? a.c.cap : a.limit, sms = device_sm_count();
+    const int64_t rows = (int64_t)a.c.heads * a.c.batch;
+    // few rows: several CTAs each, as long as the GPU has room and a CTA has at least 2048 slots
+    int ctas = 1;
+    while (ctas < 8 && ((rows * ctas * 2 <= 2 * sms && cap / (2 * ctas) >= 2048) || cap > 16384 * ctas)) ctas *= 2;
+    const int each = (cap + ctas - 1) / ctas;
+    if (each <= 2048) return launch_evict<512, 4>(a, ctas, s);
+    if (each <= 8192) return launch_evict<512, 16>(a, ctas, s);
+    if (each <= 16384) return launch_evict<1024, 16>(a, ctas, s);
+    return launch(qevict_long_kernel, dim3(a.c.heads, a.c.batch), dim3(kLongThreads), 0, s, pdl_enabled(), a);
 }
 
 // ------------------------------------------------------------------- host side
@@ -374,9 +717,20 @@ cs_status check_evict(const cs_qcache *q, const int32_t *length, const int32_t *
 
 size_t trim_scratch(int batch, int heads, int keep) { return align256((size_t)batch * heads * keep * sizeof(int32_t)); }
 
-// append and read: 256 threads take 8 channels each of the key and value rows of one head
-dim3 rows_grid(const QCacheK &c, int n) {
-    return dim3((unsigned)(((int64_t)n * 2 * (c.d / 8) + 255) / 256), c.heads, c.batch);
+// Launches append's or read's kernel of the cache's d_head.
+template <typename F>
+cudaError_t by_d(int d, F f) {
+    switch (d) {
+    case 64: return f(std::integral_constant<int, 64>());
+    case 128: return f(std::integral_constant<int, 128>());
+    case 192: return f(std::integral_constant<int, 192>());
+    default: return f(std::integral_constant<int, 256>());
+    }
+}
+template <int D>
+dim3 rows_grid(const QRowsCall &a) {
+    const int64_t rows = (int64_t)a.n * a.c.heads, each = RowPart<D>::ROWS * kRowSteps;
+    return dim3((unsigned)((rows + each - 1) / each), a.c.batch);
 }
 
 cs_status rows_call(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n, const int32_t *start,
@@ -389,6 +743,14 @@ cs_status rows_call(const cs_qcache *cache, const cs_head_rows *k, const cs_head
     CS_CHECK(n >= 0 && n <= kMaxTokens, "%s: n=%d outside [0, %d]", who, n, kMaxTokens);
     CS_CHECK((start != nullptr) != (slots != nullptr), "%s: exactly one of start and slots is required", who);
     CS_CHECK(aligned(start, 4) && aligned(slots, 4), "%s: start and slots must be 4-byte aligned", who);
+    if ((int64_t)n * cache->n_heads >= (int64_t(1) << 31) - 4096) {
+        set_error("%s: n x n_heads = %lld is too large", who, (long long)n * cache->n_heads);
+        return CS_ERR_UNSUPPORTED;
+    }
+    // with 2^s >= n, 2^(31 + s) / n rounded up is off by at most 1, which x < 2^31 times 2^-(31 + s) keeps below 1 / n
+    a->shift = 31;
+    while ((int64_t(1) << (a->shift - 31)) < n) ++a->shift;
+    a->mul = n > 0 ? (uint32_t)((uint64_t(1) << a->shift) / n + (n > 1)) : 0;
     a->n = n;
     a->start = start;
     a->slots = slots;
@@ -427,7 +789,9 @@ cs_status cs_qcache_append(const cs_qcache *cache, const cs_head_rows *k, const 
     a.n_new = n_new;
     a.pos = pos;
     if (n == 0) return CS_OK;
-    const cudaError_t e = launch(qappend_kernel, rows_grid(a.c, n), dim3(256), 0, (cudaStream_t)stream, pdl_enabled(), a);
+    const cudaError_t e = by_d(a.c.d, [&](auto d) {
+        return launch(qappend_kernel<d()>, rows_grid<d()>(a), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
+    });
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
@@ -438,7 +802,9 @@ cs_status cs_qcache_read(const cs_qcache *cache, const cs_head_rows *k, const cs
     const cs_status st = rows_call(cache, k, v, n, start, slots, ws, ws_bytes, who, &a);
     if (st != CS_OK) return st;
     if (n == 0) return CS_OK;
-    const cudaError_t e = launch(qread_kernel, rows_grid(a.c, n), dim3(256), 0, (cudaStream_t)stream, pdl_enabled(), a);
+    const cudaError_t e = by_d(a.c.d, [&](auto d) {
+        return launch(qread_kernel<d()>, rows_grid<d()>(a), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
+    });
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
@@ -510,8 +876,7 @@ cs_status cs_qcache_evict(const cs_qcache *cache, const int32_t *length, int lim
     a.recent = recent;
     a.out = slots;
     a.err = static_cast<uint32_t *>(ws);
-    const cudaError_t e = launch(qevict_kernel, dim3(a.c.heads, a.c.batch), dim3(kEvictThreads), 0, (cudaStream_t)stream,
-                                 pdl_enabled(), a);
+    const cudaError_t e = choose_slots(a, (cudaStream_t)stream);
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
@@ -543,11 +908,12 @@ cs_status cs_qcache_trim(const cs_qcache *src, const int32_t *length, int keep, 
     a.recent = recent;
     a.out = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kControlBytes);
     a.err = static_cast<uint32_t *>(ws);
-    cudaError_t e = launch(qevict_kernel, dim3(a.c.heads, a.c.batch), dim3(kEvictThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
-    const int words = 2 * (a.c.d / 8 + a.c.d / kQGroup) + 2;
+    cudaError_t e = choose_slots(a, (cudaStream_t)stream);
     if (e == cudaSuccess)
-        e = launch(qtrim_kernel, dim3((unsigned)(((int64_t)a.keep * words + 255) / 256), a.c.heads, a.c.batch), dim3(256), 0,
-                   (cudaStream_t)stream, pdl_enabled(), a, to);
+        e = by_d(a.c.d, [&](auto d) {
+            return launch(qtrim_kernel<d()>, dim3((a.keep + kTrimSlots - 1) / kTrimSlots, a.c.heads, a.c.batch), dim3(256), 0,
+                          (cudaStream_t)stream, pdl_enabled(), a, to);
+        });
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
