@@ -34,21 +34,34 @@ __device__ __forceinline__ int slot_of(const QRowsCall &a, int b, int h, int t) 
     return -1;
 }
 
-__device__ __forceinline__ void load8(const QRowsK &r, int64_t i, float (&x)[8]) {
-    if (!r.vec) {
+// 8 elements of a row as they lie in memory.
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+
+    __device__ __forceinline__ void load(const QRowsK &r, int64_t i) {
+        const T *p = reinterpret_cast<const T *>(r.p) + i;
+        if (r.vec) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = q_load1(r, i + e);
-    } else if (r.dt == CS_F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(r.p) + i);
-        const float4 lo = p[0], hi = p[1];
-        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(r.p + 2 * i);
-        if (r.dt == CS_F16) unpack16(v, x, static_cast<const __half *>(nullptr));
-        else unpack16(v, x, static_cast<const __nv_bfloat16 *>(nullptr));
+            for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = ld_dep(reinterpret_cast<const uint4 *>(p) + e);
+        } else {
+            T x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = ld_dep(p + e);
+            memcpy(v, x, sizeof x);
+        }
     }
-}
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        constexpr int N = Vec<T>::N;
+#pragma unroll
+        for (int e = 0; e < 8 / N; ++e) {
+            float y[N];
+            unpack<T>(v[e], y);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[e * N + i] = y[i];
+        }
+    }
+};
 
 __device__ __forceinline__ void store8(const QRowsK &r, int64_t i, const float (&x)[8]) {
     if (!r.vec) {
@@ -75,68 +88,97 @@ __device__ __forceinline__ void store8(const QRowsK &r, int64_t i, const float (
     }
 }
 
-// A row's part that one thread has: 8 channels, D / 8 threads to a row.  A CTA
-// takes kRowSteps x 256 / (D / 8) of a sequence's rows, which are numbered with
-// the token running fastest, then the head, so that codes are written (and read)
-// in long runs.  All of a thread's loads are issued before it works on any.
-constexpr int kRowThreads = 256, kRowSteps = 2;
-template <int D>
+// The part of a sequence's rows that one thread has: N channels of a key row and
+// of its value row, D / N threads to a row.  Rows are numbered with the token
+// running fastest, then the head, so that codes are written (and read) in long runs.
+constexpr int kRowThreads = 256, kPart = 16;
+template <int D, int N>
 struct RowPart {
-    static constexpr int PER = D / 8, ROWS = kRowThreads / PER;
-    int c8, t[kRowSteps], h[kRowSteps], slot[kRowSteps];   // slot -1: no such row, or none for it
-    bool row[kRowSteps];
+    static constexpr int PER = D / N, ROWS = kRowThreads / PER;   // rows of a CTA
+    int c, t, h;   // first channel
+    bool row;      // there is such a row
 
-    // limit: how many of the n tokens the sequence has
-    __device__ __forceinline__ RowPart(const QRowsCall &a, int b, int limit) {
+    // limit: how many of the n tokens the sequence has; step: rows of how many CTAs come before
+    __device__ __forceinline__ RowPart(const QRowsCall &a, int limit, uint32_t step) {
         const int r = threadIdx.x / PER;
-        c8 = threadIdx.x % PER * 8;
-        const uint32_t rows = (uint32_t)a.n * a.c.heads;
-#pragma unroll
-        for (int i = 0; i < kRowSteps; ++i) {
-            const uint32_t x = (blockIdx.x * kRowSteps + i) * (uint32_t)ROWS + r;
-            h[i] = (int)((uint64_t)x * a.mul >> a.shift);
-            t[i] = (int)(x - (uint32_t)h[i] * a.n);
-            row[i] = r < ROWS && x < rows && t[i] < limit;
-            slot[i] = row[i] ? slot_of(a, b, h[i], t[i]) : -1;
-        }
+        c = threadIdx.x % PER * N;
+        const uint32_t x = step * (uint32_t)ROWS + r;
+        h = (int)((uint64_t)x * a.mul >> a.shift);
+        t = (int)(x - (uint32_t)h * a.n);
+        row = r < ROWS && x < (uint32_t)a.n * a.c.heads && t < limit;
     }
 };
 
-// The 8 codes of channels x whose group lies in [lo, hi], beside the group's
-// scale and offset: the nearest of (x - z) / s in exact arithmetic.  An fp32
-// quotient below 16 is off by less than 1e-5, so only one within 1e-4 of a half
-// is divided again in 64 bits.  The group's threads go through this together.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float lo, float hi, __half &sh, __half &zh) {
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// The least and the largest of N values; NaN if one of them is.
+template <int N>
+__device__ __forceinline__ void bounds(const float (&x)[N], float &lo, float &hi) {
+    lo = hi = x[0];
+#pragma unroll
+    for (int e = 1; e < N; e += 2) {
+        lo = min_nan(lo, x[e], x[e + 1 < N ? e + 1 : e]);
+        hi = max_nan(hi, x[e], x[e + 1 < N ? e + 1 : e]);
+    }
+}
+
+// The codes of channels x whose group lies in [lo, hi], beside the group's scale
+// and offset: the nearest of (x - z) / s in exact arithmetic.  An fp32 quotient
+// below 16 is off by three roundings, 3 x 2^-24 x 16 < 3e-6; one within 8e-6 of a
+// half m + 1/2 is decided by the sign of x - z - (m + 1/2) s.  There x - z is
+// taken as an unevaluated sum of two fp32 numbers, (m + 1/2) s has 17 bits, and
+// the difference of the two near numbers is exact.  (In 64 bits these divisions
+// took a quarter of the kernel's time: bf16 rows often hit a half exactly.)
+__device__ __forceinline__ uint2 quantise(const float (&x)[kPart], float lo, float hi, __half &sh, __half &zh) {
     sh = __float2half_rn((hi - lo) * (1.f / 15.f));
     zh = __float2half_rn(lo);
     const float s = __half2float(sh), z = __half2float(zh);
-    if (s == 0.f) return 0;
+    if (s == 0.f) return make_uint2(0, 0);
     const float inv = 1.f / s;
-    // rounded scales and offsets can take the ends past 0 and 15
-    const bool past = (lo - z) * inv < -0.499f || (hi - z) * inv > 15.499f;
-    float n[8];
-    bool half = past;
+    float n[kPart], far = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float q = (x[e] - z) * inv;
-        n[e] = (q + 12582912.f) - 12582912.f;   // 1.5 2^23: rounds to the nearest integer, halves to even
-        half |= fabsf(q - n[e]) > 0.4999f;
+    for (int e = 0; e < kPart; e += 2) {
+        float d[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float q = (x[e + i] - z) * inv;
+            n[e + i] = (q + 12582912.f) - 12582912.f;   // 1.5 2^23: rounds to the nearest integer, halves to even
+            d[i] = fabsf(q - n[e + i]);
+        }
+        far = max_nan(far, d[0], d[1]);
     }
-    if (half) {
+    // rounded scales and offsets can take the ends past 0 and 15, too
+    if (far > 0.499992f || (lo - z) * inv < -0.499f || (hi - z) * inv > 15.499f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kPart; ++e) {
             const float q = (x[e] - z) * inv;
             float r = rintf(q);
-            if (fabsf(fabsf(q - r) - 0.5f) < 1e-4f) r = (float)rint(((double)x[e] - (double)z) / (double)s);
+            if (fabsf(fabsf(q - r) - 0.5f) < 1e-5f) {
+                const float m = floorf(q), d = x[e] - z, xx = d + z;
+                const float rest = (x[e] - xx) + ((xx - d) - z);   // what d lacks of x - z
+                const float over = fmaf(-(m + 0.5f), s, d) + rest;
+                r = over > 0.f ? m + 1.f : over < 0.f ? m : 2.f * rintf(0.5f * m + 0.25f);
+            }
             n[e] = fminf(fmaxf(r, 0.f), 15.f);
         }
     }
-    const float a = fmaf(fmaf(fmaf(n[3], 16.f, n[2]), 16.f, n[1]), 16.f, n[0]);
-    const float b = fmaf(fmaf(fmaf(n[7], 16.f, n[6]), 16.f, n[5]), 16.f, n[4]);
-    return (uint32_t)a | (uint32_t)b << 16;
+    // four codes are added up exactly in fp32
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)fmaf(fmaf(fmaf(n[4 * e + 3], 16.f, n[4 * e + 2]), 16.f, n[4 * e + 1]), 16.f, n[4 * e]);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-template <int D>
+// Bound by issue slots, not by memory.
+template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads) qappend_kernel(QRowsCall a) {
     pdl_wait();
     pdl_launch_dependents();
@@ -149,84 +191,76 @@ __global__ void __launch_bounds__(kRowThreads) qappend_kernel(QRowsCall a) {
             limit = limit < 0 ? 0 : a.n;
         }
     }
-    const RowPart<D> p(a, b, limit);
-    float x[kRowSteps][2][8];
-#pragma unroll
-    for (int i = 0; i < kRowSteps; ++i)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][v][e] = 0.f;
-            const QRowsK &r = v ? a.v : a.k;
-            if (p.slot[i] >= 0) load8(r, b * r.ldb + p.t[i] * r.ldt + p.h[i] * r.ldh + p.c8, x[i][v]);
-        }
+    // the rows' loads do not wait for their slots
+    const RowPart<D, kPart> p(a, limit, blockIdx.x);
+    Raw8<T> raw[2][2] = {};
+    if (p.row) {
+        const int64_t ki = b * a.k.ldb + p.t * a.k.ldt + p.h * a.k.ldh + p.c, vi = b * a.v.ldb + p.t * a.v.ldt + p.h * a.v.ldh + p.c;
+        raw[0][0].load(a.k, ki);
+        raw[0][1].load(a.k, ki + 8);
+        raw[1][0].load(a.v, vi);
+        raw[1][1].load(a.v, vi + 8);
+    }
     const int first = a.pos ? ld_dep(a.pos + b) : 0;
+    const int slot = p.row ? slot_of(a, b, p.h, p.t) : -1;
+    const int64_t at = slot >= 0 ? a.c.slot0(b, p.h) + slot : 0;
 #pragma unroll
-    for (int i = 0; i < kRowSteps; ++i) {
-        const int64_t at = p.slot[i] >= 0 ? a.c.slot0(b, p.h[i]) + p.slot[i] : 0;
+    for (int v = 0; v < 2; ++v) {
+        float x[kPart], lo, hi;
+        raw[v][0].get(*reinterpret_cast<float(*)[8]>(x));
+        raw[v][1].get(*reinterpret_cast<float(*)[8]>(x + 8));
+        bounds(x, lo, hi);
+        if (!(fmaxf(fabsf(lo), fabsf(hi)) <= 65504.f) || lo != lo) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            float lo = INFINITY, hi = -INFINITY;
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                odd |= !(fabsf(x[i][v][e]) <= 65504.f);
-                lo = fminf(lo, x[i][v][e]);
-                hi = fmaxf(hi, x[i][v][e]);
-            }
-            if (odd) {
-                lo = INFINITY;
-                hi = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float &y = x[i][v][e];
-                    y = y != y ? 0.f : fminf(fmaxf(y, -65504.f), 65504.f);
-                    lo = fminf(lo, y);
-                    hi = fmaxf(hi, y);
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-            }
-            if (p.slot[i] < 0) continue;
-            __half sh, zh;
-            const uint32_t codes = quantise8(x[i][v], lo, hi, sh, zh);
-            reinterpret_cast<uint32_t *>(v ? a.c.v : a.c.k)[at * (D / 8) + p.c8 / 8] = codes;
-            if (p.c8 % kQGroup == 0)
-                (v ? a.c.vs : a.c.ks)[at * (D / kQGroup) + p.c8 / kQGroup] =
-                    (uint32_t)__half_as_ushort(sh) | (uint32_t)__half_as_ushort(zh) << 16;
+            for (int e = 0; e < kPart; ++e) x[e] = x[e] != x[e] ? 0.f : fminf(fmaxf(x[e], -65504.f), 65504.f);
+            bounds(x, lo, hi);
         }
-        if (p.slot[i] >= 0 && p.c8 == 0) {
-            if (a.c.weight) a.c.weight[at] = 0.f;
-            if (a.c.pos) a.c.pos[at] = first + p.t[i];
+#pragma unroll
+        for (int o = 1; o < kQGroup / kPart; o <<= 1) {
+            lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
         }
+        if (slot < 0) continue;
+        __half sh, zh;
+        const uint2 codes = quantise(x, lo, hi, sh, zh);
+        reinterpret_cast<uint2 *>(v ? a.c.v : a.c.k)[at * (D / kPart) + p.c / kPart] = codes;
+        if (p.c % kQGroup == 0)
+            (v ? a.c.vs : a.c.ks)[at * (D / kQGroup) + p.c / kQGroup] =
+                (uint32_t)__half_as_ushort(sh) | (uint32_t)__half_as_ushort(zh) << 16;
+    }
+    if (slot >= 0 && p.c == 0) {
+        if (a.c.weight) a.c.weight[at] = 0.f;
+        if (a.c.pos) a.c.pos[at] = first + p.t;
     }
 }
 
+// 8 channels to a thread here, of two rows: 16-byte stores side by side (with 16
+// channels a warp's stores leave gaps, and 8,192 rows of 128 took 12.5 instead of 11.5 us).
+constexpr int kReadSteps = 2;
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) qread_kernel(QRowsCall a) {
     pdl_wait();
     pdl_launch_dependents();
+    using Part = RowPart<D, 8>;
     const int b = blockIdx.y;
-    const RowPart<D> p(a, b, a.n);
-    uint32_t codes[kRowSteps][2], sz[kRowSteps][2];
+    const Part p[kReadSteps] = {Part(a, a.n, blockIdx.x * kReadSteps), Part(a, a.n, blockIdx.x * kReadSteps + 1)};
+    uint32_t codes[kReadSteps][2], sz[kReadSteps][2];
 #pragma unroll
-    for (int i = 0; i < kRowSteps; ++i)
+    for (int i = 0; i < kReadSteps; ++i) {
+        const int slot = p[i].row ? slot_of(a, b, p[i].h, p[i].t) : -1;
+        const int64_t at = a.c.slot0(b, p[i].h) + slot;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            codes[i][v] = sz[i][v] = 0;
-            if (p.slot[i] < 0) continue;
-            const int64_t at = a.c.slot0(b, p.h[i]) + p.slot[i];
-            codes[i][v] = ld_dep(reinterpret_cast<const uint32_t *>(v ? a.c.v : a.c.k) + at * (D / 8) + p.c8 / 8);
-            sz[i][v] = ld_dep((v ? a.c.vs : a.c.ks) + at * (D / kQGroup) + p.c8 / kQGroup);
+            codes[i][v] = slot >= 0 ? ld_dep(reinterpret_cast<const uint32_t *>(v ? a.c.v : a.c.k) + at * (D / 8) + p[i].c / 8) : 0;
+            sz[i][v] = slot >= 0 ? ld_dep((v ? a.c.vs : a.c.ks) + at * (D / kQGroup) + p[i].c / kQGroup) : 0;
         }
+    }
 #pragma unroll
-    for (int i = 0; i < kRowSteps; ++i)
+    for (int i = 0; i < kReadSteps; ++i) {
+        if (!p[i].row) continue;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            if (!p.row[i]) continue;
+            const QRowsK &r = v ? a.v : a.k;
             float s, z, x[8];
             half2x(sz[i][v], s, z);
 #pragma unroll
@@ -237,9 +271,9 @@ __global__ void __launch_bounds__(kRowThreads) qread_kernel(QRowsCall a) {
                 x[e] = fmaf(s, n.x, z);
                 x[e + 4] = fmaf(s, n.y, z);
             }
-            const QRowsK &r = v ? a.v : a.k;
-            store8(r, b * r.ldb + p.t[i] * r.ldt + p.h[i] * r.ldh + p.c8, x);
+            store8(r, b * r.ldb + p[i].t * r.ldt + p[i].h * r.ldh + p[i].c, x);
         }
+    }
 }
 
 // --------------------------------------------------------------- evict, trim
@@ -358,38 +392,47 @@ __global__ void __launch_bounds__(kLongThreads) qevict_long_kernel(QEvictCall a)
 
 // A cluster of C CTAs of T threads per (sequence, head), K slots to a thread, all
 // in registers: a warp has 32 K consecutive slots.  The slots to give up are the
-// first e of the order (class, weight, slot): three histograms find the last
-// one's class and key (2 + 10, 11 and 11 bits), each CTA its own slots' counts,
-// which the cluster adds up a slice per CTA; then ballots number the chosen
-// slots, and the equal ones, in slot order.
-constexpr int kBins = 3 * 1024;
+// first e of the order (class, weight, slot).  One reduction gives the classes'
+// sizes and the keys' range, which a histogram of 2048 bins cuts up (weights
+// spread over many powers of two, so bins by leading bits would be few and
+// crowded); each CTA counts its own slots and the cluster adds a slice of the
+// bins per CTA.  The bin of the last slot to go holds few keys: they are gathered
+// and ranked against one another, or, if they are many (equal weights), cut up
+// again.  Then ballots number the chosen slots, and the equal ones, in slot order.
+constexpr int kBins = 2048, kRank = 256;
 
 template <int T>
 struct EvictShared {
     int hist[kBins];
     int red[kBins];
     int wsum[32];
-    int tot[8];          // the slices' totals
-    int pick[2];         // the bin, and what comes before it
+    uint32_t stat[T / 32][4];
+    uint32_t cstat[8][4];    // the CTAs'
+    int tot[8];              // the slices' totals
+    int pick[3];             // the bin, what comes before it, and its own count
+    uint32_t list[kRank];    // the first CTA's: keys to rank
+    int listed;
+    uint32_t last;           // the last key to go, and how many equal to it go
+    int ties;
     int lower[T / 32], same[T / 32];
-    int2 cta[8];         // the CTAs' chosen and equal slots
+    int2 cta[8];             // the CTAs' chosen and equal slots
     int used;
 };
 
-// The bin of the cluster's `want`-th value (from 1) among nb bins, and how many
-// lie in lower bins.
+// The bin of the cluster's `want`-th value (from 1), how many lie in lower bins, and in it.
 template <int T>
-__device__ int2 find_bin(EvictShared<T> &sh, cg::cluster_group &cl, int nb, int want) {
+__device__ int3 find_bin(EvictShared<T> &sh, cg::cluster_group &cl, int want) {
     const int C = (int)cl.num_blocks(), me = (int)cl.block_rank(), tid = threadIdx.x;
-    const int *counts = sh.hist;
-    int slice = nb, lo = 0, before = 0, owner = 0;
+    int *counts = sh.hist;
+    const int slice = kBins / C;
+    int lo = 0, before = 0, owner = 0;
     if (C > 1) {
-        slice = nb / C;
         lo = me * slice;
         cl.sync();
         int sum = 0;
         for (int i = tid; i < slice; i += T) {
             int v = 0;
+#pragma unroll 8
             for (int r = 0; r < C; ++r) v += cl.map_shared_rank(sh.hist, r)[lo + i];
             sh.red[i] = v;
             sum += v;
@@ -417,6 +460,7 @@ __device__ int2 find_bin(EvictShared<T> &sh, cg::cluster_group &cl, int nb, int 
                         int *to = C > 1 ? cl.map_shared_rank(sh.pick, r) : sh.pick;
                         to[0] = lo + i;
                         to[1] = at;
+                        to[2] = counts[i];
                     }
                     break;
                 }
@@ -425,7 +469,47 @@ __device__ int2 find_bin(EvictShared<T> &sh, cg::cluster_group &cl, int nb, int 
     }
     if (C > 1) cl.sync();
     else __syncthreads();
-    return make_int2(sh.pick[0], sh.pick[1]);
+    return make_int3(sh.pick[0], sh.pick[1], sh.pick[2]);
+}
+
+// Over the cluster: the sums of a and b, the least lo, the largest hi.
+template <int T>
+__device__ uint4 reduce_stat(EvictShared<T> &sh, cg::cluster_group &cl, uint32_t a, uint32_t b, uint32_t lo, uint32_t hi) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = (int)cl.num_blocks();
+    a = __reduce_add_sync(kFull, a);
+    b = __reduce_add_sync(kFull, b);
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    if (lane == 0) {
+        sh.stat[warp][0] = a;
+        sh.stat[warp][1] = b;
+        sh.stat[warp][2] = lo;
+        sh.stat[warp][3] = hi;
+    }
+    __syncthreads();
+    const bool in = lane < T / 32;
+    a = __reduce_add_sync(kFull, in ? sh.stat[lane % (T / 32)][0] : 0u);
+    b = __reduce_add_sync(kFull, in ? sh.stat[lane % (T / 32)][1] : 0u);
+    lo = __reduce_min_sync(kFull, sh.stat[lane % (T / 32)][2]);
+    hi = __reduce_max_sync(kFull, sh.stat[lane % (T / 32)][3]);
+    if (C > 1) {
+        if ((int)threadIdx.x < C) {
+            uint32_t *to = cl.map_shared_rank(&sh.cstat[0][0], threadIdx.x) + 4 * cl.block_rank();
+            to[0] = a;
+            to[1] = b;
+            to[2] = lo;
+            to[3] = hi;
+        }
+        cl.sync();
+        const bool at = lane < C;
+        a = __reduce_add_sync(kFull, at ? sh.cstat[lane & 7][0] : 0u);
+        b = __reduce_add_sync(kFull, at ? sh.cstat[lane & 7][1] : 0u);
+        lo = __reduce_min_sync(kFull, at ? sh.cstat[lane & 7][2] : 0xffffffffu);
+        hi = __reduce_max_sync(kFull, at ? sh.cstat[lane & 7][3] : 0u);
+    } else {
+        __syncthreads();
+    }
+    return make_uint4(a, b, lo, hi);
 }
 
 template <int T, int K>
@@ -436,6 +520,7 @@ __global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
     const int row = blockIdx.x / C, h = row % a.c.heads, b = row / a.c.heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < kBins; i += T) sh.hist[i] = 0;
+    if (tid == 0) sh.listed = 0;
     if (C > 1) cl.sync();   // the others' shared memory is there
     pdl_wait();
     pdl_launch_dependents();
@@ -455,43 +540,96 @@ __global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
         const int slot = first + 32 * i;
         key[i] = slot < cap ? __float_as_uint(ld_dep(a.c.weight + slot0 + slot)) : 0;
     }
+    if (a.c.pos) {
+        int p[K];
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int slot = first + 32 * i;
-        const int c = a.c.pos ? sc(slot < cap ? ld_dep(a.c.pos + slot0 + slot) : 0) : 1;
-        cls |= (uint32_t)c << (2 * i);
+        for (int i = 0; i < K; ++i) p[i] = first + 32 * i < cap ? ld_dep(a.c.pos + slot0 + first + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) cls |= (uint32_t)sc(p[i]) << (2 * i);
+    } else {
+        cls = 0x55555555u;
     }
     if (C > 1) cl.sync();
     else __syncthreads();
     const int used = sh.used;
     const int e = a.keep >= 0 ? max(0, used - a.keep) : max(0, a.n - (cap - used));
+    uint32_t n0 = 0, n2 = 0, lo = 0xffffffffu, hi = 0;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         key[i] = weight_key(__uint_as_float(key[i]));
         if (first + 32 * i >= used) cls |= 3u << (2 * i);
+        const uint32_t c = cls >> (2 * i) & 3u;
+        n0 += c == 0;
+        n2 += c == 2;
+        if (c == 1) {
+            lo = min(lo, key[i]);
+            hi = max(hi, key[i]);
+        }
     }
     int want = e;
-    uint32_t pc = 0, pk = 0;   // the last one's class and key
+    uint32_t pc = 1, pk = 0;   // the last one's class and key
     if (e > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const uint32_t c = cls >> (2 * i) & 3u;
-            if (c < 3) atomicAdd(&sh.hist[c * 1024 + (key[i] >> 22)], 1);
-        }
-        int2 p = find_bin<T>(sh, cl, kBins, want);
-        pc = (uint32_t)p.x >> 10;
-        pk = (uint32_t)(p.x & 1023) << 22;
-        want -= p.y;
-#pragma unroll 1
-        for (int shift = 11; shift >= 0; shift -= 11) {
-            for (int i = tid; i < 2048; i += T) sh.hist[i] = 0;
-            __syncthreads();
+        uint4 st = reduce_stat(sh, cl, n0, n2, lo, hi);
+        const int plain = used - (int)st.x - (int)st.y;
+        if (want <= (int)st.x || want > (int)st.x + plain) {
+            // it is an empty slot, or a protected one
+            pc = want <= (int)st.x ? 0 : 2;
+            want -= pc ? (int)st.x + plain : 0;
+            lo = 0xffffffffu;
+            hi = 0;
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if ((cls >> (2 * i) & 3u) == pc && (key[i] ^ pk) >> (shift + 11) == 0) atomicAdd(&sh.hist[key[i] >> shift & 2047u], 1);
-            p = find_bin<T>(sh, cl, 2048, want);
-            pk |= (uint32_t)p.x << shift;
+                if ((cls >> (2 * i) & 3u) == pc) {
+                    lo = min(lo, key[i]);
+                    hi = max(hi, key[i]);
+                }
+            if (C > 1) cl.sync();   // the others have read the first answer
+            st = reduce_stat(sh, cl, 0, 0, lo, hi);
+        } else {
+            want -= (int)st.x;
+        }
+        lo = st.z;
+        hi = st.w;
+        for (;;) {
+            const int shift = max(0, 21 - __clz(hi - lo));   // (hi - lo) >> shift < 2048
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if ((cls >> (2 * i) & 3u) == pc && key[i] >= lo && key[i] <= hi) atomicAdd(&sh.hist[(key[i] - lo) >> shift], 1);
+            const int3 p = find_bin<T>(sh, cl, want);
             want -= p.y;
+            lo += (uint32_t)p.x << shift;
+            hi = min(hi, lo + ((1u << shift) - 1u));
+            pk = lo;
+            if (shift == 0) break;
+            if (p.z <= kRank) {
+                uint32_t *list = C > 1 ? cl.map_shared_rank(sh.list, 0) : sh.list;
+                int *listed = C > 1 ? cl.map_shared_rank(&sh.listed, 0) : &sh.listed;
+#pragma unroll
+                for (int i = 0; i < K; ++i)
+                    if ((cls >> (2 * i) & 3u) == pc && key[i] >= lo && key[i] <= hi) list[atomicAdd(listed, 1)] = key[i];
+                if (C > 1) cl.sync();
+                else __syncthreads();
+                if (me == 0 && tid < p.z) {
+                    const uint32_t mine = sh.list[tid];
+                    int less = 0, equal = 0;
+                    for (int i = 0; i < p.z; ++i) {
+                        less += sh.list[i] < mine;
+                        equal += sh.list[i] == mine;
+                    }
+                    if (want > less && want <= less + equal)   // equal keys write the same
+                        for (int r = 0; r < C; ++r) {
+                            *cl.map_shared_rank(&sh.last, r) = mine;
+                            *cl.map_shared_rank(&sh.ties, r) = want - less;
+                        }
+                }
+                if (C > 1) cl.sync();
+                else __syncthreads();
+                pk = sh.last;
+                want = sh.ties;
+                break;
+            }
+            for (int i = tid; i < kBins; i += T) sh.hist[i] = 0;
+            __syncthreads();
         }
     }
     // `want` of the slots equal to (pc, pk) go, the first ones
@@ -501,10 +639,10 @@ __global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
     for (int i = 0; i < K; ++i) {
         const uint32_t c = cls >> (2 * i) & 3u;
         const bool in = e > 0 && c < 3;
-        const bool lo = in && (c < pc || (c == pc && key[i] < pk)), eq = in && c == pc && key[i] == pk;
-        lower |= (uint32_t)lo << i;
+        const bool lt = in && (c < pc || (c == pc && key[i] < pk)), eq = in && c == pc && key[i] == pk;
+        lower |= (uint32_t)lt << i;
         same |= (uint32_t)eq << i;
-        nl += __popc(__ballot_sync(kFull, lo));
+        nl += __popc(__ballot_sync(kFull, lt));
         ns += __popc(__ballot_sync(kFull, eq));
     }
     if (lane == 0) {
@@ -512,16 +650,10 @@ __global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
         sh.same[warp] = ns;
     }
     __syncthreads();
-    int bl = 0, bs = 0, tl = 0, ts = 0;
-    for (int w = 0; w < T / 32; ++w) {
-        if (w < warp) {
-            bl += sh.lower[w];
-            bs += sh.same[w];
-        }
-        tl += sh.lower[w];
-        ts += sh.same[w];
-    }
+    const int vl = lane < T / 32 ? sh.lower[lane % (T / 32)] : 0, vs = lane < T / 32 ? sh.same[lane % (T / 32)] : 0;
+    int bl = __reduce_add_sync(kFull, lane < warp ? vl : 0), bs = __reduce_add_sync(kFull, lane < warp ? vs : 0);
     if (C > 1) {
+        const int tl = __reduce_add_sync(kFull, vl), ts = __reduce_add_sync(kFull, vs);
         if (tid < C) cl.map_shared_rank(sh.cta, tid)[me] = make_int2(tl, ts);
         cl.sync();
         for (int r = 0; r < me; ++r) {
@@ -533,19 +665,21 @@ __global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
     const int room = a.keep >= 0 ? a.keep : a.n;
     int32_t *out = a.out + ((int64_t)b * a.c.heads + h) * room;
     const uint32_t below = (1u << lane) - 1u;
+    if (a.keep >= 0 || nl + ns > 0) {
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int slot = first + 32 * i;
-        const uint32_t wl = __ballot_sync(kFull, lower >> i & 1u), we = __ballot_sync(kFull, same >> i & 1u);
-        const int eqs = bs + __popc(we & below);
-        const bool gone = (lower >> i & 1u) || ((same >> i & 1u) && eqs < want);
-        const int at = bl + __popc(wl & below) + min(eqs, want);   // slots before this one that go
-        bl += __popc(wl);
-        bs += __popc(we);
-        if (a.keep >= 0) {
-            if (slot < used && !gone && slot - at < room) out[slot - at] = slot;
-        } else if (gone && at < room) {
-            out[at] = slot;
+        for (int i = 0; i < K; ++i) {
+            const int slot = first + 32 * i;
+            const uint32_t wl = __ballot_sync(kFull, lower >> i & 1u), we = __ballot_sync(kFull, same >> i & 1u);
+            const int eqs = bs + __popc(we & below);
+            const bool gone = (lower >> i & 1u) || ((same >> i & 1u) && eqs < want);
+            const int at = bl + __popc(wl & below) + min(eqs, want);   // slots before this one that go
+            bl += __popc(wl);
+            bs += __popc(we);
+            if (a.keep >= 0) {
+                if (slot < used && !gone && slot - at < room) out[slot - at] = slot;
+            } else if (gone && at < room) {
+                out[at] = slot;
+            }
         }
     }
     if (a.keep < 0 && me == 0)
@@ -621,14 +755,16 @@ cudaError_t launch_evict(const QEvictCall &a, int ctas, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, qevict_kernel<T, K>, a);
 }
 
+constexpr int kMinSlots = 2048;   // (a cluster's barriers cost more than halving fewer: 40 rows of 2,048 in two CTAs each took 8.1, not 5.1 us)
 cudaError_t choose_slots(const QEvictCall &a, cudaStream_t s) {
     const int cap = a.keep >= 0 ? a.c.cap : a.limit, sms = device_sm_count();
     const int64_t rows = (int64_t)a.c.heads * a.c.batch;
     // few rows: several CTAs each, as long as the GPU has room and a CTA has at least 2048 slots
     int ctas = 1;
-    while (ctas < 8 && ((rows * ctas * 2 <= 2 * sms && cap / (2 * ctas) >= 2048) || cap > 16384 * ctas)) ctas *= 2;
+    while (ctas < 8 && ((rows * ctas * 2 <= 2 * sms && cap / (2 * ctas) >= kMinSlots) || cap > 16384 * ctas)) ctas *= 2;
     const int each = (cap + ctas - 1) / ctas;
     if (each <= 2048) return launch_evict<512, 4>(a, ctas, s);
+    if (each <= 4096) return launch_evict<512, 8>(a, ctas, s);
     if (each <= 8192) return launch_evict<512, 16>(a, ctas, s);
     if (each <= 16384) return launch_evict<1024, 16>(a, ctas, s);
     return launch(qevict_long_kernel, dim3(a.c.heads, a.c.batch), dim3(kLongThreads), 0, s, pdl_enabled(), a);
@@ -727,9 +863,8 @@ cudaError_t by_d(int d, F f) {
     default: return f(std::integral_constant<int, 256>());
     }
 }
-template <int D>
-dim3 rows_grid(const QRowsCall &a) {
-    const int64_t rows = (int64_t)a.n * a.c.heads, each = RowPart<D>::ROWS * kRowSteps;
+dim3 rows_grid(const QRowsCall &a, int each) {
+    const int64_t rows = (int64_t)a.n * a.c.heads;
     return dim3((unsigned)((rows + each - 1) / each), a.c.batch);
 }
 
@@ -790,7 +925,12 @@ cs_status cs_qcache_append(const cs_qcache *cache, const cs_head_rows *k, const 
     a.pos = pos;
     if (n == 0) return CS_OK;
     const cudaError_t e = by_d(a.c.d, [&](auto d) {
-        return launch(qappend_kernel<d()>, rows_grid<d()>(a), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
+        auto go = [&](auto kernel) {
+            return launch(kernel, rows_grid(a, RowPart<d(), kPart>::ROWS), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
+        };
+        return a.k.dt == CS_F32   ? go(qappend_kernel<d(), float>)
+               : a.k.dt == CS_F16 ? go(qappend_kernel<d(), __half>)
+                                  : go(qappend_kernel<d(), __nv_bfloat16>);
     });
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
@@ -803,7 +943,7 @@ cs_status cs_qcache_read(const cs_qcache *cache, const cs_head_rows *k, const cs
     if (st != CS_OK) return st;
     if (n == 0) return CS_OK;
     const cudaError_t e = by_d(a.c.d, [&](auto d) {
-        return launch(qread_kernel<d()>, rows_grid<d()>(a), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
+        return launch(qread_kernel<d()>, rows_grid(a, RowPart<d(), 8>::ROWS * kReadSteps), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
     });
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
