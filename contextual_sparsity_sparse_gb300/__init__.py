@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 import threading
 
@@ -70,7 +71,7 @@ class _QCache(C.Structure):
                 ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("weight", C.c_void_p), ("pos", C.c_void_p)]
 
 
-class _Rows(C.Structure):
+class _Rows(C.Structure):   # cs_head_rows, for callers of the C ABI through lib()
     _fields_ = [("data", C.c_void_p), ("dtype", C.c_int), ("ld_batch", C.c_int64), ("ld_token", C.c_int64),
                 ("ld_head", C.c_int64)]
 
@@ -421,6 +422,7 @@ class QCache:
         self.ld_batch, self.ld_head = ld
         self.c = _QCache(self.batch, self.n_heads, self.d_head, self.capacity, self.ld_batch, self.ld_head, _ptr(k),
                          _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), _ptr(pos))
+        self.addr = C.addressof(self.c)
 
     def _slots(self, t, tail, ld=None):
         """The slots from one sequence and one head of t to the next, which have to be `ld` if that is given."""
@@ -468,54 +470,35 @@ class QCacheWorkspace:
         _check(lib().cs_workspace_init(self.ptr, self.nbytes, _stream(stream)))
 
 
-def _rows(t, batch, heads, d_head, what):
-    """cs_head_rows of a [batch, tokens, heads, d_head] tensor with contiguous rows."""
-    shape, st = t.shape, t.stride()
-    if len(st) != 4 or shape[0] != batch or shape[2] != heads or shape[3] != d_head or st[3] != 1:
-        raise ValueError(f"{what}: expected [{batch}, tokens, {heads}, {d_head}] with contiguous rows, got "
-                         f"{tuple(shape)} with strides {st}")
-    dt = _TORCH_DT.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{what}: dtype {t.dtype} is not fp32, fp16 or bf16")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    return _Rows(t.data_ptr(), dt, st[0], st[1], st[2])
+_qcall = None
 
 
-def _ints(t, shape, what):
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous int32 tensor of shape {shape}")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    return t.data_ptr()
+def _q():
+    """The native marshalling of the qcache calls (csrc/qcall.c), bound to libcs.so."""
+    global _qcall
+    if _qcall is None:
+        L = lib()
+        spec = importlib.util.spec_from_file_location("_qcall", _build.QCALL)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.init(torch.float32, torch.float16, torch.bfloat16, torch.int32,
+               *(C.cast(getattr(L, f"cs_qcache_{f}"), C.c_void_p).value
+                 for f in ("append", "read", "attention", "evict", "trim")))
+        _qcall = m
+    return _qcall
 
 
 def cs_qcache_append(cache: QCache, k, v, ws: QCacheWorkspace, start=None, slots=None, n_new=None, pos=None,
                      stream=None):
     """Quantise the new rows k and v [batch, n, n_heads, d_head] into slots
     start[b] + t, or slots[b, h, t] (see include/cs.h)."""
-    B, H = cache.batch, cache.n_heads
-    kr, vr = _rows(k, B, H, cache.d_head, "k"), _rows(v, B, H, cache.d_head, "v")
-    n = k.shape[1]
-    if v.shape[1] != n:
-        raise ValueError("k and v differ in their number of tokens")
-    _check(lib().cs_qcache_append(C.byref(cache.c), C.byref(kr), C.byref(vr), n, _ints(start, (B,), "start"),
-                                  _ints(slots, (B, H, n), "slots"), _ints(n_new, (B,), "n_new"),
-                                  _ints(pos, (B,), "pos"), ws.ptr, ws.nbytes, _stream(stream)))
+    _check(_q().append(cache.addr, k, v, start, slots, n_new, pos, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def cs_qcache_read(cache: QCache, k, v, ws: QCacheWorkspace, start=None, slots=None, stream=None):
     """The values of slots start[b] + t, or slots[b, h, t], into k and v
     [batch, n, n_heads, d_head] (see include/cs.h)."""
-    B, H = cache.batch, cache.n_heads
-    kr, vr = _rows(k, B, H, cache.d_head, "k"), _rows(v, B, H, cache.d_head, "v")
-    n = k.shape[1]
-    if v.shape[1] != n:
-        raise ValueError("k and v differ in their number of tokens")
-    _check(lib().cs_qcache_read(C.byref(cache.c), C.byref(kr), C.byref(vr), n, _ints(start, (B,), "start"),
-                                _ints(slots, (B, H, n), "slots"), ws.ptr, ws.nbytes, _stream(stream)))
+    _check(_q().read(cache.addr, k, v, start, slots, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def cs_qcache_attention(cache: QCache, q, length, out, ws: QCacheWorkspace, q_pos=None, mask=None, scale=0.0,
@@ -525,43 +508,30 @@ def cs_qcache_attention(cache: QCache, q, length, out, ws: QCacheWorkspace, q_po
     ceil(n_heads / 32)], the query heads to compute (cs_select's mask).
     weight: gathers decay * cache.weight + this step's attention per slot; a
     tensor that steps like cache.weight, often cache.weight itself."""
-    B = cache.batch
-    if q.dim() != 4 or q.shape != out.shape:
-        raise ValueError("q and out must be [batch, n_q, n_heads, d_head] tensors of one shape")
-    heads = q.shape[2]
-    qr, orr = _rows(q, B, heads, cache.d_head, "q"), _rows(out, B, heads, cache.d_head, "out")
     if mask is not None and (mask.element_size() != 4 or mask.is_floating_point() or not mask.is_contiguous()
-                             or tuple(mask.shape) != (B, -(-heads // 32))):
+                             or tuple(mask.shape) != (cache.batch, -(-q.shape[2] // 32))):
         raise ValueError("mask: expected contiguous 32-bit words [batch, ceil(n_heads / 32)]")
-    if weight is not None:
-        if weight.dtype != torch.float32 or tuple(weight.shape) != (B, cache.n_heads, cache.capacity):
+    if weight is not None and weight is not cache.weight:
+        if weight.dtype is not torch.float32 or weight.shape != (cache.batch, cache.n_heads, cache.capacity):
             raise ValueError("weight: expected fp32 [batch, n_heads, capacity]")
-        cache._slots(weight, (), (cache.ld_batch, cache.ld_head))
-    _check(lib().cs_qcache_attention(C.byref(cache.c), C.byref(qr), heads, q.shape[1], _ints(length, (B,), "length"),
-                                     _ints(q_pos, (B,), "q_pos"), _ptr(mask), float(scale), float(decay),
-                                     _ptr(weight), C.byref(orr), ws.ptr, ws.nbytes, _stream(stream)))
+        if cache.weight is None or weight.stride() != cache.weight.stride():
+            cache._slots(weight, (), (cache.ld_batch, cache.ld_head))
+    _check(_q().attention(cache.addr, q, length, out, q_pos, _ptr(mask) or 0, scale, _ptr(weight) or 0, decay, ws.ptr,
+                          ws.nbytes, _stream(stream)))
 
 
 def cs_qcache_evict(cache: QCache, length, limit, slots, ws: QCacheWorkspace, next_pos=None, sinks=0, recent=0,
                     stream=None):
     """slots [batch, n_heads, n] = where the next n tokens go when at most
     `limit` slots may be in use (see include/cs.h)."""
-    B = cache.batch
-    if slots.dim() != 3:
-        raise ValueError("slots: expected int32 [batch, n_heads, n]")
-    n = slots.shape[2]
-    _check(lib().cs_qcache_evict(C.byref(cache.c), _ints(length, (B,), "length"), int(limit), n,
-                                 _ints(next_pos, (B,), "next_pos"), int(sinks), int(recent),
-                                 _ints(slots, (B, cache.n_heads, n), "slots"), ws.ptr, ws.nbytes, _stream(stream)))
+    _check(_q().evict(cache.addr, length, limit, slots, next_pos, sinks, recent, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def cs_qcache_trim(cache: QCache, length, keep, dst: QCache, ws: QCacheWorkspace, next_pos=None, sinks=0, recent=0,
                    stream=None):
     """Copy each head's `keep` heaviest slots to the front of dst (see
     include/cs.h)."""
-    _check(lib().cs_qcache_trim(C.byref(cache.c), _ints(length, (cache.batch,), "length"), int(keep),
-                                _ints(next_pos, (cache.batch,), "next_pos"), int(sinks), int(recent),
-                                C.byref(dst.c), ws.ptr, ws.nbytes, _stream(stream)))
+    _check(_q().trim(cache.addr, length, keep, dst.addr, next_pos, sinks, recent, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def cs_stack_release():

@@ -10,6 +10,7 @@ import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libcs.so")
+QCALL = os.path.join(OUT_DIR, "_qcall.so")   # the qcache calls' marshalling, a CPython module
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -28,13 +30,14 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.c")) +
+            glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(QCALL):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(QCALL))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -54,9 +57,20 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(r.stdout, r.stderr)
         return obj
 
+    def compile_qcall():
+        tmp = QCALL + f".tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-shared", "-fPIC", f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}",
+               os.path.join(CSRC, "qcall.c"), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed on qcall.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, QCALL)
+
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        qcall = ex.submit(compile_qcall)
         objs = list(ex.map(compile_one, srcs))
+        qcall.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = ["nvcc", *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

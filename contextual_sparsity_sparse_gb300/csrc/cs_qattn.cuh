@@ -83,11 +83,12 @@ struct Cfg {
     static constexpr int ST = D == 64 ? 4 : MINB == 2 ? 2 : 3;
     static constexpr int RS = D + 4;                         // floats of a joined column (conflict-free)
     static constexpr int QF = NT * PARTS * (D / 32) * 32;    // uint4 fragments of q, two products each
-    static constexpr int RED = kWarps * 4 * RS;              // floats: four columns of every warp
+    static constexpr int CP = RP < 8 || 8 * RS * 4 > STAGE ? 4 : 8;   // columns that are joined at a time: a warp's go into a stage
     static constexpr int CS = 3 + G;                         // floats of a column: c1, last position, on, sums of q
-    static constexpr int STAT = kWarps * RP * 2 + 3 * RP;    // floats: the warps' bases and sums, then the joined ones
+    static constexpr int STAT = kWarps * RP * 2 + 3 * RP;    // floats: the warps' maxima (then factors) and sums, then the joined ones
     static constexpr int REC = RP * (D + 3);                 // floats of a record
-    static constexpr size_t smem_fixed = (size_t)kWarps * ST * STAGE + QF * 16 + (RED + RP * CS + STAT) * 4;
+    static_assert(CP * RS * 4 <= STAGE && RP % CP == 0, "a pass of the join fits a stage");
+    static constexpr size_t smem_fixed = (size_t)kWarps * ST * STAGE + 2 * (QF * 16 + RP * CS * 4) + STAT * 4;
 };
 
 template <int N>
@@ -184,13 +185,31 @@ __device__ __forceinline__ bool row_on(const QAttnK &k, int b, int h, int r) {
     return ld_dep(k.a.mask + (int64_t)b * ((k.a.heads + 31) / 32) + (j >> 5)) >> (j & 31) & 1u;
 }
 
-// The cache head that is the sequence's n-th with a chosen query head.
+// How many cache heads have a chosen query head; the whole warp asks together.
+__device__ __forceinline__ int heads_on(const QAttnK &k, int b) {
+    if (!k.a.mask) return k.a.c.heads;
+    int n = 0;
+    for (int h0 = 0; h0 < k.a.c.heads; h0 += 32) {
+        const int h = h0 + (threadIdx.x & 31);
+        n += __popc(__ballot_sync(kFull, h < k.a.c.heads && kv_on(k, b, h)));
+    }
+    return n;
+}
+
+// The cache head that is the sequence's n-th with a chosen query head; the whole warp asks together.
 __device__ __forceinline__ int chosen_head(const QAttnK &k, int b, int n) {
     if (!k.a.mask) return n;
-    int h = 0;
-    for (; h < k.a.c.heads - 1; ++h)
-        if (kv_on(k, b, h) && n-- == 0) break;
-    return h;
+    for (int h0 = 0; h0 < k.a.c.heads; h0 += 32) {
+        const int h = h0 + (threadIdx.x & 31);
+        const uint32_t on = __ballot_sync(kFull, h < k.a.c.heads && kv_on(k, b, h));
+        const int c = __popc(on);
+        if (n < c) {
+            const bool it = (on >> (threadIdx.x & 31) & 1u) && __popc(on & ((1u << (threadIdx.x & 31)) - 1u)) == n;
+            return h0 + __ffs(__ballot_sync(kFull, it)) - 1;
+        }
+        n -= c;
+    }
+    return k.a.c.heads - 1;   // not reached while the mask stays as it was counted
 }
 
 // In shared memory per sequence: its length, and where it starts on the axis (one more at the end).
@@ -200,14 +219,7 @@ struct Axis {
     int begin, end;   // this CTA's part
 
     template <int UT>
-    __device__ __forceinline__ int take(const QAttnK &k, int b, bool flag) {
-        const int n = q_length(k.a.length, b, k.a.c.cap, flag ? k.a.err : nullptr);
-        int heads = k.a.c.heads;
-        if (k.a.mask) {
-            heads = 0;
-            for (int h = 0; h < k.a.c.heads; ++h) heads += kv_on(k, b, h);
-        }
-        len[b] = n;
+    __device__ __forceinline__ int cost(int n, int heads) {
         return n ? ((n + UT - 1) / UT + kHeadCost) * heads : 0;
     }
 
@@ -215,28 +227,49 @@ struct Axis {
     __device__ void build(const QAttnK &k, int *smem, int *wsum, bool flag) {
         len = smem;
         pre = smem + k.a.c.batch;
-        const int B = k.a.c.batch;
+        const int B = k.a.c.batch, lane = threadIdx.x & 31;
+        uint32_t *err = flag ? k.a.err : nullptr;
         int total;
         if (B <= 32) {
             // every warp writes the same values, so no warp waits for another
-            const int lane = threadIdx.x & 31;
-            const int v = lane < B ? take<UT>(k, lane, flag) : 0;
+            const int n = lane < B ? q_length(k.a.length, lane, k.a.c.cap, err) : 0;
+            int heads = k.a.c.heads;
+            if (k.a.mask) {
+#pragma unroll 4
+                for (int b = 0; b < B; ++b) {
+                    const int on = heads_on(k, b);
+                    if (lane == b) heads = on;
+                }
+            }
+            const int v = cost<UT>(n, heads);
             int inc = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(kFull, inc, o);
-                if (lane >= o) inc += n;
+                const int m = __shfl_up_sync(kFull, inc, o);
+                if (lane >= o) inc += m;
             }
             total = __shfl_sync(kFull, inc, 31);
-            if (lane < B) pre[lane] = inc - v;
+            if (lane < B) {
+                len[lane] = n;
+                pre[lane] = inc - v;
+            }
             if (lane == 0) pre[B] = total;
             __syncwarp();
         } else {
+            if (k.a.mask) {
+                for (int b = threadIdx.x >> 5; b < B; b += kWarps) {
+                    const int on = heads_on(k, b);
+                    if (lane == 0) pre[b] = on;
+                }
+                __syncthreads();
+            }
             const int each = (B + kThreads - 1) / kThreads;
             const int b0 = min(B, (int)threadIdx.x * each), b1 = min(B, b0 + each);
             int sum = 0;
             for (int b = b0; b < b1; ++b) {
-                const int v = take<UT>(k, b, flag);
+                const int n = q_length(k.a.length, b, k.a.c.cap, err);
+                const int v = cost<UT>(n, k.a.mask ? pre[b] : k.a.c.heads);
+                len[b] = n;
                 pre[b] = v;   // not yet summed
                 sum += v;
             }
@@ -348,6 +381,12 @@ __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, i
 
 // ------------------------------------------------------------- first kernel
 
+// A row's m moves only when an x leads it by more than 2^kLead in p (moving it
+// scales all sums): most rows keep the m of their first unit.  p s 2^(kUp - e) of
+// a p up to 2^kLead, with s below 2^(e - 14), stays below 2^15.
+constexpr float kLead = 8.f;
+constexpr int kUp = 29 - 8;
+
 template <int D, int MODE>
 struct Tile {
     using C = Cfg<D, MODE>;
@@ -356,20 +395,22 @@ struct Tile {
     float l[C::NT][2];               // sums of p, this lane's slots
     float m[C::NT][2];               // largest x so far
     float ms[C::NT][2];              // the same, 0 for -inf
-    int e;                           // exponent field of the largest value scale so far; the sums hold p 2^(29 - e)
+    float t[C::NT][2];               // an x beyond this one moves m
+    int e;                           // exponent field of the largest value scale so far; the sums hold p 2^(kUp - e)
     float es;                        // the least scale with a larger one
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) {
 #pragma unroll
-            for (int t = 0; t < C::G * 4; ++t)
+            for (int x = 0; x < C::G * 4; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[t][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) o[x][n][i] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[n][i] = -INFINITY;
                 ms[n][i] = 0.f;
+                t[n][i] = -INFINITY;
                 l[n][i] = 0.f;
 #pragma unroll
                 for (int g = 0; g < C::G; ++g) z[g][n][i] = 0.f;
@@ -432,14 +473,16 @@ template <int D, int MODE, bool LO>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAttnK k) {
     using C = Cfg<D, MODE>;
     extern __shared__ __align__(16) char smem[];
-    uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * C::ST * C::STAGE);
-    float *red = reinterpret_cast<float *>(qf + C::QF);
-    float *cols = red + C::RED;
-    float *stat = cols + C::RP * C::CS;
+    // this head's query fragments and column data, and the next one's
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)kWarps * C::ST * C::STAGE), *qf_next = qf + C::QF;
+    float *cols = reinterpret_cast<float *>(qf_next + C::QF), *cols_next = cols + C::RP * C::CS;
+    float *stat = cols_next + C::RP * C::CS;
     int *axis_mem = reinterpret_cast<int *>(stat + C::STAT);
     __shared__ int wsum[32];
     __shared__ int wexp[kWarps];
-    __shared__ int64_t outs[C::RP];
+    __shared__ int woff[kWarps];
+    __shared__ int64_t outs[2][C::RP];
+    int64_t *out_row = outs[0], *out_next = outs[1];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
     const QCacheK &c = k.a.c;
@@ -508,75 +551,101 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
             for (int e = 0; e < D / 32; ++e) qv[i][e] = on ? k.sign * q_load1(k.a.q, src + e * 32 + lane) : 0.f;
         }
     };
+    // ... turned into fragments, and the columns' data, of head h of sequence b, in the `next` buffers
+    auto put_q = [&](int b, int h) {
+        __half *qh = reinterpret_cast<__half *>(qf_next);
+#pragma unroll
+        for (int qi = 0; qi < QR; ++qi) {
+            const int row = warp + qi * kWarps;
+            if (row >= C::RP) break;
+            float (&q)[D / 32] = qv[qi];
+            float big = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) big = fmaxf(big, fabsf(q[i]));
+            big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(big)));
+            // the power of two that takes the largest to [2^14, 2^15); infinities stay what they are
+            const int eb = (int)(__float_as_uint(big) >> 23);
+            const int up = big > 0.f && eb < 255 ? min(141 - eb, 127) : 0;
+            const float f1 = __uint_as_float((uint32_t)(127 + up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                // channel 32 i + lane of the row is nibble `nib` of word `w` of lane jj's two words of its group
+                const int jj = (i & 1) * 2 + (lane >> 4), w = (i & ~1) + ((lane >> 3) & 1), nib = lane & 7;
+                q[i] = q[i] * f1 * f2;
+                const float v = nib & 1 ? q[i] * 0.0625f : q[i];
+                const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+                const int col = row & 7, nt = row >> 3;
+                auto put = [&](int tile, int cc, __half x) {
+                    qh[((tile * (D / 32) + w) * 32 + cc * 4 + jj) * 8 + ((nib & 3) >> 1) * 4 + (nib & 1) * 2 + (nib >> 2)] = x;
+                };
+                put(nt * C::PARTS, col, hi);
+                if (C::PARTS == 1) put(0, col + 4, lo);
+                else if (LO) put(nt * 2 + 1, col, lo);
+            }
+            float sum[C::G];
+#pragma unroll
+            for (int g = 0; g < C::G; ++g) sum[g] = warp_sum(q[2 * g] + q[2 * g + 1]);
+            if (lane == 0) {
+                float *cc = cols_next + row * C::CS;
+                out_next[row] = out_at(k, b, h, row);
+                // takes the products back; kept where x c1 stays in fp32's range (beyond, one slot takes all as well)
+                cc[0] = fminf(fmaxf(k.c2 * exp2f((float)(24 - up)), 1.2e-38f), 1.2e30f);
+                cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + b) + (k.row0 + row) / k.group : INT_MAX);
+                cc[2] = row_on(k, b, h, row) ? 1.f : 0.f;
+#pragma unroll
+                for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * 5.9604644775390625e-8f;   // 2^-24, as the products
+            }
+        }
+    };
+    auto turn = [&]() {
+        uint4 *t = qf;
+        qf = qf_next;
+        qf_next = t;
+        float *u = cols;
+        cols = cols_next;
+        cols_next = u;
+        int64_t *v = out_row;
+        out_row = out_next;
+        out_next = v;
+    };
     if (s.u0 >= s.u1) return;   // only the last head of a CTA's part can have no unit in it
     int head = chosen_head(k, s.b, s.h);
     fetch_q(s.b, head);
+    put_q(s.b, head);
+    turn();
+    __syncthreads();
     for (;;) {
-        // ---- this head's query rows as fragments, a warp to a row
-        {
-            __half *qh = reinterpret_cast<__half *>(qf);
-#pragma unroll
-            for (int qi = 0; qi < QR; ++qi) {
-                const int row = warp + qi * kWarps;
-                if (row >= C::RP) break;
-                float (&q)[D / 32] = qv[qi];
-                float big = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) big = fmaxf(big, fabsf(q[i]));
-#pragma unroll
-                for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-                // the power of two that takes the largest to [2^14, 2^15); infinities stay what they are
-                const int eb = (int)(__float_as_uint(big) >> 23);
-                const int up = big > 0.f && eb < 255 ? min(141 - eb, 127) : 0;
-                const float f1 = __uint_as_float((uint32_t)(127 + up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    // channel 32 i + lane of the row is nibble `nib` of word `w` of lane jj's two words of its group
-                    const int jj = (i & 1) * 2 + (lane >> 4), w = (i & ~1) + ((lane >> 3) & 1), nib = lane & 7;
-                    q[i] = q[i] * f1 * f2;
-                    const float v = nib & 1 ? q[i] * 0.0625f : q[i];
-                    const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
-                    const int col = row & 7, nt = row >> 3;
-                    auto put = [&](int tile, int cc, __half h) {
-                        qh[((tile * (D / 32) + w) * 32 + cc * 4 + jj) * 8 + ((nib & 3) >> 1) * 4 + (nib & 1) * 2 + (nib >> 2)] = h;
-                    };
-                    put(nt * C::PARTS, col, hi);
-                    if (C::PARTS == 1) put(0, col + 4, lo);
-                    else put(nt * 2 + 1, col, lo);
-                }
-                float sum[C::G];
-#pragma unroll
-                for (int g = 0; g < C::G; ++g) sum[g] = warp_sum(q[2 * g] + q[2 * g + 1]);
-                if (lane == 0) {
-                    float *cc = cols + row * C::CS;
-                    const bool on = row_on(k, s.b, head, row);
-                    outs[row] = out_at(k, s.b, head, row);
-                    // takes the products back; kept where x c1 stays in fp32's range (beyond, one slot takes all as well)
-                    cc[0] = fminf(fmaxf(k.c2 * exp2f((float)(24 - up)), 1.2e-38f), 1.2e30f);
-                    cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + row) / k.group : INT_MAX);
-                    cc[2] = on ? 1.f : 0.f;
-#pragma unroll
-                    for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * 5.9604644775390625e-8f;   // 2^-24, as the products
-                }
-            }
-        }
-        __syncthreads();
         const bool two = LO && C::PARTS == 2 && k.a.q.dt == CS_F32;
-        float c1[C::NT][2], zq[C::NT][2][C::G];
+        float c1[C::NT][2], inv1[C::NT][2], zq[C::NT][2][C::G];
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float *cc = cols + (MODE == PACK4 ? (j & 1) * 2 + i : n * 8 + j * 2 + i) * C::CS;
                 c1[n][i] = cc[0];
+                inv1[n][i] = 1.f / cc[0];
 #pragma unroll
                 for (int g = 0; g < C::G; ++g) zq[n][i][g] = MODE == PACK4 && j >= 2 ? 0.f : cc[3 + g];
             }
         T.clear();
+        const int newest = by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + k.rows - 1) / k.group : 0;
         const int len = ax.len[s.b];
         float *lg = k.logit + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * k.area;
 
+        Seg nx = s;
+        bool last = s.next() >= ax.end;
+        if (!last) {
+            nx.template seek<C::UT>(ax, s.next(), s.b);
+            last = nx.u0 >= nx.u1;
+        }
+        const int nhead = last ? 0 : chosen_head(k, nx.b, nx.h);
+        bool asked = last;   // whether the next head's query rows are on their way: from the warp's last unit on
+
         for (int u = s.u0 + warp; u < s.u1; u += kWarps) {
+            if (!asked && u + kWarps >= s.u1) {
+                fetch_q(nx.b, nhead);
+                asked = true;
+            }
             __syncwarp();
             fetch_next();
             cp_async_wait<C::ST - 1>();
@@ -661,7 +730,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     lds_scales<C::G>(sb + C::UT * C::G * 4 + (sub * 16 + 8 * i + tok0) * C::G * 4, vs[sub][i]);
             // ---- what is not seen is -inf, and the value scales of slots that no row sees count as 0
             if (by_pos || (u + 1) * C::UT > len) {
-                const int newest = by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + k.rows - 1) / k.group : 0;
 #pragma unroll
                 for (int sub = 0; sub < C::SUB; ++sub)
 #pragma unroll
@@ -704,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 for (int q = 0; q < 2; ++q) {
                     mx[n][q] = fmaxf(x[0][n][q], x[0][n][2 + q]);
                     if (C::SUB == 2) mx[n][q] = fmaxf(mx[n][q], fmaxf(x[C::SUB - 1][n][q], x[C::SUB - 1][n][2 + q]));
-                    grow |= mx[n][q] > T.m[n][q];
+                    grow |= mx[n][q] > T.t[n][q];
                 }
             float vsc[C::SUB][2][C::G], top = 0.f;
 #pragma unroll
@@ -730,10 +798,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                         float m = fmaxf(mx[n][q], T.m[n][q]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                        // a column that need not move stays, and so do its sums
+                        m = m > T.t[n][q] ? m : T.m[n][q];
                         // nothing but zeros, or NaN, came before the first finite x
                         const float al = T.m[n][q] == -INFINITY ? 0.f : exp2_approx(fmaf(T.m[n][q] - m, c1[n][q], de));
                         T.m[n][q] = m;
                         T.ms[n][q] = m == -INFINITY ? 0.f : m;
+                        T.t[n][q] = fmaf(kLead, inv1[n][q], m);
                         T.l[n][q] *= al;
 #pragma unroll
                         for (int g = 0; g < C::G; ++g) T.z[g][n][q] *= al;
@@ -745,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     }
             }
             // ---- p, its sums, and p s as fragments
-            const float up = (float)(29 - T.e);
+            const float up = (float)(kUp - T.e);
 #pragma unroll
             for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -814,19 +885,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 }
         }
 
-        // ---- the next head's query rows, on their way while this one is finished
-        Seg nx = s;
-        int nhead = head;
-        bool last = s.next() >= ax.end;
         if (!last) {
-            nx.template seek<C::UT>(ax, s.next(), s.b);
-            last = nx.u0 >= nx.u1;
-            if (!last) {
-                nhead = chosen_head(k, nx.b, nx.h);
-                fetch_q(nx.b, nhead);
-            }
+            if (!asked) fetch_q(nx.b, nhead);
+            put_q(nx.b, nhead);
         }
-        // ---- the warps' sums become one
+        // ---- the warps' sums become one: each leaves its own in the stage of its ring that is free
+        const bool whole = s.whole();
+        float *rec = k.part + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * C::REC;
+        float *base = stat + 2 * kWarps * C::RP, *sum = base + C::RP, *cc1 = sum + C::RP;
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -843,32 +909,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     stat[(kWarps + warp) * C::RP + col] = T.l[n][q];
                 }
             }
-        if (lane == 0) wexp[warp] = T.e;
-        __syncthreads();
-        float *base = stat + 2 * kWarps * C::RP, *sum = base + C::RP, *cc1 = sum + C::RP;
-        if (tid < C::RP) {
-            float m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stat[w * C::RP + tid]);
-            const float at = m == -INFINITY ? 0.f : m, c = cols[tid * C::CS];
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(fmaf(stat[w * C::RP + tid] - at, c, (float)(wexp[w] - 29)));
-                stat[w * C::RP + tid] = f;
-                l = fmaf(f, stat[(kWarps + w) * C::RP + tid], l);
-            }
-            base[tid] = m;
-            // a row that is not asked for has no sum
-            sum[tid] = cols[tid * C::CS + 2] != 0.f ? l : 0.f;
-            cc1[tid] = c;
+        if (lane == 0) {
+            wexp[warp] = T.e;
+            woff[warp] = (warp * C::ST + fstage) * C::STAGE;
         }
-        const bool whole = s.whole();
-        float *rec = k.part + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * C::REC;
+        float *mine = reinterpret_cast<float *>(smem + (warp * C::ST + fstage) * C::STAGE);
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n) {
+        for (int pass = 0; pass < C::RP / C::CP; ++pass) {
+            if (pass > 0) __syncthreads();   // the last pass has been read
 #pragma unroll
-            for (int hf = 0; hf < (MODE == PACK4 ? 1 : 2); ++hf) {   // columns 4 hf .. 4 hf + 3 of the tile
-                float *mine = red + warp * 4 * C::RS;
+            for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                 for (int t = 0; t < C::G * 4; ++t) {
                     float v[4];
@@ -877,30 +927,55 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                         v[i] = T.o[t][n][i];
                         if (MODE == PACK4) v[i] += __shfl_xor_sync(kFull, v[i], 2);
                     }
-                    if (j >> 1 == hf) {
+                    const int col = n * 8 + 2 * j - pass * C::CP;   // the first of this lane's two columns
+                    if (col >= 0 && col < C::CP && (MODE != PACK4 || j < 2)) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
-                            *reinterpret_cast<float2 *>(mine + (2 * (j & 1) + q) * C::RS + t * 16 + r * 2) =
+                            *reinterpret_cast<float2 *>(mine + (col + q) * C::RS + t * 16 + r * 2) =
                                 make_float2(v[q] + T.z[t / 4][n][q], fmaf(v[2 + q], 0.0625f, T.z[t / 4][n][q]));
                     }
                 }
-                __syncthreads();
-                for (int i = tid; i < 4 * D; i += kThreads) {
-                    const int col = i / D, e = i % D, row = n * 8 + hf * 4 + col;
-                    float v = 0.f;
+            __syncthreads();
+            if (pass == 0) {
+                // a warp to a column, a lane to a warp's sums
+                for (int row = warp; row < C::RP; row += kWarps) {
+                    const float c = cols[row * C::CS];
+                    const float mw = lane < kWarps ? stat[lane * C::RP + row] : -INFINITY;
+                    float m = mw;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) v = fmaf(stat[w * C::RP + row], red[(w * 4 + col) * C::RS + e], v);
-                    const int ch = (e >> 6) * 64 + ((e >> 1) & 7) * 8 + ((e >> 4) & 3) * 2 + (e & 1);
-                    if (!whole) {
-                        rec[3 * C::RP + row * D + ch] = v;
-                    } else if (row < k.rows) {
-                        const float l = sum[row];
-                        q_store1(k.a.out, outs[row] + ch, l == 0.f ? 0.f : v / l);
+                    for (int o = 1; o < kWarps; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                    float l = 0.f;
+                    if (lane < kWarps) {
+                        const float f = exp2f(fmaf(mw - (m == -INFINITY ? 0.f : m), c, (float)(wexp[lane] - kUp)));
+                        stat[lane * C::RP + row] = f;
+                        l = f * stat[(kWarps + lane) * C::RP + row];
+                    }
+#pragma unroll
+                    for (int o = 1; o < kWarps; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+                    if (lane == 0) {
+                        base[row] = m;
+                        sum[row] = cols[row * C::CS + 2] != 0.f ? l : 0.f;   // a row that is not asked for has no sum
+                        cc1[row] = c;
                     }
                 }
                 __syncthreads();
             }
+            for (int i = tid; i < C::CP * D; i += kThreads) {
+                const int col = i / D, e = i % D, row = pass * C::CP + col;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    v = fmaf(stat[w * C::RP + row], reinterpret_cast<const float *>(smem + woff[w])[col * C::RS + e], v);
+                const int ch = (e >> 6) * 64 + ((e >> 1) & 7) * 8 + ((e >> 4) & 3) * 2 + (e & 1);
+                if (!whole) {
+                    rec[3 * C::RP + row * D + ch] = v;
+                } else if (row < k.rows) {
+                    const float l = sum[row];
+                    q_store1(k.a.out, out_row[row] + ch, l == 0.f ? 0.f : v / l);
+                }
+            }
         }
+        __syncthreads();   // the stages may be filled again
         if (!whole) {
             if (tid < 3 * C::RP) rec[tid] = base[tid];   // maximum, sum and c1 lie side by side
         } else if (weighing) {
@@ -914,6 +989,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
         if (last) break;
         s = nx;
         head = nhead;
+        turn();
         __syncthreads();
     }
 }

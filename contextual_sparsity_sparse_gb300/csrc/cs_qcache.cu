@@ -816,8 +816,9 @@ cs_status check_cache(const cs_qcache *q, bool codes, const char *who, QCacheK *
     return CS_OK;
 }
 
-cs_status check_rows(const cs_head_rows *r, const char *name, const char *who, QRowsK *out) {
-    CS_CHECK(r && r->data, "%s: %s is null", who, name);
+// empty: no tokens, so no data
+cs_status check_rows(const cs_head_rows *r, bool empty, const char *name, const char *who, QRowsK *out) {
+    CS_CHECK(r && (r->data || empty), "%s: %s is null", who, name);
     CS_CHECK(r->dtype == CS_F32 || r->dtype == CS_F16 || r->dtype == CS_BF16, "%s: %s has a bad dtype %d", who, name, (int)r->dtype);
     const int es = (int)dtype_size(r->dtype);
     CS_CHECK(aligned(r->data, es), "%s: %s must be aligned to its elements", who, name);
@@ -871,8 +872,8 @@ dim3 rows_grid(const QRowsCall &a, int each) {
 cs_status rows_call(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n, const int32_t *start,
                     const int32_t *slots, void *ws, size_t ws_bytes, const char *who, QRowsCall *a) {
     cs_status st = check_cache(cache, true, who, &a->c);
-    if (st == CS_OK) st = check_rows(k, "k", who, &a->k);
-    if (st == CS_OK) st = check_rows(v, "v", who, &a->v);
+    if (st == CS_OK) st = check_rows(k, n == 0, "k", who, &a->k);
+    if (st == CS_OK) st = check_rows(v, n == 0, "v", who, &a->v);
     if (st != CS_OK) return st;
     CS_CHECK(k->dtype == v->dtype, "%s: k and v differ in dtype", who);
     CS_CHECK(n >= 0 && n <= kMaxTokens, "%s: n=%d outside [0, %d]", who, n, kMaxTokens);
@@ -955,11 +956,11 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
     const char *who = "cs_qcache_attention";
     QAttnArgs a;
     cs_status st = check_cache(cache, true, who, &a.c);
-    if (st == CS_OK) st = check_rows(q, "q", who, &a.q);
-    if (st == CS_OK) st = check_rows(out, "out", who, &a.out);
+    if (st == CS_OK) st = check_rows(q, n_q == 0, "q", who, &a.q);
+    if (st == CS_OK) st = check_rows(out, n_q == 0, "out", who, &a.out);
     if (st != CS_OK) return st;
     CS_CHECK(q->dtype == out->dtype, "%s: q and out differ in dtype", who);
-    CS_CHECK(q->data != out->data, "%s: out must not be q", who);
+    CS_CHECK(n_q == 0 || q->data != out->data, "%s: out must not be q", who);
     CS_CHECK(n_heads >= 1 && n_heads % cache->n_heads == 0, "%s: n_heads=%d is not a multiple of the cache's %d", who, n_heads,
              cache->n_heads);
     CS_CHECK(n_q >= 0, "%s: n_q=%d is negative", who, n_q);

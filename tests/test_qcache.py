@@ -66,6 +66,21 @@ def test_append_and_read_refusals(lib, change, status):
                                   None) == status
 
 
+def test_calls_without_tokens_do_nothing(lib):
+    none = rows(None)
+    assert lib.cs_qcache_append(ref_(cache()), ref_(none), ref_(none), 0, P, None, None, P, P, 1 << 20, None) == 0
+    assert lib.cs_qcache_read(ref_(cache()), ref_(none), ref_(none), 0, None, P, P, 1 << 20, None) == 0
+    assert lib.cs_qcache_attention(ref_(cache()), ref_(none), 8, 0, P, None, None, 0.0, 1.0, None, ref_(none), P, 1 << 30, None) == 0
+
+
+@pytest.mark.parametrize("groups,good,bad", [(1, 4, 2), (2, 8, 4), (3, 4, 2), (4, 16, 8)])
+def test_scales_are_aligned_to_what_is_copied_of_a_slot(lib, groups, good, bad):
+    for at, status in ((good, 0), (bad, INVALID)):
+        c = cache(d_head=64 * groups, ks=P + at)
+        r = rows(None)
+        assert lib.cs_qcache_read(ref_(c), ref_(r), ref_(r), 0, P, None, P, 1 << 20, None) == status
+
+
 def test_append_wants_positions_exactly_when_the_cache_has_them(lib):
     r = rows()
     assert lib.cs_qcache_append(ref_(cache(pos=None)), ref_(r), ref_(r), 1, P, None, None, P, P, 1 << 20, None) == INVALID
