@@ -20,38 +20,33 @@ int64_t units_of(int cap, int d) { return (cap + unit_of(d) - 1) / unit_of(d); }
 // The longest that a call's split axis can be.
 int64_t cost_of(int batch, int kv_heads, int cap, int d) { return (int64_t)batch * kv_heads * (units_of(cap, d) + kHeadCost); }
 
-// Floats of a CTA's half of the logits: the units of its part of the axis (with
-// one CTA per SM at the least), or a whole head's if that is less.
-int64_t area_floats(int batch, int kv_heads, int cap, int d, int rows, int sms) {
-    const int64_t part = cost_of(batch, kv_heads, cap, d) / (sms > 0 ? sms : 1) + 1 + kWarps + kHeadCost;
-    const int64_t head = units_of(cap, d);
-    return (part < head ? part : head) * unit_of(d) * cols_of(rows);
-}
-
-size_t part_bytes(int d, int rows, int sms) {
-    return align256((size_t)2 * (sms > 0 ? sms : 1) * 2 * cols_of(rows) * (d + 3) * sizeof(float));
+int ctas_of(int sms) { return kMaxPerSm * (sms > 0 ? sms : 1); }
+size_t left_bytes(int sms) { return align256((size_t)ctas_of(sms) * 4 * sizeof(int4)); }
+size_t part_bytes(int d, int rows, int sms) { return align256((size_t)ctas_of(sms) * 2 * cols_of(rows) * (d + 3) * sizeof(float)); }
+// Two areas per CTA for the units of its part of the split axis (at least kWarps).
+size_t logit_bytes(int64_t cost, int d, int rows, int sms) {
+    return align256((size_t)2 * (cost + (int64_t)ctas_of(sms) * (kWarps + 1)) * unit_of(d) * cols_of(rows) * sizeof(float));
 }
 
 }  // namespace
 
 size_t qattn_scratch(int batch, int kv_heads, int cap, int d, int heads, int n_q, int sms) {
     const int rows = heads / kv_heads * n_q;
-    return part_bytes(d, rows, sms) +
-           align256((size_t)2 * (sms > 0 ? sms : 1) * 2 * area_floats(batch, kv_heads, cap, d, rows, sms) * sizeof(float));
+    return left_bytes(sms) + part_bytes(d, rows, sms) + logit_bytes(cost_of(batch, kv_heads, cap, d), d, rows, sms);
 }
 
 cudaError_t launch_qattn(const QAttnArgs &a, cudaStream_t s) {
-    QAttnK k{a, a.heads / a.c.heads, 0, 0, 0, nullptr, nullptr, 0, (a.scale < 0 ? -a.scale : a.scale) * 1.44269504088896341f,
+    QAttnK k{a, a.heads / a.c.heads, 0, 0, 0, 0, nullptr, nullptr, nullptr, 0, (a.scale < 0 ? -a.scale : a.scale) * 1.44269504088896341f,
              a.scale < 0 ? -1.f : 1.f};
     const int rows = k.group * a.n_q, d = a.c.d;
-    k.part = reinterpret_cast<float *>(a.scratch);
-    k.logit = reinterpret_cast<float *>(a.scratch + part_bytes(d, rows, a.sms));
+    k.left = reinterpret_cast<int4 *>(a.scratch);
+    k.part = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms));
+    k.logit = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms) + part_bytes(d, rows, a.sms));
     const int64_t cost = cost_of(a.c.batch, a.c.heads, a.c.cap, d);
     const bool lo = a.q.dt != CS_BF16;
     // a later pass adds its weights to an earlier one's
     for (k.row0 = 0; k.row0 < rows; k.row0 += kPass) {
         k.rows = rows - k.row0 < kPass ? rows - k.row0 : kPass;
-        k.area = area_floats(a.c.batch, a.c.heads, a.c.cap, d, k.rows, a.sms);
         if (k.row0 > 0 && a.weight) {
             k.a.decay = 1.f;
             k.a.c.weight = a.weight;

@@ -17,7 +17,8 @@
 // asynchronous copies, which runs on across heads; at a head's end the warps'
 // sums are joined.  A head that lies in one CTA is finished there; else the CTA
 // leaves a partial record, and the second kernel joins the records and
-// finishes (with the same split, every CTA a share of the record sums).
+// finishes (for every CTA of the first a few small ones, so that uneven
+// leavings even out; each adds up a share of the records' sums and of the weights).
 // Starting and joining a head costs a CTA about as long as kHeadCost units, so
 // a head is that much longer on the axis.
 //
@@ -45,13 +46,16 @@ namespace cs {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxPerSm = 2;   // CTAs of the first kernel
 constexpr int kHeadCost = 24;
 
 struct QAttnK {
     QAttnArgs a;
     int group, rows;     // query heads per cache head; rows of this pass
     int row0;            // its first row: row r is head r % group of the group, token r / group
-    int grid;            // CTAs of both kernels
+    int grid;            // CTAs of the first kernel
+    int subs;            // CTAs of the second kernel for each of them
+    int4 *left;          // [grid, 2, 2] what the first kernel left to finish (Left)
     float *part;         // [grid, 2] records: per column its maximum, sum and c1, then the sums of p v
     float *logit;        // [grid, 2, area / RP, RP] x, for the weights
     int64_t area;        // floats of one CTA's half of logit
@@ -79,7 +83,7 @@ struct Cfg {
     static constexpr int SUB = UT / 16;
     static constexpr int RB = D / 2;                         // bytes of a row
     static constexpr int STAGE = UT * (2 * RB + 8 * G + 4);  // one unit: keys, values, their scales, positions
-    static constexpr int MINB = D * NT <= 128 ? 2 : 1;       // CTAs per SM
+    static constexpr int MINB = D * NT <= 128 ? kMaxPerSm : 1;   // CTAs per SM
     static constexpr int ST = D == 64 ? 4 : MINB == 2 ? 2 : 3;
     static constexpr int RS = D + 4;                         // floats of a joined column (conflict-free)
     static constexpr int QF = NT * PARTS * (D / 32) * 32;    // uint4 fragments of q, two products each
@@ -328,7 +332,7 @@ __device__ __forceinline__ int64_t out_at(const QAttnK &k, int b, int head, int 
 
 // The weights of n slots from slot0 on, from the x that were left at lg: RP / 4
 // threads to a slot, each four columns.  base, c1, inv: per column.
-template <int RP>
+template <int RP, int U, bool AHEAD>
 __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, int64_t slot0, const float *base, const float *c1,
                                       const float *inv) {
     constexpr int L = RP / 4;
@@ -340,9 +344,9 @@ __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, i
         cc[i] = c1[c + i];
         ii[i] = inv[c + i];
     }
-    // whole warps go round, so that the shuffles have all their lanes; the next round's loads are under way while
-    // this one is worked on and stored
-    constexpr int U = 8, STEP = kThreads / L;
+    // U slots a round, loads first (the compiler may not move them over stores); whole warps go round, so that the
+    // shuffles have all their lanes.  AHEAD: the next round's loads are under way while this one is worked on.
+    constexpr int STEP = kThreads / L;
     struct Round {
         float4 x[U];
         float old[U];
@@ -360,10 +364,11 @@ __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, i
         }
     };
     Round now, next;
-    load(now, 0);
+    if (AHEAD) load(now, 0);
 #pragma unroll 1
     for (int t0 = 0; t0 < n; t0 += U * STEP) {
-        load(next, t0 + U * STEP);
+        if (AHEAD) load(next, t0 + U * STEP);
+        else load(now, t0);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int t = t0 + i * STEP + threadIdx.x / L;
@@ -375,7 +380,7 @@ __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, i
             for (int o = 1; o < L; o <<= 1) w += __shfl_xor_sync(kFull, w, o);
             if (t < n && c == 0) k.a.weight[slot0 + t] = fmaf(k.a.decay, now.old[i], w);
         }
-        now = next;
+        if (AHEAD) now = next;
     }
 }
 
@@ -488,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
     const QCacheK &c = k.a.c;
     pdl_wait();
     pdl_launch_dependents();
+    if (tid < 2) k.left[blockIdx.x * 4 + tid] = k.left[blockIdx.x * 4 + 2 + tid] = make_int4(0, 0, 0, 0);
     Axis ax{};
     ax.build<C::UT>(k, axis_mem, wsum, blockIdx.x == 0);
     if (ax.begin >= ax.end) return;
@@ -978,13 +984,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
         __syncthreads();   // the stages may be filled again
         if (!whole) {
             if (tid < 3 * C::RP) rec[tid] = base[tid];   // maximum, sum and c1 lie side by side
+            if (tid < 2) {
+                // by the threads that cleared the entry
+                const int p0 = s.first / ax.per;
+                k.left[blockIdx.x * 4 + 2 * (s.u0 == 0) + tid] =
+                    tid == 0 ? make_int4(s.b, head, s.u0 * C::UT, min(len, s.u1 * C::UT))
+                             : make_int4(p0, (s.first + s.nu - 1) / ax.per - p0 + 1, 0, 0);
+            }
         } else if (weighing) {
             if (tid < C::RP) {
                 base[tid] = base[tid] == -INFINITY ? 0.f : base[tid];
                 sum[tid] = sum[tid] == 0.f ? 0.f : 1.f / sum[tid];
             }
             __syncthreads();
-            weigh<C::RP>(k, lg, len, c.slot0(s.b, head), base, cc1, sum);
+            weigh<C::RP, 8, true>(k, lg, len, c.slot0(s.b, head), base, cc1, sum);
         }
         if (last) break;
         s = nx;
@@ -996,101 +1009,125 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
 
 // ------------------------------------------------------------ second kernel
 
+// What a CTA of the first kernel left of a head that others have parts of, too.
+struct Left {
+    int b, head, t0, t1;   // its slots [t0, t1)
+    int p0, n;             // the head's n records (0: nothing left) are of CTAs p0, p0 + 1, ...
+};
+
 // Finishes the heads that lie in more than one CTA, and writes what no CTA came
 // by: zero rows (and decayed weights) of empty sequences and heads not chosen.
+// A CTA has up to two heads of one CTA of the first kernel, and a share of each.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads) qattn_join_kernel(QAttnK k) {
+__global__ void __launch_bounds__(kThreads, 4) qattn_join_kernel(QAttnK k) {
     using C = Cfg<D, MODE>;
-    extern __shared__ __align__(16) int axis_mem[];
-    __shared__ int wsum[32];
-    __shared__ float base[C::RP], inv[C::RP], cc1[C::RP];
+    constexpr int RP = C::RP, REC = C::REC;
+    extern __shared__ __align__(16) float factor[];   // [2, grid, RP]
+    __shared__ float base[2][RP], inv[2][RP], cc1[2][RP];
     __shared__ float red[kThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x / k.subs, sub = blockIdx.x % k.subs;
     const QCacheK &c = k.a.c;
-    float *factor = reinterpret_cast<float *>(axis_mem + 2 * c.batch + 1);   // [records, RP]
     pdl_wait();
     pdl_launch_dependents();
-    Axis ax{};
-    ax.build<C::UT>(k, axis_mem, wsum, false);
-    if (ax.begin < ax.end) {
-        Seg s{};
-        s.template seek<C::UT>(ax, ax.begin, first_seq(ax, c.batch, ax.begin));
-        for (;;) {
-            if (s.u0 < s.u1 && !s.whole()) {
-                const int head = chosen_head(k, s.b, s.h);
-                const int p0 = s.first / ax.per, n = (s.first + s.nu - 1) / ax.per - p0 + 1;
-                auto rec = [&](int p) { return k.part + ((int64_t)(p0 + p) * 2 + (p == 0)) * C::REC; };
-                // a warp to a column: its base and sum over the n records
-                for (int row = warp; row < C::RP; row += kWarps) {
-                    float m = -INFINITY, l = 0.f;
-                    for (int p = lane; p < n; p += 32) m = fmaxf(m, ld_dep(rec(p) + row));
+    Left s[2];
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                    if (m == -INFINITY) m = 0.f;
-                    const float c = ld_dep(rec(0) + 2 * C::RP + row);
-                    for (int p = lane; p < n; p += 32) {
-                        const float f = exp2f((ld_dep(rec(p) + row) - m) * c);
-                        factor[p * C::RP + row] = f;
-                        l = fmaf(f, ld_dep(rec(p) + C::RP + row), l);
-                    }
-                    l = warp_sum(l);
-                    if (lane == 0) {
-                        base[row] = m;
-                        inv[row] = l == 0.f ? 0.f : 1.f / l;
-                        cc1[row] = c;
-                    }
+    for (int i = 0; i < 2; ++i) {
+        const int4 x = ld_dep(k.left + cta * 4 + 2 * i), y = ld_dep(k.left + cta * 4 + 2 * i + 1);
+        s[i] = Left{x.x, x.y, x.z, x.w, y.x, y.y};
+    }
+    // the heads that no CTA came by, of this CTA's share of all
+    const int64_t heads = (int64_t)c.batch * c.heads, each = (heads + gridDim.x - 1) / gridDim.x;
+    const int64_t h0 = min(heads, blockIdx.x * each), h1 = min(heads, h0 + each);
+    auto idle = [&](int64_t i) {
+        const int b = (int)(i / c.heads), n = ld_dep(k.a.length + b);
+        return n <= 0 || !kv_on(k, b, (int)(i % c.heads));
+    };
+    bool some = false;
+    for (int64_t i = h0 + tid; i < h1; i += kThreads) some |= idle(i);
+    if (__syncthreads_or(some)) {
+        for (int64_t i = h0; i < h1; ++i) {
+            if (!idle(i)) continue;
+            const int b = (int)(i / c.heads), h = (int)(i % c.heads);
+            for (int e = tid; e < k.rows * D; e += kThreads) q_store1(k.a.out, out_at(k, b, h, e / D) + e % D, 0.f);
+            if (k.a.weight)
+                for (int e = tid; e < q_length(k.a.length, b, c.cap, nullptr); e += kThreads) {
+                    const int64_t slot = c.slot0(b, h) + e;
+                    k.a.weight[slot] = k.a.decay == 0.f ? 0.f : k.a.decay * ld_dep(c.weight + slot);
                 }
-                __syncthreads();
-                // this CTA's share of the output values: many records are added up by 8 warps, few by one thread
-                const int mine = blockIdx.x - p0, total = k.rows * D;
-                const int e0 = (int)((int64_t)total * mine / n), e1 = (int)((int64_t)total * (mine + 1) / n);
-                if (n > kWarps) {
-                    for (int i0 = e0; i0 < e1; i0 += 32) {
-                        const int i = i0 + lane;
-                        float v = 0.f;
-                        if (i < e1) {
-#pragma unroll 4
-                            for (int p = warp; p < n; p += kWarps) v = fmaf(factor[p * C::RP + i / D], ld_dep(rec(p) + 3 * C::RP + i), v);
-                        }
-                        red[tid] = v;
-                        __syncthreads();
-                        if (warp == 0 && i < e1) {
-                            v = 0.f;
-#pragma unroll
-                            for (int w = 0; w < kWarps; ++w) v += red[w * 32 + lane];
-                            q_store1(k.a.out, out_at(k, s.b, head, i / D) + i % D, v * inv[i / D]);
-                        }
-                        __syncthreads();
-                    }
-                } else {
-                    for (int i = e0 + tid; i < e1; i += kThreads) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int p = 0; p < kWarps; ++p)
-                            if (p < n) v = fmaf(factor[p * C::RP + i / D], ld_dep(rec(p) + 3 * C::RP + i), v);
-                        q_store1(k.a.out, out_at(k, s.b, head, i / D) + i % D, v * inv[i / D]);
-                    }
-                }
-                if (k.a.weight) {
-                    const int t0 = s.u0 * C::UT, t1 = min(ax.len[s.b], s.u1 * C::UT);
-                    weigh<C::RP>(k, k.logit + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * k.area, t1 - t0, c.slot0(s.b, head) + t0, base,
-                                 cc1, inv);
-                }
-                __syncthreads();
-            }
-            if (s.next() >= ax.end) break;
-            s.template seek<C::UT>(ax, s.next(), s.b);
         }
     }
-    for (int64_t i = blockIdx.x; i < (int64_t)c.batch * c.heads; i += gridDim.x) {
-        const int b = (int)(i / c.heads), h = (int)(i % c.heads);
-        if (ax.len[b] > 0 && kv_on(k, b, h)) continue;
-        for (int e = tid; e < k.rows * D; e += kThreads) q_store1(k.a.out, out_at(k, b, h, e / D) + e % D, 0.f);
-        if (k.a.weight)
-            for (int e = tid; e < ax.len[b]; e += kThreads) {
-                const int64_t slot = c.slot0(b, h) + e;
-                k.a.weight[slot] = k.a.decay == 0.f ? 0.f : k.a.decay * ld_dep(c.weight + slot);
+    if (s[0].n == 0 && s[1].n == 0) return;
+    auto rec = [&](const Left &x, int p) { return k.part + ((int64_t)(x.p0 + p) * 2 + (p == 0)) * REC; };
+    // a warp to a column of a head: its maximum and sum over the n records
+    for (int i = warp; i < 2 * RP; i += kWarps) {
+        const Left x = i < RP ? s[0] : s[1];
+        const int row = i % RP, n = x.n;
+        float *f = factor + (int64_t)(i / RP) * k.grid * RP + row;
+        if (n == 0) continue;
+        const float c1 = ld_dep(rec(x, 0) + 2 * RP + row);
+        float m = lane < n ? ld_dep(rec(x, lane) + row) : -INFINITY, l = lane < n ? ld_dep(rec(x, lane) + RP + row) : 0.f;
+        const float m0 = m, l0 = l;
+        for (int p = lane + 32; p < n; p += 32) m = fmaxf(m, ld_dep(rec(x, p) + row));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        if (m == -INFINITY) m = 0.f;
+        const float g0 = exp2f((m0 - m) * c1);
+        if (lane < n) f[lane * RP] = g0;
+        l = lane < n ? g0 * l0 : 0.f;
+        for (int p = lane + 32; p < n; p += 32) {
+            const float g = exp2f((ld_dep(rec(x, p) + row) - m) * c1);
+            f[p * RP] = g;
+            l = fmaf(g, ld_dep(rec(x, p) + RP + row), l);
+        }
+        l = warp_sum(l);
+        if (lane == 0) {
+            base[i / RP][row] = m;
+            inv[i / RP][row] = l == 0.f ? 0.f : 1.f / l;
+            cc1[i / RP][row] = c1;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Left &x = s[i];
+        if (x.n == 0) continue;
+        const float *f = factor + (int64_t)i * k.grid * RP;
+        // this CTA's share of the output values: many records are added up by 8 warps, few by one thread
+        const int64_t total = k.rows * D, part = (int64_t)(cta - x.p0) * k.subs + sub, parts = (int64_t)x.n * k.subs;
+        const int e0 = (int)(total * part / parts), e1 = (int)(total * (part + 1) / parts);
+        if (x.n > kWarps) {
+            for (int a = e0; a < e1; a += 32) {
+                const int e = a + lane;
+                float v = 0.f;
+                if (e < e1) {
+#pragma unroll 4
+                    for (int p = warp; p < x.n; p += kWarps) v = fmaf(f[p * RP + e / D], ld_dep(rec(x, p) + 3 * RP + e), v);
+                }
+                red[tid] = v;
+                __syncthreads();
+                if (warp == 0 && e < e1) {
+                    v = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) v += red[w * 32 + lane];
+                    q_store1(k.a.out, out_at(k, x.b, x.head, e / D) + e % D, v * inv[i][e / D]);
+                }
+                __syncthreads();
             }
+        } else {
+            for (int e = e0 + tid; e < e1; e += kThreads) {
+                float v = 0.f;
+#pragma unroll
+                for (int p = 0; p < kWarps; ++p)
+                    if (p < x.n) v = fmaf(f[p * RP + e / D], ld_dep(rec(x, p) + 3 * RP + e), v);
+                q_store1(k.a.out, out_at(k, x.b, x.head, e / D) + e % D, v * inv[i][e / D]);
+            }
+        }
+        if (k.a.weight) {
+            const int n = x.t1 - x.t0, a0 = (int)((int64_t)n * sub / k.subs), a1 = (int)((int64_t)n * (sub + 1) / k.subs);
+            weigh<RP, 4, false>(k, k.logit + ((int64_t)cta * 2 + i) * k.area + (int64_t)a0 * RP, a1 - a0,
+                                c.slot0(x.b, x.head) + x.t0 + a0, base[i], cc1[i], inv[i]);
+        }
     }
 }
 
@@ -1099,16 +1136,23 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     using C = Cfg<D, MODE>;
     const size_t axis = (2 * (size_t)k.a.c.batch + 1) * sizeof(int), smem = C::smem_fixed + axis;
     static_assert(C::smem_fixed + (2 * kQMaxBatch + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
-    int64_t grid = (int64_t)k.a.sms * (smem <= 112 * 1024 ? C::MINB : 1);
-    if (grid < 1) grid = 1;
+    // 228 KB per SM, of which 1 KB per CTA and its static variables are spoken for
+    const int fit = (int)(228 * 1024 / (smem + 2048));
+    const int64_t grid = (int64_t)(k.a.sms > 0 ? k.a.sms : 1) * (fit < C::MINB ? fit : C::MINB);
     const int64_t most = (cost + kWarps - 1) / kWarps;
     k.grid = (int)(most < grid ? most : grid);
-    const size_t join = axis + (size_t)k.grid * C::RP * sizeof(float);
+    // the longest part that a CTA can have, or a whole head, in x
+    int64_t part = (cost + k.grid - 1) / k.grid;
+    if (part < kWarps) part = kWarps;
+    const int64_t head = (k.a.c.cap + C::UT - 1) / C::UT;
+    k.area = (part < head ? part : head) * C::UT * C::RP;
+    const size_t join = 2 * (size_t)k.grid * C::RP * sizeof(float);
+    k.subs = 2;   // one wave of four per SM (64 ragged sequences of up to 8,192 slots: 108, 101, 104 us with 1, 2, 3)
     cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && join > 48 * 1024)
         e = cudaFuncSetAttribute(qattn_join_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join);
     if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, LO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
-    if (e == cudaSuccess) e = launch(qattn_join_kernel<D, MODE>, dim3(k.grid), dim3(kThreads), join, s, pdl_enabled(), k);
+    if (e == cudaSuccess) e = launch(qattn_join_kernel<D, MODE>, dim3(k.grid * k.subs), dim3(kThreads), join, s, pdl_enabled(), k);
     return e;
 }
 
