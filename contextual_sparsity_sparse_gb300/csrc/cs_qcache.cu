@@ -513,7 +513,8 @@ __device__ uint4 reduce_stat(EvictShared<T> &sh, cg::cluster_group &cl, uint32_t
 }
 
 template <int T, int K>
-__global__ void __launch_bounds__(T) qevict_kernel(QEvictCall a) {
+// Two CTAs of 512 per SM (512 rows of 8,192 slots: 12.0 us; with registers for one 16.2, for three, spilling, 13.0).
+__global__ void __launch_bounds__(T, 1024 / T) qevict_kernel(QEvictCall a) {
     __shared__ EvictShared<T> sh;
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
