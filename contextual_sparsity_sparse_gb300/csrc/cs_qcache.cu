@@ -969,7 +969,7 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
         set_error("%s: %d query rows per cache head, above %d", who, n_heads / cache->n_heads * n_q, kQMaxRows);
         return CS_ERR_UNSUPPORTED;
     }
-    if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16 + 16) >= INT32_MAX) {
+    if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16 + 32) >= INT32_MAX) {
         set_error("%s: batch x n_heads x capacity is too large", who);
         return CS_ERR_UNSUPPORTED;
     }

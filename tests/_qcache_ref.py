@@ -37,7 +37,7 @@ def attention(k, ks, v, vs, pos, q, length, q_pos=None, on=None, scale=0.0, old=
     """(out, its error bound per unit step, weight, its error bound).  k..pos are the cache's arrays, q [B, n_q, H, d];
     on: bool [B, H].  The bounds add, for every row, the first-order effect of
 
-      - a logit error of at most 2^-18 A, A = scale sum |q| (|offset| + s code): q in two fp16 parts (2^-22), products exact,
+      - a logit error of at most 2^-18 A, A = |scale| sum |q| (|offset| + s code): q in two fp16 parts (2^-22), products exact,
         sums of 16 channels whose partial sums may be cut off (2^-22 of their size, 4 chains of 4), a handful of fp32
         roundings, the exponent's argument in fp32;
       - 2^-18 for p, its two fp16 parts, the exponential and the division;
@@ -68,7 +68,7 @@ def attention(k, ks, v, vs, pos, q, length, q_pos=None, on=None, scale=0.0, old=
                         continue
                     x = q[b, t, j].double()
                     s = sc * (kk[ok] @ x)
-                    delta = 2.0 ** -18 * (sc * (ka[ok] @ x.abs())).max()
+                    delta = 2.0 ** -18 * (abs(sc) * (ka[ok] @ x.abs())).max()
                     e = torch.exp(s - s.max())
                     p = e / e.sum()
                     rel = 2 * delta + 2.0 ** -18 + n / 16 * 2.0 ** -23

@@ -269,6 +269,42 @@ def test_attention_of_chosen_heads(group):
     assert not out[1].any() and torch.equal(w[1].cpu(), cpu[4][1])
 
 
+@pytest.mark.parametrize("B,kv,group", [(3, 40, 1), (40, 5, 3), (34, 33, 2)])
+def test_attention_of_few_chosen_heads_of_many(B, kv, group):
+    """More cache heads and more sequences than a warp has lanes; most heads are not read, some sequences are empty."""
+    S, d = 37, 64
+    g = gen(B, kv, group)
+    cache, cpu = filled(B, kv, S, d, g)
+    on = torch.rand(B, kv * group, generator=g) < 0.1
+    on[1] = False
+    length = torch.randint(0, S + 1, (B,), generator=g)
+    length[2] = 0
+    attend(cache, cpu, some_q(B, 1, kv * group, d, torch.float32, g), length.tolist(), on=on, decay=0.5)
+
+
+@pytest.mark.parametrize("scale", [0.3, -0.2, 1e-6])
+def test_attention_scale(scale):
+    g = gen(19)
+    cache, cpu = filled(2, 2, 130, 64, g)
+    attend(cache, cpu, some_q(2, 1, 6, 64, torch.float32, g), [130, 66], scale=scale)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("group", [2, 8, 12])
+def test_attention_rising_and_falling_logits(d, group):
+    """Slots in the order of their logits, up for one sequence and down for the other, steep enough that the running
+    maxima move in every unit, or never after the first."""
+    S = 700
+    g = gen(d, group, 20)
+    cache, cpu = filled(2, 1, S, d, g)
+    ramp = torch.linspace(-30, 30, S)[:, None] * torch.ones(d) / d
+    k, ks = ref.quantise(torch.stack([ramp, ramp.flip(0)])[:, None] + 0.01 * torch.randn(2, 1, S, d, generator=g))
+    cache.k.copy_(k)
+    cache.k_scale.copy_(ks)
+    q = 1.0 + 0.1 * torch.rand(2, 1, group, d, generator=g)
+    attend(cache, (k, ks) + tuple(cpu[2:]), q, [S, S], scale=1.0)
+
+
 def test_attention_length_out_of_range_is_clamped_and_flagged():
     g = gen(10)
     cache, cpu = filled(2, 1, 20, 64, g)
