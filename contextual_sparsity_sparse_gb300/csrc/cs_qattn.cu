@@ -4,10 +4,10 @@
 
 namespace cs {
 
-extern template cudaError_t run_qattn<64>(QAttnK, int, bool, int64_t, cudaStream_t);
-extern template cudaError_t run_qattn<128>(QAttnK, int, bool, int64_t, cudaStream_t);
-extern template cudaError_t run_qattn<192>(QAttnK, int, bool, int64_t, cudaStream_t);
-extern template cudaError_t run_qattn<256>(QAttnK, int, bool, int64_t, cudaStream_t);
+extern template cudaError_t run_qattn<64>(QAttnK, int, int64_t, cudaStream_t);
+extern template cudaError_t run_qattn<128>(QAttnK, int, int64_t, cudaStream_t);
+extern template cudaError_t run_qattn<192>(QAttnK, int, int64_t, cudaStream_t);
+extern template cudaError_t run_qattn<256>(QAttnK, int, int64_t, cudaStream_t);
 
 namespace {
 
@@ -43,7 +43,6 @@ cudaError_t launch_qattn(const QAttnArgs &a, cudaStream_t s) {
     k.part = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms));
     k.logit = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms) + part_bytes(d, rows, a.sms));
     const int64_t cost = cost_of(a.c.batch, a.c.heads, a.c.cap, d);
-    const bool lo = a.q.dt != CS_BF16;
     // a later pass adds its weights to an earlier one's
     for (k.row0 = 0; k.row0 < rows; k.row0 += kPass) {
         k.rows = rows - k.row0 < kPass ? rows - k.row0 : kPass;
@@ -52,10 +51,10 @@ cudaError_t launch_qattn(const QAttnArgs &a, cudaStream_t s) {
             k.a.c.weight = a.weight;
         }
         const int mode = mode_of(k.rows);
-        const cudaError_t e = d == 64    ? run_qattn<64>(k, mode, lo, cost, s)
-                              : d == 128 ? run_qattn<128>(k, mode, lo, cost, s)
-                              : d == 192 ? run_qattn<192>(k, mode, lo, cost, s)
-                                         : run_qattn<256>(k, mode, lo, cost, s);
+        const cudaError_t e = d == 64    ? run_qattn<64>(k, mode, cost, s)
+                              : d == 128 ? run_qattn<128>(k, mode, cost, s)
+                              : d == 192 ? run_qattn<192>(k, mode, cost, s)
+                                         : run_qattn<256>(k, mode, cost, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

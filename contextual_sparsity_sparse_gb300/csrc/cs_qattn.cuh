@@ -76,9 +76,9 @@ struct QAttnK {
 // Query columns per pass and how they sit in the 8 columns of a product.
 enum QMode { PACK4 = 0, ONE8 = 1, TWO8 = 2 };
 
-// The launchers of one d_head (mode, whether p s and q have second parts).
+// Launches both kernels of one d_head.
 template <int D>
-cudaError_t run_qattn(QAttnK k, int mode, bool lo, int64_t cost, cudaStream_t s);
+cudaError_t run_qattn(QAttnK k, int mode, int64_t cost, cudaStream_t s);
 
 #ifdef CS_QATTN_KERNELS
 
@@ -484,8 +484,8 @@ __device__ __forceinline__ void fetch(const QAttnK &k, uint32_t stage, int64_t s
         cp_async_or0<4>(stage + C::UT * (2 * C::RB + C::G * 8) + lane * 4, lane < n ? c.pos + slot0 + lane : c.pos, lane < n);
 }
 
-// LO: p s has a second fp16 part (always so in PACK4).
-template <int D, int MODE, bool LO>
+// LO: p s has a second fp16 part (always so in PACK4).  TWO: q has one, too, and sums are kept to fp32's precision.
+template <int D, int MODE, bool LO, bool TWO>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAttnK k) {
     using C = Cfg<D, MODE>;
     extern __shared__ __align__(16) char smem[];
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 };
                 put(nt * C::PARTS, col, hi);
                 if (C::PARTS == 1) put(0, col + 4, lo);
-                else if (LO) put(nt * 2 + 1, col, lo);
+                else if (TWO) put(nt * 2 + 1, col, lo);
             }
             float sum[C::G];
 #pragma unroll
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
     turn();
     __syncthreads();
     for (;;) {
-        const bool two = LO && C::PARTS == 2 && k.a.q.dt == CS_F32;
+        constexpr bool two = TWO && C::PARTS == 2;
         float c1[C::NT][2], inv1[C::NT][2], zq[C::NT][2][C::G];
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
@@ -846,60 +846,102 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                             v = exp2_approx(fmaf(v - T.ms[n][q], c1[n][q], up));
                             T.l[n][q] += v;
                         }
+            // p s of one group and 16 slots as fragments; LO: in two parts
+            auto weights = [&](int g, int sub, uint32_t (&ph)[C::NT][2], uint32_t (&pl)[C::NT][2]) {
 #pragma unroll
-            for (int g = 0; g < C::G; ++g)
+                for (int i = 0; i < 2; ++i) {
+                    const float sc = vsc[sub][i][g];
+                    const float zo = fmaf(8.f, sc, __half2float(__ushort_as_half((unsigned short)(vs[sub][i][g] >> 16))));
 #pragma unroll
-                for (int sub = 0; sub < C::SUB; ++sub) {
-                    uint32_t ph[C::NT][2], pl[C::NT][2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float sc = vsc[sub][i][g];
-                        const float zo = fmaf(8.f, sc, __half2float(__ushort_as_half((unsigned short)(vs[sub][i][g] >> 16))));
-#pragma unroll
-                        for (int n = 0; n < C::NT; ++n) {
-                            const float p0 = x[sub][n][2 * i], p1 = x[sub][n][2 * i + 1];
-                            T.z[g][n][0] = fmaf(p0, zo, T.z[g][n][0]);
-                            T.z[g][n][1] = fmaf(p1, zo, T.z[g][n][1]);
-                            const float a0 = p0 * sc, a1 = p1 * sc;
-                            const uint32_t h = pack_h2(a0, a1);
-                            uint32_t lo = 0;
-                            if (LO) {
-                                float h0, h1;
-                                half2x(h, h0, h1);
-                                lo = pack_h2(a0 - h0, a1 - h1);
-                            }
-                            if (MODE == PACK4) {
-                                ph[n][i] = transpose8x8(j >= 2 ? lo : h);
-                            } else {
-                                ph[n][i] = transpose8x8(h);
-                                if (LO) pl[n][i] = transpose8x8(lo);
-                            }
+                    for (int n = 0; n < C::NT; ++n) {
+                        const float p0 = x[sub][n][2 * i], p1 = x[sub][n][2 * i + 1];
+                        T.z[g][n][0] = fmaf(p0, zo, T.z[g][n][0]);
+                        T.z[g][n][1] = fmaf(p1, zo, T.z[g][n][1]);
+                        const float a0 = p0 * sc, a1 = p1 * sc;
+                        const uint32_t h = pack_h2(a0, a1);
+                        uint32_t lo = 0;
+                        if (LO) {
+                            float h0, h1;
+                            half2x(h, h0, h1);
+                            lo = pack_h2(a0 - h0, a1 - h1);
                         }
-                    }
-                    // the values' words: rows of a product are channels, its columns the slots' order of the keys' rows
-                    uint32_t vw[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vw[i] = lds<uint32_t>(ub + vat[i & 1][g] + (sub * 16 + 8 * (i >> 1)) * C::RB);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t a = __byte_perm(vw[0], vw[1], half ? 0x7632 : 0x5410);
-                        const uint32_t b = __byte_perm(vw[2], vw[3], half ? 0x7632 : 0x5410);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const uint32_t av = t ? a >> 8 : a, bv = t ? b >> 8 : b;
-                            uint32_t fr[4];
-                            fr[0] = hsub2u(and_or(av, 0x000f000fu, 0x64006400u), 0x64086408u);
-                            fr[1] = hsub2u(and_or(av, 0x00f000f0u, 0x64006400u), 0x64806480u);
-                            fr[2] = hsub2u(and_or(bv, 0x000f000fu, 0x64006400u), 0x64086408u);
-                            fr[3] = hsub2u(and_or(bv, 0x00f000f0u, 0x64006400u), 0x64806480u);
-#pragma unroll
-                            for (int n = 0; n < C::NT; ++n) {
-                                mma16816(T.o[g * 4 + half * 2 + t][n], fr, ph[n][0], ph[n][1]);
-                                if (MODE != PACK4 && LO) mma16816(T.o[g * 4 + half * 2 + t][n], fr, pl[n][0], pl[n][1]);
-                            }
+                        if (MODE == PACK4) {
+                            ph[n][i] = transpose8x8(j >= 2 ? lo : h);
+                        } else {
+                            ph[n][i] = transpose8x8(h);
+                            if (LO) pl[n][i] = transpose8x8(lo);
                         }
                     }
                 }
+            };
+            // the values' words of one group and 16 slots, and of them the fragment of channels 2 t, 2 t + 1 (of 8) of
+            // every lane row: rows of a product are channels, its columns the slots' order of the keys' rows
+            auto words = [&](int g, int sub, uint32_t (&w)[4]) {
+                uint32_t vw[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vw[i] = lds<uint32_t>(ub + vat[i & 1][g] + (sub * 16 + 8 * (i >> 1)) * C::RB);
+                w[0] = __byte_perm(vw[0], vw[1], 0x5410);
+                w[1] = __byte_perm(vw[2], vw[3], 0x5410);
+                w[2] = __byte_perm(vw[0], vw[1], 0x7632);
+                w[3] = __byte_perm(vw[2], vw[3], 0x7632);
+            };
+            auto fragment = [&](const uint32_t (&w)[4], int t, uint32_t (&fr)[4]) {
+                const uint32_t av = t & 1 ? w[t & 2] >> 8 : w[t & 2], bv = t & 1 ? w[(t & 2) + 1] >> 8 : w[(t & 2) + 1];
+                fr[0] = hsub2u(and_or(av, 0x000f000fu, 0x64006400u), 0x64086408u);
+                fr[1] = hsub2u(and_or(av, 0x00f000f0u, 0x64006400u), 0x64806480u);
+                fr[2] = hsub2u(and_or(bv, 0x000f000fu, 0x64006400u), 0x64086408u);
+                fr[3] = hsub2u(and_or(bv, 0x00f000f0u, 0x64006400u), 0x64806480u);
+            };
+            if (TWO) {
+                // A product's sum is cut off, not rounded, so long chains drift: for fp32 outputs a unit's products are
+                // summed from zero and added to the others with a rounding.
+#pragma unroll
+                for (int g = 0; g < C::G; ++g) {
+                    uint32_t ph[C::SUB][C::NT][2], pl[C::SUB][C::NT][2], w[C::SUB][4];
+#pragma unroll
+                    for (int sub = 0; sub < C::SUB; ++sub) {
+                        weights(g, sub, ph[sub], pl[sub]);
+                        words(g, sub, w[sub]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        float sum[C::NT][4] = {};
+#pragma unroll
+                        for (int sub = 0; sub < C::SUB; ++sub) {
+                            uint32_t fr[4];
+                            fragment(w[sub], t, fr);
+#pragma unroll
+                            for (int n = 0; n < C::NT; ++n) {
+                                if (MODE != PACK4) mma16816(sum[n], fr, pl[sub][n][0], pl[sub][n][1]);
+                                mma16816(sum[n], fr, ph[sub][n][0], ph[sub][n][1]);
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) T.o[g * 4 + t][n][i] += sum[n][i];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < C::G; ++g)
+#pragma unroll
+                    for (int sub = 0; sub < C::SUB; ++sub) {
+                        uint32_t ph[C::NT][2], pl[C::NT][2], w[4];
+                        weights(g, sub, ph, pl);
+                        words(g, sub, w);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            uint32_t fr[4];
+                            fragment(w, t, fr);
+#pragma unroll
+                            for (int n = 0; n < C::NT; ++n) {
+                                mma16816(T.o[g * 4 + t][n], fr, ph[n][0], ph[n][1]);
+                                if (MODE != PACK4 && LO) mma16816(T.o[g * 4 + t][n], fr, pl[n][0], pl[n][1]);
+                            }
+                        }
+                    }
+            }
         }
 
         if (!last) {
@@ -1142,7 +1184,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_join_kernel(QAttnK k) {
     }
 }
 
-template <int D, int MODE, bool LO>
+template <int D, int MODE, bool LO, bool TWO>
 cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     using C = Cfg<D, MODE>;
     const size_t axis = (2 * (size_t)k.a.c.batch + 1) * sizeof(int), smem = C::smem_fixed + axis;
@@ -1159,10 +1201,10 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     k.area = (part < head ? part : head) * C::UT * C::RP;
     const size_t join = 2 * (size_t)k.grid * C::RP * sizeof(float);
     k.subs = 2;   // one wave of four per SM (64 ragged sequences of up to 8,192 slots: 108, 101, 104 us with 1, 2, 3)
-    cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, LO, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && join > 48 * 1024)
         e = cudaFuncSetAttribute(qattn_join_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join);
-    if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, LO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
+    if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, LO, TWO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
     if (e == cudaSuccess) e = launch(qattn_join_kernel<D, MODE>, dim3(k.grid * k.subs), dim3(kThreads), join, s, pdl_enabled(), k);
     return e;
 }
@@ -1170,10 +1212,16 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
 }  // namespace
 
 template <int D>
-cudaError_t run_qattn(QAttnK k, int mode, bool lo, int64_t cost, cudaStream_t s) {
-    if (mode == PACK4) return run<D, PACK4, true>(k, cost, s);
-    if (mode == ONE8) return lo ? run<D, ONE8, true>(k, cost, s) : run<D, ONE8, false>(k, cost, s);
-    return lo ? run<D, TWO8, true>(k, cost, s) : run<D, TWO8, false>(k, cost, s);
+cudaError_t run_qattn(QAttnK k, int mode, int64_t cost, cudaStream_t s) {
+    const int dt = k.a.q.dt;
+    if (mode == PACK4) return dt == CS_F32 ? run<D, PACK4, true, true>(k, cost, s) : run<D, PACK4, true, false>(k, cost, s);
+    if (mode == ONE8)
+        return dt == CS_F32   ? run<D, ONE8, true, true>(k, cost, s)
+               : dt == CS_F16 ? run<D, ONE8, true, false>(k, cost, s)
+                              : run<D, ONE8, false, false>(k, cost, s);
+    return dt == CS_F32   ? run<D, TWO8, true, true>(k, cost, s)
+           : dt == CS_F16 ? run<D, TWO8, true, false>(k, cost, s)
+                          : run<D, TWO8, false, false>(k, cost, s);
 }
 
 #endif  // CS_QATTN_KERNELS

@@ -2,4 +2,4 @@
 #define CS_QATTN_KERNELS
 #include "cs_qattn.cuh"
 
-template cudaError_t cs::run_qattn<192>(cs::QAttnK, int, bool, int64_t, cudaStream_t);
+template cudaError_t cs::run_qattn<192>(cs::QAttnK, int, int64_t, cudaStream_t);
