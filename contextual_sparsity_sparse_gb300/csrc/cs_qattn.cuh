@@ -37,7 +37,10 @@
 // bits; the second is zero for 16-bit inputs).  p s is scaled by the largest
 // scale's power of two (kUp) and split likewise; for bf16 outputs one part is
 // enough (2^-12 beside the output's 2^-9).  With at most 4 rows the two parts
-// sit in the same 8 columns.  All sums and the softmax statistics are fp32.
+// sit in the same 8 columns.  All sums and the softmax statistics are fp32; for
+// fp32 outputs a unit's value products are summed apart (see there): the output
+// is then within 1e-7 to 7e-7 of its norm at 128 to 60,001 slots, before it drifted
+// to 2e-6.
 //
 // Bound (64 ragged sequences of up to 8,192 slots, 64 over 8 heads of 128, bf16:
 // 100 us of which the bytes need 47): 850 instructions per unit of 32 slots, 200
