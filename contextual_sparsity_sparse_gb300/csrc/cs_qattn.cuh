@@ -38,9 +38,9 @@
 // scale's power of two (kUp) and split likewise; for bf16 outputs one part is
 // enough (2^-12 beside the output's 2^-9).  With at most 4 rows the two parts
 // sit in the same 8 columns.  All sums and the softmax statistics are fp32; for
-// fp32 outputs a unit's value products are summed apart (see there): the output
-// is then within 1e-7 to 7e-7 of its norm at 128 to 60,001 slots, before it drifted
-// to 2e-6.
+// fp32 outputs (TWO) the keys' codes are taken as n - 8 outright and a unit's value
+// products are summed apart (see there): over cases of 1 to 60,001 slots the output
+// is then within 1e-7 to 2e-7 of its norm, before it was off by up to 2e-6.
 //
 // Bound (64 ragged sequences of up to 8,192 slots, 64 over 8 heads of 128, bf16:
 // 100 us of which the bytes need 47): 850 instructions per unit of 32 slots, 200
@@ -607,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 float *cc = cols_next + row * C::CS;
                 out_next[row] = out_at(k, b, h, row);
                 // takes the products back; kept where x c1 stays in fp32's range (beyond, one slot takes all as well)
-                cc[0] = fminf(fmaxf(k.c2 * exp2f((float)(24 - up)), 1.2e-38f), 1.2e30f);
+                cc[0] = fminf(fmaxf(k.c2 * exp2f((float)((TWO ? 0 : 24) - up)), 1.2e-38f), 1.2e30f);
                 cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + b) + (k.row0 + row) / k.group : INT_MAX);
                 cc[2] = row_on(k, b, h, row) ? 1.f : 0.f;
 #pragma unroll
-                for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * 5.9604644775390625e-8f;   // 2^-24, as the products
+                for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * (TWO ? 1.f : 5.9604644775390625e-8f);   // 2^-24, as the products
             }
         }
     };
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float a0 = -8.f * zq[n][q][g];
+                        const float a0 = TWO ? 0.f : -8.f * zq[n][q][g];
 #pragma unroll
                         for (int sub = 0; sub < C::SUB; ++sub) acc[sub][n][q] = acc[sub][n][2 + q] = a0;
                     }
@@ -713,8 +713,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                                 for (int i = 0; i < 2; ++i) {
                                     uint32_t v = w ? kw[sub][i].y : kw[sub][i].x;
                                     if (step) v >>= 8;
-                                    a[i] = v & 0x000f000fu;
-                                    a[i + 2] = v & 0x00f000f0u;
+                                    if (TWO) {
+                                        // a product's 16 terms are cut off alike, after the largest: n - 8 itself is nearer 0
+                                        a[i] = hsub2u(and_or(v, 0x000f000fu, 0x64006400u), 0x64086408u);
+                                        a[i + 2] = hsub2u(and_or(v, 0x00f000f0u, 0x64006400u), 0x64806480u);
+                                    } else {
+                                        a[i] = v & 0x000f000fu;
+                                        a[i + 2] = v & 0x00f000f0u;
+                                    }
                                 }
                                 mma16816(acc[sub][n], a, step ? b.z : b.x, step ? b.w : b.y);
                                 if (two) mma16816(acc[sub][n], a, step ? b2.z : b2.x, step ? b2.w : b2.y);
