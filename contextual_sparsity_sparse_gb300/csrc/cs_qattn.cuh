@@ -22,25 +22,29 @@
 // Starting and joining a head costs a CTA about as long as kHeadCost units, so
 // a head is that much longer on the axis.
 //
-// Products.  mma.sync m16n8k16 in fp16 with fp32 sums: the query rows are the
+// Products.  mma.sync m16n8k16 with fp32 sums: the query rows are the
 // 8 columns, so a batch-1 head wastes little, and the codes are the A operand
-// straight from their packed words.  For the keys, 16 slots x 16 channels: a
+// straight from their packed words.  For the keys, in fp16, 16 slots x 16 channels: a
 // nibble ANDed out of a word is an fp16 subnormal n 2^-24 (or, four bits up,
 // n 2^-20), exact in the product; the factor 16 goes into q, and the sums start
-// at -8 (sum q).  For the values, 16 channels x 16 slots: two slots' words are
-// interleaved by byte permutes, n is ORed into 1024 + n and 1032 subtracted.
+// at -8 (sum q).  For the values, in bf16, 16 channels x 16 slots: two slots' words are
+// interleaved by byte permutes, and a nibble ANDed out is bf16's n 2^-133 (four bits
+// up n 2^-129: the bit that leaves the fraction is the exponent's lowest, and the least
+// exponent has the subnormals' steps); one multiply-add by 2^127 takes it to (n - 8) / 64 (or / 4).
 // The tensor-memory path of the newer matrix instructions needs 128 rows and
 // operands in shared memory; with at most 16 query rows per head the products
 // are not what bounds this kernel, the instructions around them are.
 //
 // Precision.  q is scaled by a power of two and split into two fp16 parts (22
-// bits; the second is zero for 16-bit inputs).  p s is scaled by the largest
-// scale's power of two (kUp) and split likewise; for bf16 outputs one part is
-// enough (2^-12 beside the output's 2^-9).  With at most 4 rows the two parts
-// sit in the same 8 columns.  All sums and the softmax statistics are fp32; for
+// bits; the second is zero for 16-bit inputs).  p s goes in bf16 parts of 8 bits each:
+// two for 16-bit outputs (what is left out is 2^-17 of a term or less, beside output roundings of 2^-8 and
+// 2^-11), three for fp32 ones (2^-26).  bf16 has fp32's range, so a term keeps its bits however
+// small it is beside others: fp16 parts under one power of two for a warp's slots, rows and groups cost the others
+// up to 13 bits where one slot's or one group's scale was 2^15 of theirs, with no weight at all on it (fp32 outputs off by 6e-5).
+// With at most 4 rows the first two parts sit in the same 8 columns.  All sums and the softmax statistics are fp32; for
 // fp32 outputs (TWO) the keys' codes are taken as n - 8 outright and a unit's value
-// products are summed apart (see there): over cases of 1 to 60,001 slots the output
-// is then within 1e-7 to 2e-7 of its norm, before it was off by up to 2e-6.
+// products are summed apart (see there).  Logits of size X (64 channels in eight products, each cut off
+// after 24 bits) move fp32 outputs by 2^-21 X of the terms at most.
 //
 // Bound (64 ragged sequences of up to 8,192 slots, 64 over 8 heads of 128, bf16:
 // 100 us of which the bytes need 47): 850 instructions per unit of 32 slots, 200
@@ -144,6 +148,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_bf(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -164,8 +173,14 @@ __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    const __half2 r = __floats2half2_rn(lo, hi);
+// a b + c of two bf16 pairs
+__device__ __forceinline__ uint32_t bfma2u(uint32_t a, uint32_t b, uint32_t c) {
+    using P = const __nv_bfloat162 *;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<P>(&a), *reinterpret_cast<P>(&b), *reinterpret_cast<P>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
@@ -401,10 +416,8 @@ __device__ __forceinline__ void weigh(const QAttnK &k, const float *lg, int n, i
 // ------------------------------------------------------------- first kernel
 
 // A row's m moves only when an x leads it by more than 2^kLead in p (moving it
-// scales all sums): most rows keep the m of their first unit.  p s 2^(kUp - e) of
-// a p up to 2^kLead, with s below 2^(e - 14), stays below 2^15.
+// scales all sums): most rows keep the m of their first unit.
 constexpr float kLead = 8.f;
-constexpr int kUp = 29 - 8;
 
 template <int D, int MODE>
 struct Tile {
@@ -415,8 +428,6 @@ struct Tile {
     float m[C::NT][2];               // largest x so far
     float ms[C::NT][2];              // the same, 0 for -inf
     float t[C::NT][2];               // an x beyond this one moves m
-    int e;                           // exponent field of the largest value scale so far; the sums hold p 2^(kUp - e)
-    float es;                        // the least scale with a larger one
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -435,8 +446,6 @@ struct Tile {
                 for (int g = 0; g < C::G; ++g) z[g][n][i] = 0.f;
             }
         }
-        e = 1;
-        es = 1.220703125e-4f;   // 2^-13
     }
 };
 
@@ -487,8 +496,8 @@ __device__ __forceinline__ void fetch(const QAttnK &k, uint32_t stage, int64_t s
         cp_async_or0<4>(stage + C::UT * (2 * C::RB + C::G * 8) + lane * 4, lane < n ? c.pos + slot0 + lane : c.pos, lane < n);
 }
 
-// LO: p s has a second fp16 part (always so in PACK4).  TWO: q has one, too, and sums are kept to fp32's precision.
-template <int D, int MODE, bool LO, bool TWO>
+// TWO: q has a second part, p s a third, and sums are kept to fp32's precision.
+template <int D, int MODE, bool TWO>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAttnK k) {
     using C = Cfg<D, MODE>;
     extern __shared__ __align__(16) char smem[];
@@ -498,7 +507,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
     float *stat = cols_next + C::RP * C::CS;
     int *axis_mem = reinterpret_cast<int *>(stat + C::STAT);
     __shared__ int wsum[32];
-    __shared__ int wexp[kWarps];
     __shared__ int woff[kWarps];
     __shared__ int64_t outs[2][C::RP];
     int64_t *out_row = outs[0], *out_next = outs[1];
@@ -800,23 +808,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     if (C::SUB == 2) mx[n][q] = fmaxf(mx[n][q], fmaxf(x[C::SUB - 1][n][q], x[C::SUB - 1][n][2 + q]));
                     grow |= mx[n][q] > T.t[n][q];
                 }
-            float vsc[C::SUB][2][C::G], top = 0.f;
-#pragma unroll
-            for (int sub = 0; sub < C::SUB; ++sub)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int g = 0; g < C::G; ++g) {
-                        vsc[sub][i][g] = __half2float(__ushort_as_half((unsigned short)(vs[sub][i][g] & 0xffffu)));
-                        top = fmaxf(top, vsc[sub][i][g]);
-                    }
-            grow |= top >= T.es;
             if (__any_sync(kFull, grow)) {
-                // an fp32 exponent field of 113 (2^-14) is fp16's 1
-                const int e = max(T.e, (int)(__reduce_max_sync(kFull, __float_as_uint(top)) >> 23) - 112);
-                const float de = (float)(T.e - e);
-                T.e = e;
-                T.es = __uint_as_float((uint32_t)(113 + e) << 23);
 #pragma unroll
                 for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -827,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                         // a column that need not move stays, and so do its sums
                         m = m > T.t[n][q] ? m : T.m[n][q];
                         // nothing but zeros, or NaN, came before the first finite x
-                        const float al = T.m[n][q] == -INFINITY ? 0.f : exp2_approx(fmaf(T.m[n][q] - m, c1[n][q], de));
+                        const float al = T.m[n][q] == -INFINITY ? 0.f : exp2_approx((T.m[n][q] - m) * c1[n][q]);
                         T.m[n][q] = m;
                         T.ms[n][q] = m == -INFINITY ? 0.f : m;
                         T.t[n][q] = fmaf(kLead, inv1[n][q], m);
@@ -842,7 +834,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     }
             }
             // ---- p, its sums, and p s as fragments
-            const float up = (float)(kUp - T.e);
 #pragma unroll
             for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -852,33 +843,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float &v = x[sub][n][2 * i + q];
-                            v = exp2_approx(fmaf(v - T.ms[n][q], c1[n][q], up));
+                            v = exp2_approx((v - T.ms[n][q]) * c1[n][q]);
                             T.l[n][q] += v;
                         }
-            // p s of one group and 16 slots as fragments; LO: in two parts
-            auto weights = [&](int g, int sub, uint32_t (&ph)[C::NT][2], uint32_t (&pl)[C::NT][2]) {
+            // p s of one group and 16 slots as fragments, in two parts of 8 bits, for fp32 outputs three
+            auto weights = [&](int g, int sub, uint32_t (&ph)[C::NT][2], uint32_t (&pl)[C::NT][2], uint32_t (&p3)[C::NT][2]) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float sc = vsc[sub][i][g];
-                    const float zo = fmaf(8.f, sc, __half2float(__ushort_as_half((unsigned short)(vs[sub][i][g] >> 16))));
+                    float sc, zo;
+                    half2x(vs[sub][i][g], sc, zo);
+                    zo = fmaf(8.f, sc, zo);
 #pragma unroll
                     for (int n = 0; n < C::NT; ++n) {
                         const float p0 = x[sub][n][2 * i], p1 = x[sub][n][2 * i + 1];
                         T.z[g][n][0] = fmaf(p0, zo, T.z[g][n][0]);
                         T.z[g][n][1] = fmaf(p1, zo, T.z[g][n][1]);
                         const float a0 = p0 * sc, a1 = p1 * sc;
-                        const uint32_t h = pack_h2(a0, a1);
-                        uint32_t lo = 0;
-                        if (LO) {
-                            float h0, h1;
-                            half2x(h, h0, h1);
-                            lo = pack_h2(a0 - h0, a1 - h1);
+                        float h0, h1, l0, l1;
+                        const uint32_t h = pack_bf2(a0, a1);
+                        bf2x(h, h0, h1);
+                        const uint32_t lo = pack_bf2(a0 - h0, a1 - h1);
+                        uint32_t third = 0;
+                        if (TWO) {
+                            bf2x(lo, l0, l1);
+                            third = pack_bf2((a0 - h0) - l0, (a1 - h1) - l1);
                         }
                         if (MODE == PACK4) {
                             ph[n][i] = transpose8x8(j >= 2 ? lo : h);
+                            if (TWO) p3[n][i] = transpose8x8(j >= 2 ? third : 0u);   // beside lo: h's sums stay exact
                         } else {
                             ph[n][i] = transpose8x8(h);
-                            if (LO) pl[n][i] = transpose8x8(lo);
+                            pl[n][i] = transpose8x8(lo);
+                            if (TWO) p3[n][i] = transpose8x8(third);
                         }
                     }
                 }
@@ -896,20 +892,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
             };
             auto fragment = [&](const uint32_t (&w)[4], int t, uint32_t (&fr)[4]) {
                 const uint32_t av = t & 1 ? w[t & 2] >> 8 : w[t & 2], bv = t & 1 ? w[(t & 2) + 1] >> 8 : w[(t & 2) + 1];
-                fr[0] = hsub2u(and_or(av, 0x000f000fu, 0x64006400u), 0x64086408u);
-                fr[1] = hsub2u(and_or(av, 0x00f000f0u, 0x64006400u), 0x64806480u);
-                fr[2] = hsub2u(and_or(bv, 0x000f000fu, 0x64006400u), 0x64086408u);
-                fr[3] = hsub2u(and_or(bv, 0x00f000f0u, 0x64006400u), 0x64806480u);
+                fr[0] = bfma2u(av & 0x000f000fu, 0x7f007f00u, 0xbe00be00u);
+                fr[1] = bfma2u(av & 0x00f000f0u, 0x7f007f00u, 0xc000c000u);
+                fr[2] = bfma2u(bv & 0x000f000fu, 0x7f007f00u, 0xbe00be00u);
+                fr[3] = bfma2u(bv & 0x00f000f0u, 0x7f007f00u, 0xc000c000u);
             };
             if (TWO) {
                 // A product's sum is cut off, not rounded, so long chains drift: for fp32 outputs a unit's products are
                 // summed from zero and added to the others with a rounding.
 #pragma unroll
                 for (int g = 0; g < C::G; ++g) {
-                    uint32_t ph[C::SUB][C::NT][2], pl[C::SUB][C::NT][2], w[C::SUB][4];
+                    uint32_t ph[C::SUB][C::NT][2], pl[C::SUB][C::NT][2], p3[C::SUB][C::NT][2], w[C::SUB][4];
 #pragma unroll
                     for (int sub = 0; sub < C::SUB; ++sub) {
-                        weights(g, sub, ph[sub], pl[sub]);
+                        weights(g, sub, ph[sub], pl[sub], p3[sub]);
                         words(g, sub, w[sub]);
                     }
 #pragma unroll
@@ -921,8 +917,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                             fragment(w[sub], t, fr);
 #pragma unroll
                             for (int n = 0; n < C::NT; ++n) {
-                                if (MODE != PACK4) mma16816(sum[n], fr, pl[sub][n][0], pl[sub][n][1]);
-                                mma16816(sum[n], fr, ph[sub][n][0], ph[sub][n][1]);
+                                mma16816_bf(sum[n], fr, p3[sub][n][0], p3[sub][n][1]);
+                                if (MODE != PACK4) mma16816_bf(sum[n], fr, pl[sub][n][0], pl[sub][n][1]);
+                                mma16816_bf(sum[n], fr, ph[sub][n][0], ph[sub][n][1]);
                             }
                         }
 #pragma unroll
@@ -936,8 +933,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 for (int g = 0; g < C::G; ++g)
 #pragma unroll
                     for (int sub = 0; sub < C::SUB; ++sub) {
-                        uint32_t ph[C::NT][2], pl[C::NT][2], w[4];
-                        weights(g, sub, ph, pl);
+                        uint32_t ph[C::NT][2], pl[C::NT][2], p3[C::NT][2], w[4];
+                        weights(g, sub, ph, pl, p3);
                         words(g, sub, w);
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
@@ -945,8 +942,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                             fragment(w, t, fr);
 #pragma unroll
                             for (int n = 0; n < C::NT; ++n) {
-                                mma16816(T.o[g * 4 + t][n], fr, ph[n][0], ph[n][1]);
-                                if (MODE != PACK4 && LO) mma16816(T.o[g * 4 + t][n], fr, pl[n][0], pl[n][1]);
+                                mma16816_bf(T.o[g * 4 + t][n], fr, ph[n][0], ph[n][1]);
+                                if (MODE != PACK4) mma16816_bf(T.o[g * 4 + t][n], fr, pl[n][0], pl[n][1]);
                             }
                         }
                     }
@@ -977,10 +974,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     stat[(kWarps + warp) * C::RP + col] = T.l[n][q];
                 }
             }
-        if (lane == 0) {
-            wexp[warp] = T.e;
-            woff[warp] = (warp * C::ST + fstage) * C::STAGE;
-        }
+        if (lane == 0) woff[warp] = (warp * C::ST + fstage) * C::STAGE;
         float *mine = reinterpret_cast<float *>(smem + (warp * C::ST + fstage) * C::STAGE);
 #pragma unroll
         for (int pass = 0; pass < C::RP / C::CP; ++pass) {
@@ -1000,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
                             *reinterpret_cast<float2 *>(mine + (col + q) * C::RS + t * 16 + r * 2) =
-                                make_float2(v[q] + T.z[t / 4][n][q], fmaf(v[2 + q], 0.0625f, T.z[t / 4][n][q]));
+                                make_float2(fmaf(v[q], 64.f, T.z[t / 4][n][q]), fmaf(v[2 + q], 4.f, T.z[t / 4][n][q]));
                     }
                 }
             __syncthreads();
@@ -1014,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                     for (int o = 1; o < kWarps; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
                     float l = 0.f;
                     if (lane < kWarps) {
-                        const float f = exp2f(fmaf(mw - (m == -INFINITY ? 0.f : m), c, (float)(wexp[lane] - kUp)));
+                        const float f = exp2f((mw - (m == -INFINITY ? 0.f : m)) * c);
                         stat[lane * C::RP + row] = f;
                         l = f * stat[(kWarps + lane) * C::RP + row];
                     }
@@ -1193,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_join_kernel(QAttnK k) {
     }
 }
 
-template <int D, int MODE, bool LO, bool TWO>
+template <int D, int MODE, bool TWO>
 cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     using C = Cfg<D, MODE>;
     const size_t axis = (2 * (size_t)k.a.c.batch + 1) * sizeof(int), smem = C::smem_fixed + axis;
@@ -1210,10 +1204,10 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     k.area = (part < head ? part : head) * C::UT * C::RP;
     const size_t join = 2 * (size_t)k.grid * C::RP * sizeof(float);
     k.subs = 2;   // one wave of four per SM (64 ragged sequences of up to 8,192 slots: 108, 101, 104 us with 1, 2, 3)
-    cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, LO, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && join > 48 * 1024)
         e = cudaFuncSetAttribute(qattn_join_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join);
-    if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, LO, TWO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
+    if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, TWO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
     if (e == cudaSuccess) e = launch(qattn_join_kernel<D, MODE>, dim3(k.grid * k.subs), dim3(kThreads), join, s, pdl_enabled(), k);
     return e;
 }
@@ -1222,15 +1216,10 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
 
 template <int D>
 cudaError_t run_qattn(QAttnK k, int mode, int64_t cost, cudaStream_t s) {
-    const int dt = k.a.q.dt;
-    if (mode == PACK4) return dt == CS_F32 ? run<D, PACK4, true, true>(k, cost, s) : run<D, PACK4, true, false>(k, cost, s);
-    if (mode == ONE8)
-        return dt == CS_F32   ? run<D, ONE8, true, true>(k, cost, s)
-               : dt == CS_F16 ? run<D, ONE8, true, false>(k, cost, s)
-                              : run<D, ONE8, false, false>(k, cost, s);
-    return dt == CS_F32   ? run<D, TWO8, true, true>(k, cost, s)
-           : dt == CS_F16 ? run<D, TWO8, true, false>(k, cost, s)
-                          : run<D, TWO8, false, false>(k, cost, s);
+    const bool two = k.a.q.dt == CS_F32;
+    if (mode == PACK4) return two ? run<D, PACK4, true>(k, cost, s) : run<D, PACK4, false>(k, cost, s);
+    if (mode == ONE8) return two ? run<D, ONE8, true>(k, cost, s) : run<D, ONE8, false>(k, cost, s);
+    return two ? run<D, TWO8, true>(k, cost, s) : run<D, TWO8, false>(k, cost, s);
 }
 
 #endif  // CS_QATTN_KERNELS
