@@ -396,8 +396,9 @@ class QCache:
     n_heads, capacity, d_head / 2], k_scale and v_scale fp16 [batch, n_heads,
     capacity, d_head / 64, 2], weight fp32 and pos int32 [batch, n_heads,
     capacity] (either may be None).  The tensors may be views, as long as their
-    slots are contiguous and all step alike over sequences and heads.  For
-    cs_qcache_evict alone, weight (and pos) are enough."""
+    slots are contiguous, all step alike over sequences and heads, and no
+    sequence or head is expanded from another's memory.  For cs_qcache_evict
+    alone, weight (and pos) are enough."""
 
     def __init__(self, k, v, k_scale, v_scale, weight=None, pos=None):
         self.k, self.v, self.k_scale, self.v_scale, self.weight, self.pos = k, v, k_scale, v_scale, weight, pos
@@ -438,6 +439,8 @@ class QCache:
         for i, n in ((0, self.batch), (1, self.n_heads)):
             if n > 1 and t.stride(i) % row:
                 raise ValueError("a cache tensor must step by whole slots")
+            if n > 1 and t.stride(i) == 0:   # a step of 0 would be read as "dense", far past the memory
+                raise ValueError("a cache tensor must not be expanded over sequences or heads")
             got.append(t.stride(i) // row if n > 1 else dense[i])
         if ld is not None and tuple(got) != tuple(ld):
             raise ValueError("a cache's tensors must step alike over sequences and heads")
