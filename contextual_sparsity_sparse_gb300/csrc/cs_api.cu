@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/cs.h: argument validation,
 // workspace layout and dispatch to the kernels.  No entry point allocates
 // device memory; every buffer is the caller's.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -48,6 +49,36 @@ int device_sm_count() {
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     return n;
+}
+
+cudaError_t allow_smem(const void *kernel) {
+    // the kernels that are done, in the first free place from where their address falls; past a full table each call sets its
+    // limit again, always to the same value
+    constexpr int kPlaces = 1024;
+    static std::atomic<uint64_t> done[kPlaces];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t key = reinterpret_cast<uintptr_t>(kernel) ^ (uint64_t)dev << 56;
+    int at = (int)((key * 0x9e3779b97f4a7c15ull) >> 54), left = kPlaces;
+    uint64_t was = 0;
+    while (left && (was = done[at].load(std::memory_order_acquire)) != 0) {
+        if (was == key) return cudaSuccess;
+        at = (at + 1) % kPlaces;
+        --left;
+    }
+    cudaFuncAttributes a;
+    int most = 0;
+    e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)a.sharedSizeBytes);
+    // another thread may have taken the place meanwhile: then this one is put behind it, or comes again
+    for (; e == cudaSuccess && left; at = (at + 1) % kPlaces, --left) {
+        was = 0;
+        if (done[at].compare_exchange_strong(was, key, std::memory_order_release) || was == key) break;
+    }
+    return e;
 }
 
 size_t dtype_size(cs_dtype t) { return t == CS_F32 ? 4 : 2; }

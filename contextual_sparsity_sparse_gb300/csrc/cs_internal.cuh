@@ -276,6 +276,11 @@ __device__ __forceinline__ int block_excl_scan(int v, int *wsum, int *total) {
 void set_error(const char *fmt, ...);
 cs_status cuda_fail(cudaError_t e, const char *what);
 
+// Lets launches of a kernel take as much dynamic shared memory as the device has beside the kernel's own, once per
+// kernel and device.  The limit is the kernel's, not the launch's: set to each launch's size, one thread's call could
+// lower it between another's setting and its launch.
+cudaError_t allow_smem(const void *kernel);
+
 // Launch with optional programmatic-dependent-launch attribute.
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

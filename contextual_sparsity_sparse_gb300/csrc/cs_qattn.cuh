@@ -1204,9 +1204,8 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     k.area = (part < head ? part : head) * C::UT * C::RP;
     const size_t join = 2 * (size_t)k.grid * C::RP * sizeof(float);
     k.subs = 2;   // one wave of four per SM (64 ragged sequences of up to 8,192 slots: 108, 101, 104 us with 1, 2, 3)
-    cudaError_t e = cudaFuncSetAttribute(qattn_kernel<D, MODE, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && join > 48 * 1024)
-        e = cudaFuncSetAttribute(qattn_join_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&qattn_kernel<D, MODE, TWO>));
+    if (e == cudaSuccess && join > 48 * 1024) e = allow_smem(reinterpret_cast<const void *>(&qattn_join_kernel<D, MODE>));
     if (e == cudaSuccess) e = launch(qattn_kernel<D, MODE, TWO>, dim3(k.grid), dim3(kThreads), smem, s, pdl_enabled(), k);
     if (e == cudaSuccess) e = launch(qattn_join_kernel<D, MODE>, dim3(k.grid * k.subs), dim3(kThreads), join, s, pdl_enabled(), k);
     return e;
