@@ -363,7 +363,7 @@ ffn_reduce_kernel(const float *part, int G, int B, int d, int dp,
 template <typename T, int TB, bool GLU, bool PRE, int MAXV>
 cudaError_t run_gather(const FfnArgs &a, FfnK k, size_t smem, cudaStream_t s) {
     auto fn = ffn_gather_kernel<T, TB, GLU, PRE, MAXV>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
     // one thread per vector when a row has at most 1024 of them
     const int thr = ((k.nvec + MAXV - 1) / MAXV + 31) & ~31;

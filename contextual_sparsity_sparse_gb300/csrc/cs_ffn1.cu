@@ -284,7 +284,7 @@ cudaError_t run1(const FfnK &k, size_t smem, int G, cudaStream_t s) {
     case 4: fn = ffn_gather1_kernel<T, GLU, PRE, 4, 3>; break;
     default: return cudaErrorNotSupported;
     }
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
     const int thr = (k.nvec + 31) & ~31;
     return launch(fn, dim3(G), dim3(thr), smem, s, pdl_enabled(), k);

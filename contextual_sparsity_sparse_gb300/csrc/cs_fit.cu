@@ -244,7 +244,7 @@ cs_status cs_fit_predictor(const cs_ffn_layer *layer, cs_predictor *pred, const 
     cholesky_kernel<<<1, 1024, 0, s>>>(A, r, lambda, err);
     // 4. one solve per neuron
     const size_t smem = sizeof(double) * (size_t)kSolveWarps * r;
-    e = cudaFuncSetAttribute(chol_solve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_smem(reinterpret_cast<const void *>(chol_solve_kernel));
     if (e != cudaSuccess) return cuda_fail(e, "cs_fit_predictor(solve attribute)");
     const int sms = std::max(1, device_sm_count());
     const int grid = std::min((f + kSolveWarps - 1) / kSolveWarps, 8 * sms);

@@ -801,7 +801,7 @@ cudaError_t run_tc(const FfnArgs &f, cudaStream_t s) {
         auto fn = ks256 ? tc_gate_kernel<T, false, NP, 256>
                         : ks128 ? tc_gate_kernel<T, false, NP, 128>
                                 : (glu ? tc_gate_kernel<T, true, NP, 64> : tc_gate_kernel<T, false, NP, 64>);
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_smem(reinterpret_cast<const void *>(fn));
         if (e != cudaSuccess) return e;
         e = launch(fn, dim3(sms), dim3(kTcThreads), smem, s, pdl_enabled(), a);
         if (e != cudaSuccess) return e;
@@ -814,7 +814,7 @@ cudaError_t run_tc(const FfnArgs &f, cudaStream_t s) {
         a.stages = std::min(8, (int)(kTcSmemBudget / stage));
         const size_t smem = (size_t)a.stages * stage + 1024;
         auto fn = tc_down_kernel<T, NP, MT>;
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_smem(reinterpret_cast<const void *>(fn));
         if (e != cudaSuccess) return e;
         e = launch(fn, dim3(sms), dim3(kTcThreads), smem, s, pdl_enabled(), a);
         if (e != cudaSuccess) return e;

@@ -294,7 +294,7 @@ cudaError_t run_tb(const GemvK &k0, cudaStream_t s, size_t per_cta) {
     k.chunk_rows = std::min(k.chunk_rows, k.rows_per_cta);
     const size_t smem = vbytes + 2 * (size_t)k.chunk_rows * k.ldb;
     auto fn = stream_gemv_kernel<T, TB, EPI>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
     dim3 grid((k.nrows + k.rows_per_cta - 1) / k.rows_per_cta, (k.B + TB - 1) / TB);
     return launch(fn, grid, dim3(kThreads), smem, s, pdl_enabled(), k);

@@ -61,3 +61,45 @@ def test_cache_attention_of_small_and_large_batches():
             return lambda: cs.cs_qcache_attention(cache, q, length, out, ws), check
         return make
     at_once([maker(1), maker(4096)], 3000)
+
+
+@pytest.mark.parametrize("sizes", [(512, 8192), (2560, 5120)])
+def test_predictors_of_small_and_large_layers(sizes):
+    def maker(d):
+        def make():
+            f, r = 4096, 256
+            g = torch.Generator("cuda").manual_seed(d)
+            rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+            pred = cs.Predictor(rand(r, d).half(), rand(f, r).half())
+            x, out, first = rand(d), torch.zeros(f, device="cuda"), torch.zeros(f, device="cuda")
+            ws = cs.Workspace(d, f, r)
+            cs.cs_predict(pred, x, first, ws)
+
+            def check():
+                assert torch.equal(out, first) and out.any()
+            return lambda: cs.cs_predict(pred, x, out, ws), check
+        return make
+    at_once([maker(d) for d in sizes], 3000)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("B", [1, 2])
+@pytest.mark.parametrize("sizes", [(4096, 5120), (512, 8192)])
+def test_layers_of_two_widths(sizes, B, glu):
+    def maker(d):
+        def make():
+            f = 2048
+            g = torch.Generator("cuda").manual_seed(d)
+            rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+            layer = cs.FfnLayer(rand(f, d).half(), rand(f, d).half(), w_up=rand(f, d).half() if glu else None)
+            x, out, first = rand(B, d), torch.zeros(B, d, device="cuda"), torch.zeros(B, d, device="cuda")
+            idx = torch.arange(f, dtype=torch.int32, device="cuda").repeat(B, 1)
+            count = torch.full((B,), 64, dtype=torch.int32, device="cuda")
+            ws = cs.Workspace(d, f, 64, B=B)
+            cs.cs_sparse_ffn(layer, x, idx, count, first, ws)
+
+            def check():
+                assert torch.equal(out, first) and out.any()
+            return lambda: cs.cs_sparse_ffn(layer, x, idx, count, out, ws), check
+        return make
+    at_once([maker(d) for d in sizes], 3000)
