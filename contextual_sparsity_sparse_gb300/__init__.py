@@ -458,12 +458,23 @@ class QCache:
 
 class QCacheWorkspace:
     """Device workspace of the cs_qcache_* calls on caches of this one's sizes,
-    with up to n_heads query heads and n_q query tokens per sequence."""
+    with up to n_heads query heads (0: no cs_qcache_attention) and n_q query
+    tokens per sequence.  weights=False: for attention that gathers none, whose
+    workspace stays small however long the cache.  That of a cache without
+    codes serves cs_qcache_evict alone."""
 
-    def __init__(self, cache: QCache, n_heads=None, n_q=1, device=None, stream=None):
+    def __init__(self, cache: QCache, n_heads=None, n_q=1, device=None, stream=None, weights=True):
         heads = cache.n_heads if n_heads is None else int(n_heads)
-        n = lib().cs_qcache_workspace_size(cache.batch, cache.n_heads, cache.capacity, cache.d_head or QCACHE_GROUP,
-                                           heads, int(n_q))
+
+        def size(capacity, heads):
+            return lib().cs_qcache_workspace_size(cache.batch, cache.n_heads, capacity, cache.d_head or QCACHE_GROUP,
+                                                  heads, int(n_q))
+        if cache.k is None:
+            n = size(1, 0)
+        elif weights:
+            n = size(cache.capacity, heads)
+        else:
+            n = size(1, heads) and max(size(1, heads), size(cache.capacity, 0))
         if n == 0:
             raise ValueError("no cs_qcache call takes these sizes")
         self.nbytes = n

@@ -23,16 +23,23 @@ int64_t cost_of(int batch, int kv_heads, int cap, int d) { return (int64_t)batch
 int ctas_of(int sms) { return kMaxPerSm * (sms > 0 ? sms : 1); }
 size_t left_bytes(int sms) { return align256((size_t)ctas_of(sms) * 4 * sizeof(int4)); }
 size_t part_bytes(int d, int rows, int sms) { return align256((size_t)ctas_of(sms) * 2 * cols_of(rows) * (d + 3) * sizeof(float)); }
-// Two areas per CTA for the units of its part of the split axis (at least kWarps).
-size_t logit_bytes(int64_t cost, int d, int rows, int sms) {
-    return align256((size_t)2 * (cost + (int64_t)ctas_of(sms) * (kWarps + 1)) * unit_of(d) * cols_of(rows) * sizeof(float));
+// For every number of CTAs per SM, which goes by the batch and by the rows of a pass.
+size_t logit_bytes(int64_t cost, int cap, int d, int rows, int sms) {
+    int64_t units = 0;
+    for (int n = 1; n <= kMaxPerSm; ++n) {
+        const int grid = qattn_grid(cost, ctas_of(sms) / kMaxPerSm * n);
+        const int64_t u = grid * qattn_area(cost, grid, units_of(cap, d));
+        units = u > units ? u : units;
+    }
+    return align256((size_t)units * unit_of(d) * cols_of(rows) * sizeof(float));
 }
 
 }  // namespace
 
-size_t qattn_scratch(int batch, int kv_heads, int cap, int d, int heads, int n_q, int sms) {
+size_t qattn_scratch(int batch, int kv_heads, int cap, int d, int heads, int n_q, bool weights, int sms) {
     const int rows = heads / kv_heads * n_q;
-    return left_bytes(sms) + part_bytes(d, rows, sms) + logit_bytes(cost_of(batch, kv_heads, cap, d), d, rows, sms);
+    return left_bytes(sms) + part_bytes(d, rows, sms) +
+           (weights ? logit_bytes(cost_of(batch, kv_heads, cap, d), cap, d, rows, sms) : 0);
 }
 
 cudaError_t launch_qattn(const QAttnArgs &a, cudaStream_t s) {
@@ -41,7 +48,7 @@ cudaError_t launch_qattn(const QAttnArgs &a, cudaStream_t s) {
     const int rows = k.group * a.n_q, d = a.c.d;
     k.left = reinterpret_cast<int4 *>(a.scratch);
     k.part = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms));
-    k.logit = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms) + part_bytes(d, rows, a.sms));
+    if (a.weight) k.logit = reinterpret_cast<float *>(a.scratch + left_bytes(a.sms) + part_bytes(d, rows, a.sms));
     const int64_t cost = cost_of(a.c.batch, a.c.heads, a.c.cap, d);
     // a later pass adds its weights to an earlier one's
     for (k.row0 = 0; k.row0 < rows; k.row0 += kPass) {

@@ -75,10 +75,24 @@ struct QAttnK {
     int subs;            // CTAs of the second kernel for each of them
     int4 *left;          // [grid, 2, 2] what the first kernel left to finish (Left)
     float *part;         // [grid, 2] records: per column its maximum, sum and c1, then the sums of p v
-    float *logit;        // [grid, 2, area / RP, RP] x, for the weights
-    int64_t area;        // floats of one CTA's half of logit
+    float *logit;        // [grid, area / RP, RP] x, for the weights (null without weights)
+    int64_t area;        // floats of one CTA's part of logit: a head's end in front, if it has one, then one head at a time
     float c2, sign;      // |scale| log2(e), and the scale's sign
 };
+
+// CTAs of the first kernel where `most` fit the GPU, for an axis of `cost` units at the most.
+inline int qattn_grid(int64_t cost, int64_t most) {
+    const int64_t useful = (cost + kWarps - 1) / kWarps;
+    return (int)(useful < most ? useful : most);
+}
+// The most units whose x one CTA keeps at a time, of heads of up to `head` units: one piece of a head as long as its
+// part of the axis, or the end of one and a piece of another, which has a head's cost in front of it.
+inline int64_t qattn_area(int64_t cost, int grid, int64_t head) {
+    int64_t part = (cost + grid - 1) / grid;
+    if (part < kWarps) part = kWarps;
+    const int64_t one = part < head ? part : head, two = part - kHeadCost < 2 * head ? part - kHeadCost : 2 * head;
+    return one > two ? one : two;
+}
 
 // Query columns per pass and how they sit in the 8 columns of a product.
 enum QMode { PACK4 = 0, ONE8 = 1, TWO8 = 2 };
@@ -635,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
         out_next = v;
     };
     if (s.u0 >= s.u1) return;   // only the last head of a CTA's part can have no unit in it
+    // the x of the head's end that this CTA's part begins with stay; the heads after it follow one another behind them
+    const int64_t front = s.u0 == 0 ? 0 : (int64_t)(s.u1 - s.u0) * C::UT * C::RP;
     int head = fhead;
     fetch_q(s.b, head);   // ahead of the ring's first copies, behind which it would wait
 #pragma unroll 1
@@ -658,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
         T.clear();
         const int newest = by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + k.rows - 1) / k.group : 0;
         const int len = ax.len[s.b];
-        float *lg = k.logit + ((int64_t)blockIdx.x * 2 + (s.u0 == 0)) * k.area;
+        float *lg = k.logit + blockIdx.x * k.area + (s.u0 == 0 ? front : 0);
 
         Seg nx = s;
         bool last = s.next() >= ax.end;
@@ -1181,8 +1197,10 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_join_kernel(QAttnK k) {
         }
         if (k.a.weight) {
             const int n = x.t1 - x.t0, a0 = (int)((int64_t)n * sub / k.subs), a1 = (int)((int64_t)n * (sub + 1) / k.subs);
-            weigh<RP, 4, false>(k, k.logit + ((int64_t)cta * 2 + i) * k.area + (int64_t)a0 * RP, a1 - a0,
-                                c.slot0(x.b, x.head) + x.t0 + a0, base[i], cc1[i], inv[i]);
+            // behind the units of the CTA's first piece, as they were left
+            const int64_t at = i == 0 ? 0 : (s[0].t1 - s[0].t0 + C::UT - 1) / C::UT * C::UT;
+            weigh<RP, 4, false>(k, k.logit + cta * k.area + (at + a0) * RP, a1 - a0, c.slot0(x.b, x.head) + x.t0 + a0, base[i],
+                                cc1[i], inv[i]);
         }
     }
 }
@@ -1194,14 +1212,8 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
     static_assert(C::smem_fixed + (2 * kQMaxBatch + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
     // 228 KB per SM, of which 1 KB per CTA and its static variables are spoken for
     const int fit = (int)(228 * 1024 / (smem + 2048));
-    const int64_t grid = (int64_t)(k.a.sms > 0 ? k.a.sms : 1) * (fit < C::MINB ? fit : C::MINB);
-    const int64_t most = (cost + kWarps - 1) / kWarps;
-    k.grid = (int)(most < grid ? most : grid);
-    // the longest part that a CTA can have, or a whole head, in x
-    int64_t part = (cost + k.grid - 1) / k.grid;
-    if (part < kWarps) part = kWarps;
-    const int64_t head = (k.a.c.cap + C::UT - 1) / C::UT;
-    k.area = (part < head ? part : head) * C::UT * C::RP;
+    k.grid = qattn_grid(cost, (int64_t)(k.a.sms > 0 ? k.a.sms : 1) * (fit < C::MINB ? fit : C::MINB));
+    k.area = qattn_area(cost, k.grid, (k.a.c.cap + C::UT - 1) / C::UT) * C::UT * C::RP;
     const size_t join = 2 * (size_t)k.grid * C::RP * sizeof(float);
     k.subs = 2;   // one wave of four per SM (64 ragged sequences of up to 8,192 slots: 108, 101, 104 us with 1, 2, 3)
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(&qattn_kernel<D, MODE, TWO>));

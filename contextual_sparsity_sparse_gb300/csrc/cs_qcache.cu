@@ -920,11 +920,12 @@ extern "C" {
 
 size_t cs_qcache_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n_q) {
     if (batch < 1 || batch > kQMaxBatch || kv_heads < 1 || kv_heads > kMaxHeads || capacity < 1 || capacity > kMaxCapacity ||
-        d_head < kQGroup || d_head > 256 || d_head % kQGroup || n_heads < kv_heads || n_heads % kv_heads || n_q < 1 ||
-        (int64_t)n_heads / kv_heads * n_q > kQMaxRows)
+        d_head < kQGroup || d_head > 256 || d_head % kQGroup)
         return 0;
-    const size_t attn = qattn_scratch(batch, kv_heads, capacity, d_head, n_heads, n_q, device_sm_count());
     const size_t trim = trim_scratch(batch, kv_heads, capacity);
+    if (n_heads == 0) return kControlBytes + trim;
+    if (n_heads < kv_heads || n_heads % kv_heads || n_q < 1 || (int64_t)n_heads / kv_heads * n_q > kQMaxRows) return 0;
+    const size_t attn = qattn_scratch(batch, kv_heads, capacity, d_head, n_heads, n_q, true, device_sm_count());
     return kControlBytes + (attn > trim ? attn : trim);
 }
 
@@ -1002,7 +1003,7 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
     a.weight = weight;
     a.sms = device_sm_count();
     st = check_qws(ws, ws_bytes,
-                   kControlBytes + qattn_scratch(a.c.batch, a.c.heads, a.c.cap, a.c.d, n_heads, n_q, a.sms), who);
+                   kControlBytes + qattn_scratch(a.c.batch, a.c.heads, a.c.cap, a.c.d, n_heads, n_q, weight != nullptr, a.sms), who);
     if (st != CS_OK) return st;
     a.err = static_cast<uint32_t *>(ws);
     a.scratch = static_cast<char *>(ws) + kControlBytes;

@@ -40,7 +40,8 @@ struct QAttnArgs {
     char *scratch;           // the workspace behind its control words
     int sms;
 };
-size_t qattn_scratch(int batch, int kv_heads, int cap, int d, int heads, int n_q, int sms);
+// weights: whether the call gathers them
+size_t qattn_scratch(int batch, int kv_heads, int cap, int d, int heads, int n_q, bool weights, int sms);
 cudaError_t launch_qattn(const QAttnArgs &a, cudaStream_t s);
 
 __device__ __forceinline__ float q_load1(const QRowsK &r, int64_t i) {

@@ -445,8 +445,13 @@ typedef struct cs_head_rows {
 /*
  * Workspace bytes of the cs_qcache_* calls below on a cache of these sizes,
  * with up to n_heads query heads (a multiple of kv_heads) and n_q query tokens
- * per sequence; 0 for sizes that no call takes.  Initialise it once with
- * cs_workspace_init; cs_get_device_error reads its error word.
+ * per sequence; 0 for sizes that no call takes.  n_heads == 0: for the calls
+ * other than cs_qcache_attention.  Most of the attention's part is for calls that
+ * gather weights: the logits that one CTA keeps at a time, together at most the
+ * cache's slots x query columns (4, 8 or 16) x 4 bytes, and 15 MB.  A call without
+ * weights needs no more than this gives for a capacity of 1, and nor do append,
+ * read and evict.  Initialise it once with cs_workspace_init;
+ * cs_get_device_error reads its error word.
  */
 size_t cs_qcache_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n_q);
 
