@@ -752,6 +752,18 @@ __global__ void __launch_bounds__(256) qtrim_kernel(QEvictCall a, QCacheK dst) {
     }
 }
 
+// The weights of a step without query tokens: nothing is added to what the slots had.
+constexpr int kDecayThreads = 256, kDecaySlots = 4096;
+__global__ void __launch_bounds__(kDecayThreads) qdecay_kernel(QAttnArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int used = q_length(a.length, b, a.c.cap, a.err), t0 = blockIdx.x * kDecaySlots, t1 = min(used, t0 + kDecaySlots);
+    const int64_t slot0 = a.c.slot0(b, h);
+    for (int t = t0 + threadIdx.x; t < t1; t += kDecayThreads)
+        a.weight[slot0 + t] = a.decay == 0.f ? 0.f : a.decay * ld_dep(a.c.weight + slot0 + t);
+}
+
 // Launches the choice of slots for rows of up to `cap` slots.
 template <int T, int K>
 cudaError_t launch_evict(const QEvictCall &a, int ctas, cudaStream_t s) {
@@ -1007,8 +1019,10 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
     if (st != CS_OK) return st;
     a.err = static_cast<uint32_t *>(ws);
     a.scratch = static_cast<char *>(ws) + kControlBytes;
-    if (n_q == 0) return CS_OK;
-    const cudaError_t e = launch_qattn(a, (cudaStream_t)stream);
+    if (n_q == 0 && !weight) return CS_OK;
+    const cudaError_t e = n_q > 0 ? launch_qattn(a, (cudaStream_t)stream)
+                                  : launch(qdecay_kernel, dim3((a.c.cap + kDecaySlots - 1) / kDecaySlots, a.c.heads, a.c.batch),
+                                           dim3(kDecayThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 

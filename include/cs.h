@@ -497,8 +497,8 @@ cs_status cs_qcache_read(const cs_qcache *cache, const cs_head_rows *k, const cs
  *   scale: the factor on q . k; 0 means 1 / sqrt(d_head).
  *   weight: device fp32 or NULL, laid out like cache->weight (and allowed to
  *      be it): weight[i] = decay * cache->weight[i] + the sum of p_i over the
- *      head's group and the n_q tokens, for i < length[b]; other slots are not
- *      written.  decay == 0 reads no old weights.
+ *      head's group and the n_q tokens (which may be none), for i < length[b];
+ *      other slots are not written.  decay == 0 reads no old weights.
  * A row that sees no slot, and a head that is not chosen, gives zeros and
  * adds no weight.  Sums and softmax statistics are fp32; with the same
  * arguments the results are the same bit for bit.
