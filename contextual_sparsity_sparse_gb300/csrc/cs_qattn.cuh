@@ -232,6 +232,11 @@ __device__ __forceinline__ bool row_on(const QAttnK &k, int b, int h, int r) {
     return ld_dep(k.a.mask + (int64_t)b * ((k.a.heads + 31) / 32) + (j >> 5)) >> (j & 31) & 1u;
 }
 
+// The last position that a row sees; past the largest there is, that.
+__device__ __forceinline__ int last_seen(const QAttnK &k, int b, int r) {
+    return (int)min((int64_t)ld_dep(k.a.q_pos + b) + (k.row0 + r) / k.group, (int64_t)INT_MAX);
+}
+
 // How many cache heads have a chosen query head; the whole warp asks together.
 __device__ __forceinline__ int heads_on(const QAttnK &k, int b) {
     if (!k.a.mask) return k.a.c.heads;
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 out_next[row] = out_at(k, b, h, row);
                 // takes the products back; kept where x c1 stays in fp32's range (beyond, one slot takes all as well)
                 cc[0] = fminf(fmaxf(k.c2 * exp2f((float)((TWO ? 0 : 24) - up)), 1.2e-38f), 1.2e30f);
-                cc[1] = __int_as_float(by_pos ? ld_dep(k.a.q_pos + b) + (k.row0 + row) / k.group : INT_MAX);
+                cc[1] = __int_as_float(by_pos ? last_seen(k, b, row) : INT_MAX);
                 cc[2] = row_on(k, b, h, row) ? 1.f : 0.f;
 #pragma unroll
                 for (int g = 0; g < C::G; ++g) cc[3 + g] = sum[g] * (TWO ? 1.f : 5.9604644775390625e-8f);   // 2^-24, as the products
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                 for (int g = 0; g < C::G; ++g) zq[n][i][g] = MODE == PACK4 && j >= 2 ? 0.f : cc[3 + g];
             }
         T.clear();
-        const int newest = by_pos ? ld_dep(k.a.q_pos + s.b) + (k.row0 + k.rows - 1) / k.group : 0;
+        const int newest = by_pos ? last_seen(k, s.b, k.rows - 1) : 0;
         const int len = ax.len[s.b];
         float *lg = k.logit + blockIdx.x * k.area + (s.u0 == 0 ? front : 0);
 
