@@ -515,6 +515,11 @@ __device__ __forceinline__ void fetch(const QAttnK &k, uint32_t stage, int64_t s
         cp_async_or0<4>(stage + C::UT * (2 * C::RB + C::G * 8) + lane * 4, lane < n ? c.pos + slot0 + lane : c.pos, lane < n);
 }
 
+// Slots that 16-bit outputs sum up in one chain of cut off products per warp (an eighth of them each).  Over 131,072 slots
+// of one head and CTA a chain lost 2e-5 to 6e-5 of a flat average, an eighth of fp16's half step at the most; over 2^24 it
+// would lose bf16's.  Longer pieces take the fp32 outputs' kernel, which loses nothing.
+constexpr int64_t kChain = 131072;
+
 // TWO: q has a second part, p s a third, and sums are kept to fp32's precision.
 template <int D, int MODE, bool TWO>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAttnK k) {
@@ -1232,7 +1237,10 @@ cudaError_t run(QAttnK k, int64_t cost, cudaStream_t s) {
 
 template <int D>
 cudaError_t run_qattn(QAttnK k, int mode, int64_t cost, cudaStream_t s) {
-    const bool two = k.a.q.dt == CS_F32;
+    // with one CTA per SM, the longest piece of a head that a CTA can have
+    constexpr int UT = Cfg<D, TWO8>::UT;
+    const int64_t head = (k.a.c.cap + UT - 1) / UT, part = cost / (k.a.sms > 0 ? k.a.sms : 1), piece = part < head ? part : head;
+    const bool two = k.a.q.dt == CS_F32 || piece * UT > kChain;
     if (mode == PACK4) return two ? run<D, PACK4, true>(k, cost, s) : run<D, PACK4, false>(k, cost, s);
     if (mode == ONE8) return two ? run<D, ONE8, true>(k, cost, s) : run<D, ONE8, false>(k, cost, s);
     return two ? run<D, TWO8, true>(k, cost, s) : run<D, TWO8, false>(k, cost, s);

@@ -143,3 +143,27 @@ def test_wide_slots_first(group, d, dt):
     kn[:, :, :S // 2, 0] = 4
     vs[:, :, :S // 2, :, 0] *= 2.0 ** 17
     check(kn, ks, vn, vs, q, dt)
+
+
+@pytest.mark.parametrize("group", [1, 8])
+def test_long_heads_of_16_bits_do_not_drift(group):
+    """304 heads of 400,000 slots: a CTA has a whole head or more to itself, and a warp of it sums up 50,000 slots.  All slots
+    weigh the same and a channel's code is the same in all of them (12 to 15), so the output is a mean that is easily told.
+    A rounding to fp16 is off by 2^-11 / sqrt(3) at the most in the mean square, and over 304 x 4 values that is 2^-11 / 60 =
+    8e-6 of the mean; four times that are allowed."""
+    B, kv, S, d = 38, 8, 400_000, 64
+    g = torch.Generator("cuda").manual_seed(group)
+    k = torch.zeros(B, kv, S, d // 2, dtype=torch.uint8, device="cuda")
+    v = torch.tensor([0xdc, 0xfe], dtype=torch.uint8, device="cuda").repeat(d // 4).expand(B, kv, S, d // 2).contiguous()
+    ks = torch.zeros(B, kv, S, 1, 2, dtype=torch.float16, device="cuda")
+    vs = torch.rand(B, kv, S, 1, 2, generator=g, device="cuda").add_(0.5).half()
+    cache = cs.QCache(k, v, ks, vs)
+    q = torch.zeros(B, 1, kv * group, d, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(q)
+    ws = cs.QCacheWorkspace(cache, n_heads=kv * group, weights=False)
+    cs.cs_qcache_attention(cache, q, torch.full((B,), S, dtype=torch.int32, device="cuda"), out, ws)
+    code = torch.tensor([12, 13, 14, 15], dtype=torch.float64, device="cuda").repeat(d // 4)
+    s, z = (vs[..., 0, i].double().mean(-1)[..., None] for i in (0, 1))
+    want = (z + s * code).view(B, 1, kv, 1, d)
+    rel = out.double().view(B, 1, kv, group, d) / want - 1
+    assert rel.mean().abs() <= 4 * 2.0 ** -11 / 60 and rel.abs().max() <= 2.0 ** -11 + 1e-5
