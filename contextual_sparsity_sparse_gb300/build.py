@@ -70,13 +70,13 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         qcall = ex.submit(compile_qcall)
         objs = list(ex.map(compile_one, srcs))
-        qcall.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = ["nvcc", *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    qcall.result()   # told after the library is there: only the cache calls need the module
     return LIB
 
 
