@@ -234,7 +234,8 @@ __device__ __forceinline__ bool row_on(const QAttnK &k, int b, int h, int r) {
 
 // The last position that a row sees; past the largest there is, that.
 __device__ __forceinline__ int last_seen(const QAttnK &k, int b, int r) {
-    return (int)min((int64_t)ld_dep(k.a.q_pos + b) + (k.row0 + r) / k.group, (int64_t)INT_MAX);
+    const int t = (k.row0 + r) / k.group;
+    return min(ld_dep(k.a.q_pos + b), INT_MAX - t) + t;
 }
 
 // How many cache heads have a chosen query head; the whole warp asks together.
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
     };
     if (s.u0 >= s.u1) return;   // only the last head of a CTA's part can have no unit in it
     // the x of the head's end that this CTA's part begins with stay; the heads after it follow one another behind them
-    const int64_t front = s.u0 == 0 ? 0 : (int64_t)(s.u1 - s.u0) * C::UT * C::RP;
+    const int front = s.u0 == 0 ? 0 : s.u1 - s.u0;
     int head = fhead;
     fetch_q(s.b, head);   // ahead of the ring's first copies, behind which it would wait
 #pragma unroll 1
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
         T.clear();
         const int newest = by_pos ? last_seen(k, s.b, k.rows - 1) : 0;
         const int len = ax.len[s.b];
-        float *lg = k.logit + blockIdx.x * k.area + (s.u0 == 0 ? front : 0);
+        float *lg = k.logit + blockIdx.x * k.area + (s.u0 == 0 ? front : 0) * (int64_t)(C::UT * C::RP);
 
         Seg nx = s;
         bool last = s.next() >= ax.end;
