@@ -27,7 +27,8 @@
 // straight from their packed words.  For the keys, in fp16, 16 slots x 16 channels: a
 // nibble ANDed out of a word is an fp16 subnormal n 2^-24 (or, four bits up,
 // n 2^-20), exact in the product; the factor 16 goes into q, and the sums start
-// at -8 (sum q).  For the values, in bf16, 16 channels x 16 slots: two slots' words are
+// at -8 (sum q); where n - 8 itself is the operand, n is ORed into the fraction of 1024 and 1032 subtracted (Kim, Henry,
+// Fahim and Awadalla, "Who Says Elephants Can't Run", 2022).  For the values, in bf16, 16 channels x 16 slots: two slots' words are
 // interleaved by byte permutes, and a nibble ANDed out is bf16's n 2^-133 (four bits
 // up n 2^-129: the bit that leaves the fraction is the exponent's lowest, and the least
 // exponent has the subnormals' steps); one multiply-add by 2^127 takes it to (n - 8) / 64 (or / 4).
@@ -47,10 +48,13 @@
 // after 24 bits) move fp32 outputs by 2^-21 X of the terms at most.
 //
 // Bound (64 ragged sequences of up to 8,192 slots, 64 over 8 heads of 128, bf16:
-// 100 us of which the bytes need 47): 850 instructions per unit of 32 slots, 200
-// for the keys, 310 for p and the values, 90 for the maxima and x, 250 for
-// copies, heads' starts and joins; with all of a unit's arithmetic left out the
-// copies and joins alone take 81 us.  What else was tried: four warps to a CTA,
+// 107 us of which the bytes need 47): 900 instructions per unit of 32 slots, of which some
+// 200 are for the keys, 360 for p and the values, 80 for the maxima and x, 250 for
+// copies, heads' starts and joins.  The first kernel issues in 62% of its cycles, keeps
+// the tensor pipe busy for 27% and moves 374 MB in 90 us (62% of a copy's rate, the
+// logits that it leaves included).  When the call took 100 us, its
+// copies and joins alone, with all of a unit's arithmetic left out, took 81, and of one long sequence's 47 us 36.
+// What else was tried then: four warps to a CTA,
 // four CTAs to an SM, 126 us; one CTA of 8, 12 or 16 warps per SM with more
 // registers, 118, 114, 119 us; keys and values of a stage replaced one after
 // the other as they are used, 109 us.
@@ -63,8 +67,13 @@ namespace cs {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPerSm = 2;   // CTAs of the first kernel
-// A head's fixed cost on the axis in units.  64 ragged sequences of up to 8,192 slots with 8, 16, 24, 32, 48:
-// 123, 112, 101, 102, 104 us; 32 of up to 4,096 slots of 64 channels: 62, 47, 42, 42, 44 us.
+// A head's fixed cost on the axis in units: 8, 16, 24, 32, 48 for
+//   64 ragged sequences of up to 8,192 slots (8 rows, 128 channels, bf16): 129, 116, 106, 107, 111 us
+//   the same in fp32: 144, 128, 129, 131, 135; without weights: 107, 93, 86, 87, 91; 4 rows: 116, 100, 93, 93, 97
+//   32 of up to 4,096 of 64 channels, 16 rows: 63, 47, 43, 44, 47; 16 of 128 channels, 16 rows: 55, 45, 42, 44, 46
+//   16 of 192 channels: 57, 49, 41, 41, 37; of 256: 67, 57, 49, 46, 43, 16 rows: 102, 88, 80, 73, 73
+//   40 heads of 2,048 slots: 14.0, 14.0, 13.9, 14.4, 15.0; one sequence of 131,001: 49.5, 48.5, 48.3, 48.4, 46.0
+// So 24 is the best or near it up to 128 channels; wide rows (one CTA per SM) would take 10% less with 48.
 constexpr int kHeadCost = 24;
 
 struct QAttnK {

@@ -177,8 +177,9 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[kPart], float lo, flo
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// Bound by issue slots, not by memory.  Three CTAs per SM: 7,999 tokens of 8 heads of 128 with their read-back take
-// 25.5 us; two 28.8, four (64 registers) 26.5, five 35.7.
+// 7,999 tokens of 8 heads of 128, bf16: 21 us alone, issuing in 57% of its cycles, with DRAM at 23% of a copy's rate, so
+// bound by neither: a thread loads its rows, waits, quantises and stores once (fp32 20.9 us, fp16 20.4).  With the
+// read-back, in a graph: three CTAs per SM 25.5 us, two 28.8, four (64 registers) 26.5, five 35.7.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowThreads, 3) qappend_kernel(QRowsCall a) {
     pdl_wait();
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads) qread_kernel(QRowsCall a) {
             half2x(sz[i][v], s, z);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                // nibbles e and e + 4 as fp16 1024 + n, less 1024
+                // nibbles e and e + 4 as fp16 1024 + n, less 1024 (Kim et al., "Who Says Elephants Can't Run", 2022)
                 const uint32_t w = (codes[i][v] >> (4 * e) & 0x000f000fu) | 0x64006400u;
                 const float2 n = __half22float2(__hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1024.f)));
                 x[e] = fmaf(s, n.x, z);
@@ -514,7 +515,8 @@ __device__ uint4 reduce_stat(EvictShared<T> &sh, cg::cluster_group &cl, uint32_t
 }
 
 template <int T, int K>
-// Two CTAs of 512 per SM (512 rows of 8,192 slots: 12.0 us; with registers for one 16.2, for three, spilling, 13.0).
+// Two CTAs of 512 per SM: 512 full rows of 8,192 slots give up one slot each in 23.7 us, 37 in 26.3 (with registers for one
+// CTA 33.9 and 35.8, for three, spilling, 24.0 and 26.7); rows of 4,096 15.4 and 16.4 (22.4 and 23.5; 14.2 and 15.5).
 __global__ void __launch_bounds__(T, 1024 / T) qevict_kernel(QEvictCall a) {
     __shared__ EvictShared<T> sh;
     cg::cluster_group cl = cg::this_cluster();

@@ -416,10 +416,10 @@ cs_status cs_fit_predictor(const cs_ffn_layer *layer, cs_predictor *pred, const 
  *   ld_batch, ld_head: slots from one sequence (head) to the next, the same
  *                     for all six arrays; 0 means dense.
  * d_head is 64, 128, 192 or 256; batch <= 4096; k and v 16-byte aligned, the
- * scales 4-byte (d_head 128: 8, 256: 16), weight and pos 4-byte.  Which slots of a sequence are in use is the caller's to
- * keep: calls take the number per sequence (slots 0 .. length - 1), one
- * number for all heads, and none of them changes it.  One cache object stands
- * for one layer.
+ * scales 4-byte (d_head 128: 8, 256: 16), weight and pos 4-byte.  Which slots
+ * of a sequence are in use is the caller's to keep: calls take the number per
+ * sequence (slots 0 .. length - 1), one number for all heads, and none of them
+ * changes it.  One cache object stands for one layer.
  */
 typedef struct cs_qcache {
     int batch, n_heads, d_head, capacity;
@@ -474,9 +474,11 @@ cs_status cs_qcache_append(const cs_qcache *cache, const cs_head_rows *k, const 
                            void *ws, size_t ws_bytes, cs_stream_t stream);
 
 /*
- * The values that slots stand for, offset + scale * code, rounded once to the
- * output's dtype.  Slots are given as in cs_qcache_append; one outside
- * [0, capacity) gives a zero row (and sets CS_DEVERR_INDEX unless it is -1).
+ * The values that slots stand for, offset + scale * code, rounded to fp32 and
+ * from there, for 16-bit outputs, to the output's dtype (a group that spans
+ * nearly +-65504 stands for values up to 65536, an infinity in fp16).  Slots
+ * are given as in cs_qcache_append; one outside [0, capacity) gives a zero row
+ * (and sets CS_DEVERR_INDEX unless it is -1).
  */
 cs_status cs_qcache_read(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n,
                          const int32_t *start, const int32_t *slots, void *ws, size_t ws_bytes,
@@ -500,8 +502,9 @@ cs_status cs_qcache_read(const cs_qcache *cache, const cs_head_rows *k, const cs
  *      head's group and the n_q tokens (which may be none), for i < length[b];
  *      other slots are not written.  decay == 0 reads no old weights.
  * A row that sees no slot, and a head that is not chosen, gives zeros and
- * adds no weight.  Sums and softmax statistics are fp32; with the same
- * arguments the results are the same bit for bit.
+ * adds no weight.  Sums and softmax statistics are fp32; the weights of slots
+ * go into the value products with 16 bits for 16-bit outputs and 24 for
+ * fp32.  With the same arguments the results are the same bit for bit.
  */
 cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int n_heads, int n_q,
                               const int32_t *length, const int32_t *q_pos, const uint32_t *mask, float scale,
@@ -513,8 +516,8 @@ cs_status cs_qcache_attention(const cs_qcache *cache, const cs_head_rows *q, int
  * most `limit` slots may be in use: first the slots given up among the
  * length[b] used ones (as many as the free ones fall short of n), then free
  * ones from length[b] on, all ascending.  Given up are the first of this
- * order: empty slots (pos < 0); then by weight, least first; then protected
- * slots, least weight first.  Equal weights go by the lower slot, -0 equals
+ * order: empty slots (pos < 0), then others, then protected ones, each class
+ * by weight, least first.  Equal weights go by the lower slot, -0 equals
  * +0, and NaN is below every number.  Protected are the tokens at positions
  * below `sinks` and at next_pos[b] - recent or later.  Needs weights only
  * (and positions, if the cache has them): k, v and the scales may be NULL.
