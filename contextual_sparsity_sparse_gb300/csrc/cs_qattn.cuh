@@ -37,7 +37,7 @@
 // are not what bounds this kernel, the instructions around them are.
 //
 // Precision.  q is scaled by a power of two and split into two fp16 parts (22
-// bits; the second is zero for 16-bit inputs).  p s goes in bf16 parts of 8 bits each:
+// bits, or steps of 2^-35 of the row's largest channel; the second is zero for 16-bit inputs).  p s goes in bf16 parts of 8 bits each:
 // two for 16-bit outputs (what is left out is 2^-17 of a term or less, beside output roundings of 2^-8 and
 // 2^-11), three for fp32 ones (2^-26).  bf16 has fp32's range, so a term keeps its bits however
 // small it is beside others: fp16 parts under one power of two for a warp's slots, rows and groups cost the others
