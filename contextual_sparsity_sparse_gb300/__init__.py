@@ -35,7 +35,9 @@ EXPORTS = ["cs_version", "cs_status_string", "cs_last_error", "cs_workspace_size
            "cs_stack_release", "cs_sparse_ffn_noalloc", "cs_decode_layer", "cs_permute_rows",
            "cs_hot_order", "cs_fit_scratch_size", "cs_fit_predictor", "cs_sparse_attention",
            "cs_decode_attention", "cs_qcache_workspace_size", "cs_qcache_append", "cs_qcache_read",
-           "cs_qcache_attention", "cs_qcache_evict", "cs_qcache_trim"]
+           "cs_qcache_attention", "cs_qcache_evict", "cs_qcache_trim", "cs_qcache_append_rows",
+           "cs_qcache_fork", "cs_qcache_tree_workspace_size", "cs_qcache_tree_attention",
+           "cs_prompt_workspace_size", "cs_prompt_attention"]
 
 
 class CsError(RuntimeError):
@@ -126,12 +128,21 @@ def lib():
             L.cs_qcache_attention.argtypes = [QC, HR, I, I, P, P, P, C.c_float, C.c_float, P, HR, P, S, P]
             L.cs_qcache_evict.argtypes = [QC, P, I, I, P, I, I, P, P, S, P]
             L.cs_qcache_trim.argtypes = [QC, P, I, P, I, I, QC, P, S, P]
+            L.cs_qcache_append_rows.argtypes = [QC, HR, HR, I, P, I, P, P, P, P, S, P]
+            L.cs_qcache_fork.argtypes = [QC, P, P, QC, P, S, P]
+            L.cs_qcache_tree_workspace_size.argtypes = [I] * 6
+            L.cs_qcache_tree_workspace_size.restype = S
+            L.cs_qcache_tree_attention.argtypes = [QC, HR, HR, HR, I, I, P, P, P, C.c_float, HR, P, S, P]
+            L.cs_prompt_workspace_size.argtypes = [I] * 6
+            L.cs_prompt_workspace_size.restype = S
+            L.cs_prompt_attention.argtypes = [HR, HR, HR, I, I, I, I, P, I, P, I, I, C.c_float, HR, P, S, P]
             for name in ("cs_workspace_init", "cs_get_device_error", "cs_pack_transpose",
                          "cs_predict", "cs_select", "cs_sparse_ffn", "cs_exact_ffn",
                          "cs_union_mask", "cs_decode_stack", "cs_stack_release",
                          "cs_sparse_ffn_noalloc", "cs_decode_layer", "cs_permute_rows", "cs_hot_order",
                          "cs_fit_predictor", "cs_sparse_attention", "cs_decode_attention", "cs_qcache_append",
-                         "cs_qcache_read", "cs_qcache_attention", "cs_qcache_evict", "cs_qcache_trim"):
+                         "cs_qcache_read", "cs_qcache_attention", "cs_qcache_evict", "cs_qcache_trim",
+                         "cs_qcache_append_rows", "cs_qcache_fork", "cs_qcache_tree_attention", "cs_prompt_attention"):
                 getattr(L, name).restype = I
             _lib = L
     return _lib
@@ -488,7 +499,7 @@ _qcall = None
 
 
 def _q():
-    """The native marshalling of the qcache calls (csrc/qcall.c), bound to libcs.so."""
+    """The native marshalling of the qcache calls and cs_prompt_attention (csrc/qcall.c), bound to libcs.so."""
     global _qcall
     if _qcall is None:
         L = lib()
@@ -496,8 +507,9 @@ def _q():
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.init(torch.float32, torch.float16, torch.bfloat16, torch.int32,
-               *(C.cast(getattr(L, f"cs_qcache_{f}"), C.c_void_p).value
-                 for f in ("append", "read", "attention", "evict", "trim")))
+               *(C.cast(getattr(L, f"cs_{f}"), C.c_void_p).value
+                 for f in ("qcache_append", "qcache_read", "qcache_attention", "qcache_evict", "qcache_trim",
+                           "qcache_append_rows", "qcache_fork", "qcache_tree_attention", "prompt_attention")))
         _qcall = m
     return _qcall
 
@@ -546,6 +558,66 @@ def cs_qcache_trim(cache: QCache, length, keep, dst: QCache, ws: QCacheWorkspace
     """Copy each head's `keep` heaviest slots to the front of dst (see
     include/cs.h)."""
     _check(_q().trim(cache.addr, length, keep, dst.addr, next_pos, sinks, recent, ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def cs_qcache_append_rows(cache: QCache, k, v, rows, ws: QCacheWorkspace, start=None, slots=None, pos=None, stream=None):
+    """Quantise rows rows[b, t] of k and v [n_rows, n_heads, d_head] (-1: no
+    token) into slots start[b] + t, or slots[b, h, t] (see include/cs.h)."""
+    _check(_q().append_rows(cache.addr, k, v, rows, start, slots, pos, ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def cs_qcache_fork(cache: QCache, source, length, ws: QCacheWorkspace, dst: QCache = None, stream=None):
+    """Sequence i of dst (of cache itself, if None) becomes sequence source[i]
+    of cache, its first length[source[i]] slots; -1 leaves it as it is (see
+    include/cs.h)."""
+    _check(_q().fork(cache.addr, source, length, 0 if dst is None else dst.addr, ws.ptr, ws.nbytes, _stream(stream)))
+
+
+class _Scratch:
+    """Device workspace of `nbytes` bytes, initialised."""
+
+    def __init__(self, nbytes, device, stream):
+        if nbytes == 0:
+            raise ValueError("no call takes these sizes")
+        self.nbytes = nbytes
+        self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        self.ptr = (self.buf.data_ptr() + 255) & ~255
+        _check(lib().cs_workspace_init(self.ptr, self.nbytes, _stream(stream)))
+
+
+class QCacheTreeWorkspace(_Scratch):
+    """Device workspace of cs_qcache_tree_attention on caches of this one's
+    sizes, with up to n_heads query heads and n drafted tokens per sequence."""
+
+    def __init__(self, cache: QCache, n_heads, n, device=None, stream=None):
+        super().__init__(lib().cs_qcache_tree_workspace_size(cache.batch, cache.n_heads, cache.capacity, cache.d_head,
+                                                             int(n_heads), int(n)), device or cache.k.device, stream)
+
+
+def cs_qcache_tree_attention(cache: QCache, q, k, v, length, out, ws: QCacheTreeWorkspace, parent=None, n_new=None,
+                             scale=0.0, stream=None):
+    """Attention of the drafted tokens q [batch, n, n_heads, d_head] over the
+    first length[b] slots, their ancestors among k and v [batch, n, kv_heads,
+    d_head] by parent [batch, n] (-1: none; None: a chain), and themselves,
+    into out (see include/cs.h)."""
+    _check(_q().tree(cache.addr, q, k, v, length, out, parent, n_new, scale, ws.ptr, ws.nbytes, _stream(stream)))
+
+
+class PromptWorkspace(_Scratch):
+    """Device workspace of cs_prompt_attention for up to `batch` sequences of
+    together up to q_total query tokens and k_total keys."""
+
+    def __init__(self, batch, n_heads, kv_heads, d_head, q_total, k_total=None, device="cuda", stream=None):
+        super().__init__(lib().cs_prompt_workspace_size(int(batch), int(n_heads), int(kv_heads), int(d_head), int(q_total),
+                                                        int(q_total if k_total is None else k_total)), device, stream)
+
+
+def cs_prompt_attention(q, k, v, out, q_start, ws: PromptWorkspace, k_start=None, causal=True, scale=0.0, stream=None):
+    """Attention of packed prompts: sequence b's query tokens are rows
+    q_start[b] .. q_start[b + 1] - 1 of q and out [tokens, n_heads, d_head], its
+    keys and values the rows of k and v [tokens, kv_heads, d_head] that k_start
+    (None: q_start) gives (see include/cs.h)."""
+    _check(_q().prompt(q, k, v, out, q_start, k_start, causal, scale, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def cs_stack_release():

@@ -21,6 +21,8 @@ struct QRowsCall {
     QRowsK k, v;
     int n;
     const int32_t *start, *slots, *n_new, *pos;
+    const int32_t *rows;     // [batch, n] the rows of k and v, or null: row (b, t)
+    int n_rows;
     uint32_t *err;
     uint32_t mul, shift;     // x / n = (x mul) >> shift for x < 2^31
 };
@@ -180,7 +182,9 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[kPart], float lo, flo
 // 7,999 tokens of 8 heads of 128, bf16: 21 us alone, issuing in 57% of its cycles, with DRAM at 23% of a copy's rate, so
 // bound by neither: a thread loads its rows, waits, quantises and stores once (fp32 20.9 us, fp16 20.4).  With the
 // read-back, in a graph: three CTAs per SM 25.5 us, two 28.8, four (64 registers) 26.5, five 35.7.
-template <int D, typename T>
+// ROWS: token t's row is rows[b, t] of all sequences' rows (64 x 6 tokens of 8 heads, 4 us; what the lookup
+// costs shows only there, so that the rows in order keep a kernel of their own).
+template <int D, typename T, bool ROWS>
 __global__ void __launch_bounds__(kRowThreads, 3) qappend_kernel(QRowsCall a) {
     pdl_wait();
     pdl_launch_dependents();
@@ -196,15 +200,23 @@ __global__ void __launch_bounds__(kRowThreads, 3) qappend_kernel(QRowsCall a) {
     // the rows' loads do not wait for their slots
     const RowPart<D, kPart> p(a, limit, blockIdx.x);
     Raw8<T> raw[2][2] = {};
-    if (p.row) {
-        const int64_t ki = b * a.k.ldb + p.t * a.k.ldt + p.h * a.k.ldh + p.c, vi = b * a.v.ldb + p.t * a.v.ldt + p.h * a.v.ldh + p.c;
+    bool row = p.row;
+    int64_t from = p.t;
+    if (ROWS) {
+        from = row ? ld_dep(a.rows + (int64_t)b * a.n + p.t) : -1;
+        row = from >= 0 && from < a.n_rows;
+        if (!row && from != -1) atomicOr(a.err, CS_DEVERR_INDEX);
+    }
+    if (row) {
+        const int64_t seq = ROWS ? 0 : b;
+        const int64_t ki = seq * a.k.ldb + from * a.k.ldt + p.h * a.k.ldh + p.c, vi = seq * a.v.ldb + from * a.v.ldt + p.h * a.v.ldh + p.c;
         raw[0][0].load(a.k, ki);
         raw[0][1].load(a.k, ki + 8);
         raw[1][0].load(a.v, vi);
         raw[1][1].load(a.v, vi + 8);
     }
     const int first = a.pos ? ld_dep(a.pos + b) : 0;
-    const int slot = p.row ? slot_of(a, b, p.h, p.t) : -1;
+    const int slot = row ? slot_of(a, b, p.h, p.t) : -1;
     const int64_t at = slot >= 0 ? a.c.slot0(b, p.h) + slot : 0;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -799,19 +811,9 @@ cudaError_t choose_slots(const QEvictCall &a, cudaStream_t s) {
     return launch(qevict_long_kernel, dim3(a.c.heads, a.c.batch), dim3(kLongThreads), 0, s, pdl_enabled(), a);
 }
 
+}  // namespace
+
 // ------------------------------------------------------------------- host side
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-#define CS_CHECK(cond, ...)                       \
-    do {                                          \
-        if (!(cond)) {                            \
-            set_error(__VA_ARGS__);               \
-            return CS_ERR_INVALID;                \
-        }                                         \
-    } while (0)
-
-constexpr int kMaxHeads = 1024, kMaxCapacity = 1 << 24, kMaxTokens = 1 << 24;
 
 // codes: whether the call reads or writes k, v and their scales.
 cs_status check_cache(const cs_qcache *q, bool codes, const char *who, QCacheK *out) {
@@ -871,6 +873,8 @@ cs_status check_qws(void *ws, size_t ws_bytes, size_t need, const char *who) {
     return CS_OK;
 }
 
+namespace {
+
 cs_status check_evict(const cs_qcache *q, const int32_t *length, const int32_t *next_pos, int sinks, int recent,
                       const char *who) {
     CS_CHECK(q->weight, "%s: the cache has no weights", who);
@@ -898,11 +902,23 @@ dim3 rows_grid(const QRowsCall &a, int each) {
     return dim3((unsigned)((rows + each - 1) / each), a.c.batch);
 }
 
+template <bool ROWS>
+cudaError_t launch_append(const QRowsCall &a, cudaStream_t s) {
+    return by_d(a.c.d, [&](auto d) {
+        auto go = [&](auto kernel) {
+            return launch(kernel, rows_grid(a, RowPart<d(), kPart>::ROWS), dim3(kRowThreads), 0, s, pdl_enabled(), a);
+        };
+        return a.k.dt == CS_F32   ? go(qappend_kernel<d(), float, ROWS>)
+               : a.k.dt == CS_F16 ? go(qappend_kernel<d(), __half, ROWS>)
+                                  : go(qappend_kernel<d(), __nv_bfloat16, ROWS>);
+    });
+}
+
 cs_status rows_call(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n, const int32_t *start,
-                    const int32_t *slots, void *ws, size_t ws_bytes, const char *who, QRowsCall *a) {
+                    const int32_t *slots, void *ws, size_t ws_bytes, const char *who, QRowsCall *a, bool empty = false) {
     cs_status st = check_cache(cache, true, who, &a->c);
-    if (st == CS_OK) st = check_rows(k, n == 0, "k", who, &a->k);
-    if (st == CS_OK) st = check_rows(v, n == 0, "v", who, &a->v);
+    if (st == CS_OK) st = check_rows(k, n == 0 || empty, "k", who, &a->k);
+    if (st == CS_OK) st = check_rows(v, n == 0 || empty, "v", who, &a->v);
     if (st != CS_OK) return st;
     CS_CHECK(k->dtype == v->dtype, "%s: k and v differ in dtype", who);
     CS_CHECK(n >= 0 && n <= kMaxTokens, "%s: n=%d outside [0, %d]", who, n, kMaxTokens);
@@ -919,7 +935,8 @@ cs_status rows_call(const cs_qcache *cache, const cs_head_rows *k, const cs_head
     a->n = n;
     a->start = start;
     a->slots = slots;
-    a->n_new = a->pos = nullptr;
+    a->n_new = a->pos = a->rows = nullptr;
+    a->n_rows = 0;
     a->err = static_cast<uint32_t *>(ws);
     return check_qws(ws, ws_bytes, kControlBytes, who);
 }
@@ -955,14 +972,27 @@ cs_status cs_qcache_append(const cs_qcache *cache, const cs_head_rows *k, const 
     a.n_new = n_new;
     a.pos = pos;
     if (n == 0) return CS_OK;
-    const cudaError_t e = by_d(a.c.d, [&](auto d) {
-        auto go = [&](auto kernel) {
-            return launch(kernel, rows_grid(a, RowPart<d(), kPart>::ROWS), dim3(kRowThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
-        };
-        return a.k.dt == CS_F32   ? go(qappend_kernel<d(), float>)
-               : a.k.dt == CS_F16 ? go(qappend_kernel<d(), __half>)
-                                  : go(qappend_kernel<d(), __nv_bfloat16>);
-    });
+    const cudaError_t e = launch_append<false>(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
+}
+
+cs_status cs_qcache_append_rows(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n_rows,
+                                const int32_t *rows, int n, const int32_t *start, const int32_t *slots,
+                                const int32_t *pos, void *ws, size_t ws_bytes, cs_stream_t stream) {
+    const char *who = "cs_qcache_append_rows";
+    QRowsCall a;
+    // no rows at all: tokens have nothing to come from, and k and v no data
+    const cs_status st = rows_call(cache, k, v, n, start, slots, ws, ws_bytes, who, &a, n_rows == 0);
+    if (st != CS_OK) return st;
+    CS_CHECK(n_rows >= 0 && n_rows <= kMaxTokens, "%s: n_rows=%d outside [0, %d]", who, n_rows, kMaxTokens);
+    CS_CHECK(n == 0 || (rows && aligned(rows, 4)), "%s: rows is null or misaligned", who);
+    CS_CHECK((pos != nullptr) == (cache->pos != nullptr), "%s: pos is required if and only if the cache has positions", who);
+    CS_CHECK(aligned(pos, 4), "%s: pos must be 4-byte aligned", who);
+    a.rows = rows;
+    a.n_rows = n_rows;
+    a.pos = pos;
+    if (n == 0) return CS_OK;
+    const cudaError_t e = launch_append<true>(a, (cudaStream_t)stream);
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 

@@ -28,6 +28,26 @@ struct QRowsK {
     int vec;                 // every row starts on a 16-byte boundary
 };
 
+// ------------------------------------------------------------------- host side
+
+constexpr int kMaxHeads = 1024, kMaxCapacity = 1 << 24, kMaxTokens = 1 << 24;
+
+inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+#define CS_CHECK(cond, ...)                       \
+    do {                                          \
+        if (!(cond)) {                            \
+            set_error(__VA_ARGS__);               \
+            return CS_ERR_INVALID;                \
+        }                                         \
+    } while (0)
+
+// codes: whether the call reads or writes k, v and their scales.
+cs_status check_cache(const cs_qcache *q, bool codes, const char *who, QCacheK *out);
+// empty: no tokens, so no data
+cs_status check_rows(const cs_head_rows *r, bool empty, const char *name, const char *who, QRowsK *out);
+cs_status check_qws(void *ws, size_t ws_bytes, size_t need, const char *who);
+
 struct QAttnArgs {
     QCacheK c;
     QRowsK q, out;

@@ -474,6 +474,19 @@ cs_status cs_qcache_append(const cs_qcache *cache, const cs_head_rows *k, const 
                            void *ws, size_t ws_bytes, cs_stream_t stream);
 
 /*
+ * The same for tokens whose rows lie anywhere: token t of sequence b is row
+ * rows[b, t] ([batch, n] int32 device) of the n_rows rows of k and v (their
+ * ld_batch is not used) -- prompts packed one behind the other, or of a tree of
+ * drafted tokens those that were accepted.  -1 means no token: its slot stays as
+ * it is.  Any other row outside [0, n_rows) is passed over like -1 and sets
+ * CS_DEVERR_INDEX.  Token t's position is pos[b] + t.  k and v must not be the
+ * cache's memory.
+ */
+cs_status cs_qcache_append_rows(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n_rows,
+                                const int32_t *rows, int n, const int32_t *start, const int32_t *slots,
+                                const int32_t *pos, void *ws, size_t ws_bytes, cs_stream_t stream);
+
+/*
  * The values that slots stand for, offset + scale * code, rounded to fp32 and
  * from there, for 16-bit outputs, to the output's dtype (a group that spans
  * nearly +-65504 stands for values up to 65536, an infinity in fp16).  Slots
@@ -540,6 +553,78 @@ cs_status cs_qcache_evict(const cs_qcache *cache, const int32_t *length, int lim
  */
 cs_status cs_qcache_trim(const cs_qcache *src, const int32_t *length, int keep, const int32_t *next_pos, int sinks,
                          int recent, const cs_qcache *dst, void *ws, size_t ws_bytes, cs_stream_t stream);
+
+/*
+ * Takes sequences over: sequence i of dst becomes sequence source[i] of src, its
+ * slots 0 .. length[source[i]] - 1 with their weights and positions; dst's other
+ * slots are not written.  source[i] == -1 leaves sequence i as it is.
+ *   source: [dst->batch] int32 device; any other value outside [0, src->batch)
+ *      leaves the sequence and sets CS_DEVERR_INDEX.
+ *   length: [src->batch] int32 device, clamped to [0, src->capacity]
+ *      (CS_DEVERR_COUNT); a source that is longer than dst->capacity is cut off
+ *      there, with CS_DEVERR_COUNT.
+ *   dst: a cache of the same n_heads and d_head, with weights (positions) if and
+ *      only if src has them, and memory of its own; or NULL (or src): in place,
+ *      as if all were read before any is written, so that sequences may change
+ *      places.
+ */
+cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int32_t *length, const cs_qcache *dst,
+                         void *ws, size_t ws_bytes, cs_stream_t stream);
+
+/*
+ * Attention for a tree of drafted tokens over the cache, before any of them is in
+ * it.  Sequence b has n drafted tokens (its first n_new[b], if n_new is given);
+ * parent[b, t] ([batch, n] int32 device) is the token that token t continues, a
+ * lower one, or -1: the last one in the cache.  Without parents (NULL) every token continues the one before it.
+ * With keys and values of the slots and of the drafted tokens,
+ *     s_i = scale q . k_i,  p = softmax(s),  out = sum_i p_i v_i,
+ * over the slots i < length[b] (clamped to [0, capacity], CS_DEVERR_COUNT) that are not
+ * empty (pos < 0, if the cache has positions), the token's ancestors in the tree, and the token itself.
+ *   q, out: n tokens of n_heads heads;  k, v: n tokens of cache->n_heads heads;
+ *      all of one dtype, fp16 or bf16.  Query head h reads cache head
+ *      h / (n_heads / cache->n_heads).  out is none of the inputs.
+ *   n_new: [batch] int32 device or NULL, clamped to [0, n] (CS_DEVERR_COUNT).
+ *      Tokens from n_new[b] on give zeros and are not seen.
+ * A parent outside [-1, t) counts as -1 and sets CS_DEVERR_INDEX.  Drafted rows count
+ * as fp16 values, as the cache would take them: clamped to +-65504, NaN as 0.
+ * 1 <= n <= 128, n x n_heads / cache->n_heads <= 1024; d_head 64 or 128.  Slots'
+ * values are rounded to fp16 for the products, q (by row and power of two) likewise; sums and softmax
+ * statistics are fp32.  The cache, its weights among it, is not changed.
+ * With the same arguments the results are the same bit for bit.
+ */
+size_t cs_qcache_tree_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n);
+cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q, const cs_head_rows *k,
+                                   const cs_head_rows *v, int n_heads, int n, const int32_t *length,
+                                   const int32_t *parent, const int32_t *n_new, float scale,
+                                   const cs_head_rows *out, void *ws, size_t ws_bytes, cs_stream_t stream);
+
+/*
+ * Attention of whole prompts, packed: sequence b's query tokens are rows
+ * q_start[b] .. q_start[b + 1] - 1 of q and out, its keys and values rows
+ * k_start[b] .. k_start[b + 1] - 1 of k and v.  Query head h reads head
+ * h / (n_heads / kv_heads):
+ *     s_j = scale q_i . k_j,  p = softmax(s),  out_i = sum_j p_j v_j,
+ * over all of the sequence's keys, or, causal, over those with
+ * j <= i + (its keys - its query tokens): the last query token sees all, and
+ * keys that lie before the queries (an earlier part of the prompt) may be given.
+ * A row that sees no key gives zeros; what a row does not see has no influence
+ * on it, NaN and infinities included.  Rows of out in no sequence are not written.
+ *   q, out: [q_total, n_heads, d_head];  k, v: [k_total, kv_heads, d_head]; one
+ *      dtype, fp16 or bf16, every row on a 16-byte boundary (else
+ *      CS_ERR_INVALID); their ld_batch is not used.  out is none of the inputs.
+ *   q_start, k_start: [batch + 1] int32 device, not falling; k_start may be NULL:
+ *      q_start (then k_total must be q_total).  Values outside [0, total], and
+ *      falling ones, are clamped and set CS_DEVERR_COUNT.
+ *   scale: the factor on q . k; 0 means 1 / sqrt(d_head).
+ * d_head is 64 or 128; batch <= 4096, n_heads <= 1024, n_heads / kv_heads <= 128.  Sums and softmax statistics are
+ * fp32; the weights go into the value products in the inputs' type.  With the
+ * same arguments the results are the same bit for bit.
+ */
+size_t cs_prompt_workspace_size(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total);
+cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, const cs_head_rows *v, int n_heads,
+                              int kv_heads, int d_head, int batch, const int32_t *q_start, int q_total,
+                              const int32_t *k_start, int k_total, int causal, float scale,
+                              const cs_head_rows *out, void *ws, size_t ws_bytes, cs_stream_t stream);
 
 /* Drops every cached stack and layer graph (waits for nothing; call when idle). */
 cs_status cs_stack_release(void);

@@ -1,0 +1,203 @@
+"""Attention of packed prompts against its plain 64-bit form."""
+import pytest
+import torch
+
+import contextual_sparsity_sparse_gb300 as cs
+
+import _prompt_ref as ref
+
+pytestmark = pytest.mark.gpu
+DTS = [torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__ as g
+    g.build()
+
+
+def starts(lens):
+    return torch.tensor([0] + list(lens), device="cuda").cumsum(0).to(torch.int32)
+
+
+def make(q_lens, k_lens, heads, kv, d, dt, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    q, k, v = r(sum(q_lens), heads, d), r(sum(k_lens), kv, d) + r(kv, d), r(sum(k_lens), kv, d) + 0.5 * r(kv, d)
+    return q.to(dt), k.to(dt), v.to(dt)
+
+
+def call(q, k, v, q_lens, k_lens=None, out=None, ws=None, **kw):
+    out = torch.full_like(q, 7.0) if out is None else out
+    if ws is None:
+        ws = cs.PromptWorkspace(len(q_lens), q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0])
+    cs.cs_prompt_attention(q, k, v, out, starts(q_lens), ws, k_start=None if k_lens is None else starts(k_lens), **kw)
+    return out, ws
+
+
+def check(q, k, v, q_lens, k_lens=None, causal=True, scale=0.0, out=None):
+    out, ws = call(q, k, v, q_lens, k_lens, causal=causal, scale=scale, out=out)
+    assert cs.cs_get_device_error(ws) == 0
+    want, bound = ref.prompt(q, k, v, q_lens, q_lens if k_lens is None else k_lens, causal, scale)
+    n = sum(q_lens)
+    off = (out[:n].double() - want[:n]).abs()
+    assert (off <= bound[:n]).all(), (off / bound[:n].clamp(min=1e-30)).max().item()
+    return out
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads,kv,d", [(1, 1, 64), (8, 8, 64), (6, 2, 128), (5, 1, 128), (16, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("q_lens", [[1], [17], [128], [129, 1, 0, 64], [300, 257], [0, 0, 3]])
+def test_causal(q_lens, heads, kv, d, dt):
+    check(*make(q_lens, q_lens, heads, kv, d, dt), q_lens)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,k_lens", [([1], [1000]), ([5, 70], [131, 70]), ([200], [1]), ([130, 3], [0, 4]), ([64], [640]),
+                                           ([1, 1, 1], [128, 129, 127]), ([0, 9], [50, 300])])
+def test_other_keys(q_lens, k_lens, causal, dt):
+    """Keys of an earlier part, none at all, or fewer than query tokens: causal rows that see nothing are zero."""
+    check(*make(q_lens, k_lens, 8, 2, 128, dt), q_lens, k_lens, causal)
+
+
+@pytest.mark.parametrize("heads,kv,d", [(128, 1, 64), (127, 1, 64), (7, 1, 128), (12, 4, 64), (40, 40, 128), (65, 1, 128)])
+def test_groups(heads, kv, d):
+    q_lens = [33, 5]
+    check(*make(q_lens, q_lens, heads, kv, d, torch.bfloat16), q_lens)
+
+
+@pytest.mark.parametrize("q_lens,k_lens,heads,kv,d,causal", [
+    ([1], [20001], 8, 1, 128, True), ([3, 1], [9000, 12345], 8, 8, 64, True), ([100], [16384], 4, 4, 128, True),
+    ([33], [30000], 16, 1, 64, False), ([2000], [2000], 2, 2, 128, True), ([1, 700], [5000, 2900], 2, 1, 128, True)])
+def test_long_keys_and_few_rows(q_lens, k_lens, heads, kv, d, causal):
+    check(*make(q_lens, k_lens, heads, kv, d, torch.float16), q_lens, k_lens, causal)
+
+
+def test_many_sequences():
+    g = torch.Generator().manual_seed(3)
+    q_lens = torch.randint(0, 40, (150,), generator=g).tolist()
+    check(*make(q_lens, q_lens, 4, 2, 64, torch.bfloat16), q_lens)
+
+
+@pytest.mark.parametrize("scale", [0.3, -0.2, 1e-30, 30.0])
+def test_scales(scale):
+    check(*make([200], [200], 2, 1, 128, torch.float16), [200], scale=scale)
+
+
+@pytest.mark.parametrize("dt", DTS)
+def test_growing_logits(dt):
+    """Every key beats the ones before it by a lot, so that the running maximum moves all the time; and the reverse."""
+    for step in (1.0, -1.0):
+        q, k, v = make([700], [700], 2, 2, 64, dt)
+        k[..., 0] = (step * torch.arange(700, device="cuda")[:, None]).to(dt)
+        q[..., 0] = 4.0
+        check(q, k, v, [700])
+
+
+def test_layouts():
+    """Slices of one projection's output, heads before tokens, and rows that are not dense."""
+    lens, heads, kv, d = [70, 131], 6, 2, 64
+    q, k, v = make(lens, lens, heads, kv, d, torch.float16)
+    want, _ = call(q, k, v, lens)
+    both = torch.cat([q, k, v], 1)
+    got, _ = call(both[:, :heads], both[:, heads:heads + kv], both[:, heads + kv:], lens, out=torch.empty_like(q))
+    assert torch.equal(got, want)
+    turned = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    got, _ = call(turned(q), turned(k), turned(v), lens, out=turned(torch.empty_like(q)))
+    assert torch.equal(got, want)
+    wide = torch.full((sum(lens), heads, d + 8), 3.0, dtype=torch.float16, device="cuda")
+    got, _ = call(q, k, v, lens, out=wide[..., :d])
+    assert torch.equal(got, want) and (wide[..., d:] == 3.0).all()
+
+
+def test_what_lies_behind_the_last_sequence():
+    """Rows in no sequence are neither read for a result nor written."""
+    lens = [50, 20]
+    q, k, v = make([100], [100], 4, 2, 64, torch.bfloat16)
+    for t in (q, k, v):
+        t[70:] = float("nan")
+    out = check(q, k, v, lens)
+    assert (out[70:] == 7.0).all()
+    shifted = torch.full_like(q, 7.0)
+    ws = cs.PromptWorkspace(1, 4, 2, 64, 100)
+    cs.cs_prompt_attention(q, k, v, shifted, torch.tensor([50, 70], dtype=torch.int32, device="cuda"), ws)
+    assert torch.equal(shifted[50:70], out[50:70]) and (shifted[:50] == 7.0).all() and (shifted[70:] == 7.0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("lens", [[40], [200, 300]])
+def test_what_is_not_seen_has_no_influence(bad, lens):
+    """NaN and infinities in keys and values reach the rows that see them, and no others."""
+    q, k, v = make(lens, lens, 4, 2, 64, torch.float16)
+    clean, _ = call(q, k, v, lens)
+    at = lens[0] - 11
+    for t in (k, v):
+        poisoned = t.clone()
+        poisoned[at] = bad
+        out, _ = call(q, poisoned if t is k else k, poisoned if t is v else v, lens)
+        assert torch.isfinite(out[:at]).all() and torch.isfinite(out[lens[0]:]).all()
+        d = torch.finfo(torch.float16).eps
+        assert ((out[:at].double() - clean[:at].double()).abs() <= 4 * d * clean[:at].double().abs() + 4 * d).all()
+        assert torch.equal(out[lens[0]:], clean[lens[0]:])
+        if t is v:
+            assert not torch.isfinite(out[at:lens[0]]).any()
+    poisoned = q.clone()
+    poisoned[at] = bad
+    out, _ = call(poisoned, k, v, lens)
+    keep = torch.arange(sum(lens)) != at
+    assert torch.equal(out[keep], clean[keep]) and torch.isnan(out[at]).all()
+
+
+def test_keys_of_minus_infinity():
+    """All of a row's logits -inf: it sees nothing that counts, and gives zeros."""
+    q, k, v = make([5], [5], 1, 1, 64, torch.float16)
+    q[:] = 1.0
+    k[:] = 0.0
+    k[..., 0] = float("-inf")
+    out, _ = call(q, k, v, [5])
+    assert (out == 0).all()
+
+
+def test_wrong_starts_are_flagged_and_stay_in_bounds():
+    q, k, v = make([64], [64], 2, 1, 64, torch.float16)
+    for at in ([0, 40, 20, 64], [-5, 10, 20, 64], [0, 10, 20, 1000], [3, 2, 1, 0]):
+        ws = cs.PromptWorkspace(3, 2, 1, 64, 64)
+        out = torch.full_like(q, 7.0)
+        cs.cs_prompt_attention(q, k, v, out, torch.tensor(at, dtype=torch.int32, device="cuda"), ws)
+        assert cs.cs_get_device_error(ws) == cs.CS_DEVERR_COUNT
+        assert torch.isfinite(out).all()
+
+
+def test_same_bits_again_captured_and_on_another_stream():
+    lens, k_lens = [130, 1, 77], [9000, 300, 77]
+    q, k, v = make(lens, k_lens, 8, 2, 128, torch.bfloat16)
+    first, ws = call(q, k, v, lens, k_lens)
+    again, _ = call(q, k, v, lens, k_lens, ws=ws)
+    assert torch.equal(first, again)
+    side = torch.cuda.Stream()
+    out, s, sk = torch.zeros_like(q), starts(lens), starts(k_lens)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cs.cs_prompt_attention(q, k, v, out, s, ws, k_start=sk)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(first, out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cs.cs_prompt_attention(q, k, v, out, s, ws, k_start=sk)
+        cs.cs_prompt_attention(q, k, v, out, s, ws, k_start=sk)
+    # other inputs, other lengths: the graph reads them anew
+    q2, k2, v2 = make(lens, k_lens, 8, 2, 128, torch.bfloat16, seed=5)
+    lens2, k_lens2 = [8, 100, 100], [1, 9276, 100]
+    for a, b in ((q, q2), (k, k2), (v, v2), (s, starts(lens2)), (sk, starts(k_lens2))):
+        a.copy_(b)
+    want, _ = call(q2, k2, v2, lens2, k_lens2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert cs.cs_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("dt", DTS)
+def test_long_prompt(dt):
+    check(*make([3001, 1500], [3001, 1500], 8, 1, 128, dt), [3001, 1500])
