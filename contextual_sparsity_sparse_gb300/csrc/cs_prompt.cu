@@ -1,12 +1,30 @@
 // Attention of whole prompts, packed one behind the other: causal or not, with
 // grouped heads.
-#include "cs_qcache.cuh"
+//
+// Two kernels.  The first lists the work: for every sequence, pairs of row tiles
+// (cs_attn_tc.cuh) with the key tiles that they see, longest first, cut along
+// the keys where few rows see many.  In the second a CTA per SM goes through
+// the list for all key/value heads: one thread loads tiles by TMA, one issues
+// the products, two warpgroups have the rows.
+//
+// The rows of a tile are whole tokens of one group of heads: 128 / group tokens.
+// A tile's box of q is [tokens][group][64 channels], so that it lands row by
+// row as the products want it, whatever q's strides.
+//
+// A product with V adds p v for all 128 keys of a tile, and p = 0 does not undo a
+// NaN or infinity in a v that a row does not see.  Such rows end up not finite,
+// which is looked for when they are written: they are worked out again, key by
+// key, from what they see alone.
+#include "cs_attn_tc.cuh"
 
 namespace cs {
 
 namespace {
 
-constexpr int kMaxGroup = 128;   // query heads of one key/value head
+constexpr int kMaxGroup = 128;         // query heads of one key/value head
+constexpr int kPromptThreads = 384;    // two warpgroups of rows, and one of which two warps issue products and loads
+constexpr int kPlanThreads = 1024;
+constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in records than they win
 
 struct PromptK {
     QRowsK q, k, v, out;
@@ -14,71 +32,439 @@ struct PromptK {
     const int32_t *q_start, *k_start;
     float scale;
     uint32_t *err;
+    int per;             // tokens of a row tile
+    int sms;
 };
 
-// The next sequence's rows, [end, its end), where starts are clamped to [0, total] and do not fall.
-__device__ __forceinline__ int2 next_rows(const int32_t *start, int b, int total, int end, uint32_t *err) {
-    const int x = b == 0 ? ld_dep(start) : end, y = ld_dep(start + b + 1);
-    const int first = min(max(x, 0), total), last = min(max(y, first), total);
-    if (x != first || y != last) atomicOr(err, CS_DEVERR_COUNT);
-    return make_int2(first, last);
+// ------------------------------------------------------------------- the list
+
+// Block-wide exclusive running maximum.
+__device__ __forceinline__ int block_excl_max(int v, int *wmax) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc = max(inc, n);
+    }
+    if (lane == 31) wmax[warp] = inc;
+    __syncthreads();
+    int before = __shfl_up_sync(kFull, inc, 1);
+    if (lane == 0) before = 0;
+    for (int w = 0; w < warp; ++w) before = max(before, wmax[w]);
+    __syncthreads();
+    return before;
 }
 
-// One row's attention by one warp, key by key: lane l has channels l + 32 i.
+// start[0 .. batch], cut to [0, total] and made not to fall, into at.
+__device__ void plan_starts(const int32_t *start, int batch, int total, int *at, int *wmax, uint32_t *err) {
+    const int each = (batch + kPlanThreads) / kPlanThreads;
+    const int b0 = min(batch + 1, (int)threadIdx.x * each), b1 = min(batch + 1, b0 + each);
+    int top = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int x = ld_dep(start + b);
+        top = max(top, min(max(x, 0), total));
+        at[b] = x;
+    }
+    int run = block_excl_max(top, wmax);
+    for (int b = b0; b < b1; ++b) {
+        const int x = at[b];
+        run = max(run, min(max(x, 0), total));
+        if (x != run) atomicOr(err, CS_DEVERR_COUNT);
+        at[b] = run;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Plan plan) {
+    extern __shared__ int starts[];
+    constexpr int BINS = 256;
+    __shared__ int scan[32], hist[BINS], longest, recs, works;
+    __shared__ unsigned long long units;
+    int *qs = starts, *ks = qs + a.batch + 1, *first = ks + a.batch + 1;
+    const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (tid == 0) {
+        longest = recs = works = 0;
+        units = 0;
+    }
+    if (tid < BINS) hist[tid] = 0;
+    for (int i = tid; i < plan.recs; i += kPlanThreads) plan.arrived[i] = 0;
+    plan_starts(a.q_start, a.batch, a.q_total, qs, scan, a.err);
+    if (a.k_start == a.q_start) ks = qs;
+    else plan_starts(a.k_start, a.batch, a.k_total, ks, scan, a.err);
+    __syncthreads();
+    const int pair = 2 * a.per;
+    // the first pair of every sequence
+    const int each = (a.batch + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(a.batch, tid * each), b1 = min(a.batch, b0 + each);
+    int n = 0, total;
+    for (int b = b0; b < b1; ++b) n += (qs[b + 1] - qs[b] + pair - 1) / pair;
+    int at = block_excl_scan(n, scan, &total);
+    for (int b = b0; b < b1; ++b) {
+        first[b] = at;
+        at += (qs[b + 1] - qs[b] + pair - 1) / pair;
+    }
+    __syncthreads();
+    // pair i: its sequence, its first token there, and the key tiles that it sees
+    auto find = [&](int i, int &b, int &t) {
+        int lo = 0, hi = a.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        t = (i - first[lo]) * pair;
+        const int n_q = qs[b + 1] - qs[b], n_k = ks[b + 1] - ks[b];
+        const int lim = a.causal ? min(max(n_k - n_q + min(t + pair, n_q), 0), n_k) : n_k;
+        return (lim + kTile - 1) / kTile;
+    };
+    unsigned long long sum = 0;
+    int most = 0;
+    for (int i = tid; i < total; i += kPlanThreads) {
+        int b, t;
+        const int tiles = find(i, b, t);
+        sum += tiles;
+        most = max(most, tiles);
+    }
+    most = __reduce_max_sync(kFull, most);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if ((tid & 31) == 0) {
+        atomicMax(&longest, most);
+        atomicAdd(&units, sum);
+    }
+    __syncthreads();
+    // No piece is longer than an SM's share of all; and with a pair's pieces fewer than twice its tiles / chunk, all
+    // pieces of cut pairs are fewer than 2 SMs' number.
+    const int chunk = (int)max((unsigned long long)kLeastPiece, (units * a.kv + a.sms - 1) / a.sms);
+    const int big = min(longest, chunk);
+    auto pieces_of = [&](int tiles) { return tiles > chunk && plan.recs > 0 ? (tiles + chunk - 1) / chunk : 1; };
+    auto bin_of = [&](int len) { return BINS - 1 - (int)((long long)min(len, big) * (BINS - 1) / max(big, 1)); };
+    for (int i = tid; i < total; i += kPlanThreads) {
+        int b, t;
+        const int tiles = find(i, b, t), pieces = pieces_of(tiles);
+        atomicAdd(&hist[bin_of((tiles + pieces - 1) / pieces)], pieces);
+        if (pieces > 1) atomicAdd(&recs, pieces);
+    }
+    __syncthreads();
+    const int mine = tid < BINS ? hist[tid] : 0;
+    int all;
+    const int place = block_excl_scan(mine, scan, &all);
+    if (tid < BINS) hist[tid] = place;
+    if (tid == 0) {
+        plan.count[0] = all;
+        plan.count[1] = recs;
+    }
+    __syncthreads();
+    for (int i = tid; i < total; i += kPlanThreads) {
+        int b, t;
+        const int tiles = find(i, b, t), pieces = pieces_of(tiles);
+        const int n_q = qs[b + 1] - qs[b], n_k = ks[b + 1] - ks[b];
+        Work w;
+        w.tok0 = qs[b] + t;
+        w.toks = min(pair, n_q - t);
+        w.seq = b;
+        w.lim0 = a.causal ? n_k - n_q + t + 1 : n_k;
+        w.n_k = n_k;
+        w.k0 = ks[b];
+        w.pieces = pieces;
+        w.rec = pieces > 1 ? atomicAdd(&works, pieces) : 0;
+        w.spare = 0;
+        const int to = atomicAdd(&hist[bin_of((tiles + pieces - 1) / pieces)], pieces);
+        for (int p = 0; p < pieces; ++p) {
+            w.j0 = (int)((long long)tiles * p / pieces);
+            w.j1 = (int)((long long)tiles * (p + 1) / pieces);
+            w.p = p;
+            plan.work[to + p] = w;
+        }
+    }
+}
+
+// -------------------------------------------------------------- the attention
+
+template <int D>
+struct PromptCfg {
+    static constexpr int DB = D / 64;
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr size_t smem = (size_t)(2 + STAGES) * DB * kBlock + 1024;
+};
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int c, int h, int row, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(m), "r"(c), "r"(h), "r"(row), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// One row by one warp, key by key, of keys [j0, j1): lane l has channels l + 32 i of o, the sums of p v.
 template <typename T, int D>
-__device__ __forceinline__ void prompt_row(const PromptK &a, int token, int head, int k0, int keys, float (&o)[D / 32]) {
+__device__ __noinline__ void prompt_row(const PromptK &a, int token, int head, int64_t k0, int j0, int j1, float c, float shift, float &m,
+                                        float &l, float (&o)[D / 32]) {
     const int lane = threadIdx.x & 31;
     const T *q = reinterpret_cast<const T *>(a.q.p) + token * a.q.ldt + head * a.q.ldh;
     const T *k = reinterpret_cast<const T *>(a.k.p) + k0 * a.k.ldt + head / a.group * a.k.ldh;
     const T *v = reinterpret_cast<const T *>(a.v.p) + k0 * a.v.ldt + head / a.group * a.v.ldh;
-    float x[D / 32], m = -INFINITY, l = 0.f;
+    float x[D / 32];
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-        x[i] = a.scale * (float)q[lane + 32 * i];
+        x[i] = a.scale < 0.f ? -(float)q[lane + 32 * i] : (float)q[lane + 32 * i];
         o[i] = 0.f;
     }
-    for (int j = 0; j < keys; ++j) {
+    for (int64_t j = j0; j < j1; ++j) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) s = fmaf(x[i], (float)k[j * a.k.ldt + lane + 32 * i], s);
         s = warp_sum(s);
         const float up = fmaxf(m, s), base = up == -INFINITY ? 0.f : up;
-        const float keep = expf(m - base), p = expf(s - base);
+        const float keep = m == -INFINITY ? 0.f : exp2f((m - base) * c), p = exp2f((s - base) * c + shift);
         m = up;
         l = fmaf(l, keep, p);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], keep, p * (float)v[j * a.v.ldt + lane + 32 * i]);
     }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) prompt_kernel(PromptK a) {
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+              PromptK a, Plan plan) {
+    using C = PromptCfg<D>;
+    using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+    extern __shared__ uint8_t dsm[];
+    __shared__ Bars<C::STAGES> bars;
+    __shared__ uint32_t tmem_at;
+    __shared__ int flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t q_at = (smem_addr(dsm) + 1023u) & ~1023u, ring = q_at + 2 * C::DB * kBlock;
+    if (warp == 8) tm_alloc(&tmem_at);
+    if (tid == 288) init_bars(bars, 1, 1);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_at;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (row >= (int64_t)a.q_total * a.heads) return;
-    const int token = (int)(row / a.heads), head = (int)(row % a.heads);
-    int2 q{}, k{};
-    for (int b = 0; b < a.batch; ++b) {
-        q = next_rows(a.q_start, b, a.q_total, q.y, a.err);
-        k = next_rows(a.k_start, b, a.k_total, k.y, a.err);
-        if (token < q.x || token >= q.y) continue;
-        const int n = k.y - k.x, keys = a.causal ? min(n, max(0, token - q.x + 1 + n - (q.y - q.x))) : n;
-        float o[D / 32];
-        prompt_row<T, D>(a, token, head, k.x, keys, o);
+    const int total = ld_dep(plan.count) * a.kv, recs = ld_dep(plan.count + 1), step = a.causal;
+
+    // Registers: 168 a thread at launch, 3 x 168 = 2 x 232 + 40.
+    if (warp < 8) {
+        regs_up<232>();
+        const int t = warp >> 2, row = tid & 127, tok = row / a.group, g = row - tok * a.group;
+        const bool neg = a.scale < 0.f;
+        const float c = fabsf(a.scale) * 1.44269504088896341f;
+        RowState r;
+        for (int i = 0;; ++i) {
+            const int x = nth_work(i);
+            if (x >= total) break;
+            const Work w = load_work(plan.work + x / a.kv);
+            const int h = x % a.kv;
+            const Span sp = span_of(w, t, a.per, step);
+            const bool valid = tok < sp.toks;
+            const int token = w.tok0 + t * a.per + tok;
+            const int lim = valid ? min(max(w.lim0 + step * (t * a.per + tok), 0), w.n_k) : 0;
+            const int all = __reduce_min_sync(kFull, valid ? lim : INT_MAX);   // keys that all of the warp's rows see
+            if (!softmax_rows<D, BF16>(r, w.j0, sp.end, t, bars, tmem, c, neg, a.err, [&](int j, float (&s)[kTile]) {
+                    if (all >= (j + 1) * kTile) return;
+                    const int off = lim - j * kTile;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            q_store1(a.out, token * a.out.ldt + head * a.out.ldh + (threadIdx.x & 31) + 32 * i, o[i]);
-        return;
+                    for (int e = 0; e < kTile; ++e) s[e] = e < off ? s[e] : -INFINITY;
+                }))
+                break;
+            const bool some = w.j0 < sp.end;
+            const uint32_t o_at = tmem + (((uint32_t)row & ~31u) << 16) + 2 * kTile + t * D;
+            T *out = reinterpret_cast<T *>(a.out.p) + token * a.out.ldt + (int64_t)(h * a.group + g) * a.out.ldh;
+            float *rec = w.pieces > 1 ? plan.rec + (int64_t)(h * recs + w.rec) * rec_floats(D) : nullptr;
+            float *my = w.pieces > 1 ? rec + w.p * rec_floats(D) + t * kTile + row : nullptr;
+            const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+            if (my) {
+                __stcg(my, r.m);
+                __stcg(my + kPair, r.l);
+            }
+            float odd = r.l * 0.f;   // NaN, if anything is not finite
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+                float o[32];
+                if (some) {
+                    tm_ld32(o_at + 32 * b, o);
+                    tm_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) odd = fmaf(o[e], 0.f, odd);
+                if (my) {
+                    if (some && valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) __stcg(my + (2 + 32 * b + e) * kPair, o[e]);
+                    }
+                } else if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                    store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o);
+                }
+            }
+            uint32_t again = __ballot_sync(kFull, valid && some && !(odd == 0.f));
+            while (again) {
+                const int from = __ffs(again) - 1;
+                again &= again - 1;
+                const int rt = __shfl_sync(kFull, token, from), rg = __shfl_sync(kFull, g, from), rl = __shfl_sync(kFull, lim, from);
+                float m, l, o[D / 32];
+                prompt_row<T, D>(a, rt, h * a.group + rg, w.k0, w.j0 * kTile, min(w.j1 * kTile, rl), c, kShift<BF16>, m, l, o);
+                T *to = reinterpret_cast<T *>(a.out.p) + rt * a.out.ldt + (int64_t)(h * a.group + rg) * a.out.ldh;
+                float *ro = my ? my - lane + from : nullptr;
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    if (my) __stcg(ro + (2 + 32 * b + lane) * kPair, o[b]);
+                    else to[32 * b + lane] = (T)(l == 0.f ? 0.f : o[b] / l);
+                }
+                if (my && lane == 0) {
+                    __stcg(ro, m);
+                    __stcg(ro + kPair, l);
+                }
+            }
+            if (my) {
+                const int last = last_piece(bars, plan.arrived + h * recs + w.rec, w.pieces, &flag, r.n_rec++, a.err);
+                if (last < 0) break;
+                if (last && valid)
+                    join_pieces<D>(rec, w.pieces, t * kTile + row, c,
+                                   [&](int b, const float *o) { store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o); });
+            }
+        }
+    } else if (warp == 8) {
+        regs_down<40>();
+        if (lane == 0) {
+            MmaState st;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const int x = nth_work(i);
+                if (x >= total) break;
+                const Work w = load_work(plan.work + x / a.kv);
+                const int end[2] = {span_of(w, 0, a.per, step).end, span_of(w, 1, a.per, step).end};
+                ok = issue_work<D, BF16, C::STAGES>(w, end, bars, tmem, q_at, ring, st, a.err);
+            }
+            if (!ok) {
+                mma_commit(&bars.drain);
+                mbar_wait(&bars.drain, 0, kWaitNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        regs_down<40>();
+        if (lane == 0) {
+            uint32_t it = 0, n_q = 0;
+            bool ok = true;
+            auto tile = [&](const CUtensorMap *m, int h, int row) {
+                const uint32_t s = it % C::STAGES;
+                if (it >= C::STAGES && !wait(&bars.empty[s], (it / C::STAGES - 1) & 1, a.err)) return false;
+                mbar_arrive_expect_tx(&bars.full[s], C::DB * kBlock);
+#pragma unroll
+                for (int b = 0; b < C::DB; ++b) load_box(ring + (s * C::DB + b) * kBlock, m, 64 * b, h, row, &bars.full[s]);
+                ++it;
+                return true;
+            };
+            for (int i = 0; ok; ++i) {
+                const int x = nth_work(i);
+                if (x >= total) break;
+                const Work w = load_work(plan.work + x / a.kv);
+                const int h = x % a.kv;
+                const int end[2] = {span_of(w, 0, a.per, step).end, span_of(w, 1, a.per, step).end};
+                const int last = max(end[0], end[1]);
+                if (last <= w.j0) continue;
+                if (n_q > 0 && !wait(&bars.q_empty, (n_q - 1) & 1, a.err)) {
+                    ok = false;
+                    break;
+                }
+                ++n_q;
+                const uint32_t bytes = C::DB * a.per * a.group * 128;
+                mbar_arrive_expect_tx(&bars.q_full, bytes * ((w.j0 < end[0]) + (w.j0 < end[1])));
+                for (int t = 0; t < 2; ++t)
+                    if (w.j0 < end[t])
+                        for (int b = 0; b < C::DB; ++b)
+                            load_box(q_at + (t * C::DB + b) * kBlock, &mq, 64 * b, h * a.group, w.tok0 + t * a.per, &bars.q_full);
+                for (int j = w.j0; ok && j < last; ++j)
+                    ok = tile(&mk, h, w.k0 + j * kTile) && tile(&mv, h, w.k0 + j * kTile);
+            }
+            if (!ok) {
+                // what is under way lands before the memory is given back
+                for (uint32_t n = it > C::STAGES ? it - C::STAGES : 0; n < it; ++n)
+                    mbar_wait(&bars.full[n % C::STAGES], n / C::STAGES & 1, kWaitNs);
+                if (n_q > 0) mbar_wait(&bars.q_full, (n_q - 1) & 1, kWaitNs);
+            }
+        }
+        __syncwarp();
+    } else {
+        regs_down<40>();
     }
+    tc_before();
+    __syncthreads();
+    if (warp == 8) tm_free(tmem);
 }
+
+// ------------------------------------------------------------------- host side
 
 bool prompt_sizes(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total) {
     return batch >= 1 && batch <= kQMaxBatch && kv_heads >= 1 && n_heads >= kv_heads && n_heads <= kMaxHeads &&
            n_heads % kv_heads == 0 && n_heads / kv_heads <= kMaxGroup && (d_head == 64 || d_head == 128) && q_total >= 0 &&
            q_total <= kMaxTokens && k_total >= 0 && k_total <= kMaxTokens;
+}
+
+// The list's place behind the control words; returns the bytes.
+size_t prompt_scratch(int batch, int n_heads, int kv_heads, int d, int q_total, int k_total, int sms, char *at, Plan *plan) {
+    const int per = kTile / (n_heads / kv_heads);
+    const int recs = k_total > kLeastPiece * kTile ? 2 * sms : 0;
+    const size_t works = (size_t)q_total / (2 * per) + batch + recs;
+    const size_t list = align256(works * sizeof(Work)), arrived = align256((size_t)recs * sizeof(unsigned));
+    if (plan) {
+        plan->count = reinterpret_cast<int *>(at);
+        plan->work = reinterpret_cast<Work *>(at + 256);
+        plan->arrived = reinterpret_cast<unsigned *>(at + 256 + list);
+        plan->rec = reinterpret_cast<float *>(at + 256 + list + arrived);
+        plan->recs = recs;
+    }
+    return 256 + list + arrived + (size_t)recs * rec_floats(d) * sizeof(float);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+    static const EncodeFn f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return f;
+}
+
+// [tokens, heads, d] rows in boxes of box_t tokens x box_h heads x 64 channels, swizzled by 128 bytes; zeros past the end.
+bool head_map(CUtensorMap *m, const QRowsK &r, int d, int heads, int tokens, int box_h, int box_t) {
+    const cuuint64_t row = (cuuint64_t)d * 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t ld[2] = {heads > 1 ? (cuuint64_t)r.ldh * 2 : row, tokens > 1 ? (cuuint64_t)r.ldt * 2 : row};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_h, (cuuint32_t)box_t}, step[3] = {1, 1, 1};
+    return encoder()(m, r.dt == CS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, ld, box, step,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+cudaError_t run_prompt(const PromptK &a, const Plan &plan, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                       cudaStream_t s) {
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&prompt_plan_kernel));
+    if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void *>(&prompt_kernel<D, BF16>));
+    if (e == cudaSuccess)
+        e = launch(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 3 * ((size_t)a.batch + 1) * sizeof(int), s, pdl_enabled(), a, plan);
+    if (e != cudaSuccess) return e;
+    // no more CTAs than there can be works
+    const int64_t most = ((int64_t)a.q_total / (2 * a.per) + a.batch + plan.recs) * a.kv;
+    return launch(prompt_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kPromptThreads), PromptCfg<D>::smem, s,
+                  pdl_enabled(), mq, mk, mv, a, plan);
 }
 
 }  // namespace
@@ -91,7 +477,7 @@ extern "C" {
 
 size_t cs_prompt_workspace_size(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total) {
     if (!prompt_sizes(batch, n_heads, kv_heads, d_head, q_total, k_total)) return 0;
-    return kControlBytes;
+    return kControlBytes + prompt_scratch(batch, n_heads, kv_heads, d_head, q_total, k_total, device_sm_count(), nullptr, nullptr);
 }
 
 cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, const cs_head_rows *v, int n_heads,
@@ -125,7 +511,11 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     CS_CHECK(q_total == 0 || (out->data != q->data && out->data != k->data && out->data != v->data),
              "%s: out must not be q, k or v", who);
     CS_CHECK(scale == scale && scale - scale == 0.f, "%s: scale must be finite", who);
-    st = check_qws(ws, ws_bytes, cs_prompt_workspace_size(batch, n_heads, kv_heads, d_head, q_total, k_total), who);
+    a.sms = device_sm_count();
+    Plan plan;
+    const size_t need = kControlBytes + prompt_scratch(batch, n_heads, kv_heads, d_head, q_total, k_total, a.sms,
+                                                       static_cast<char *>(ws) + kControlBytes, &plan);
+    st = check_qws(ws, ws_bytes, need, who);
     if (st != CS_OK) return st;
     if (q_total == 0) return CS_OK;
     a.heads = n_heads;
@@ -140,13 +530,25 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     a.k_start = k_start ? k_start : q_start;
     a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)d_head);
     a.err = static_cast<uint32_t *>(ws);
-    auto go = [&](auto kernel) {
-        return launch(kernel, dim3((unsigned)(((int64_t)q_total * n_heads + 7) / 8)), dim3(256), 0, (cudaStream_t)stream,
-                      pdl_enabled(), a);
-    };
+    a.per = kTile / a.group;
+    if (!encoder()) {
+        set_error("%s: the driver has no tensor maps", who);
+        return CS_ERR_CUDA;
+    }
+    CUtensorMap mq, mk, mv;
+    bool ok = head_map(&mq, a.q, d_head, n_heads, q_total, a.group, a.per);
+    if (k_total > 0)
+        ok = ok && head_map(&mk, a.k, d_head, kv_heads, k_total, 1, kTile) && head_map(&mv, a.v, d_head, kv_heads, k_total, 1, kTile);
+    else
+        mk = mv = mq;   // there is no key to load
+    if (!ok) {
+        set_error("%s: the strides of q, k or v cannot be described as a tensor map", who);
+        return CS_ERR_UNSUPPORTED;
+    }
     const bool h = q->dtype == CS_F16;
-    const cudaError_t e = d_head == 64 ? (h ? go(prompt_kernel<__half, 64>) : go(prompt_kernel<__nv_bfloat16, 64>))
-                                       : (h ? go(prompt_kernel<__half, 128>) : go(prompt_kernel<__nv_bfloat16, 128>));
+    auto go = [&](auto run) { return run(a, plan, mq, mk, mv, (cudaStream_t)stream); };
+    const cudaError_t e = d_head == 64 ? (h ? go(run_prompt<64, false>) : go(run_prompt<64, true>))
+                                       : (h ? go(run_prompt<128, false>) : go(run_prompt<128, true>));
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
