@@ -3,24 +3,28 @@
 // 4-bit cache (cs_qtree.cu) share.
 //
 // The query heads that share a key/value head are rows of one matrix product:
-// a row tile has 128 rows, token by token and within a token head by head, and
-// a CTA works on a pair of row tiles, so that every key and value tile in
-// shared memory is used for 256 rows.  Per tile of 128 keys and row tile t
+// a row tile has 128 rows, token by token and within a token head by head.  A
+// CTA works on two streams of key tiles of 128 keys, each with a warpgroup of its
+// own, whose threads have a row each, and 128 + d columns of tensor memory:
 //     S_t = Q_t K^T   (tcgen05, operands in shared memory, S in tensor memory),
-//     P_t = 2^(c (S_t - m) + shift)     by the 128 threads of warpgroup t,
+//     P_t = 2^(c (S_t - m) + shift)     by the threads of warpgroup t,
 //     O_t += P_t V    (tcgen05, P_t from tensor memory, where it takes S_t's place).
-// One warp issues all products, in the order
-//     S_0(0) S_1(0) | P_0(0)V S_0(1) | P_1(0)V S_1(1) | P_0(1)V S_0(2) ...
-// so that one row tile's products run while the other one's P is worked out.
-// A thread has a whole row: no shuffles, and its statistics stay in registers.
+// Wide work is a pair of row tiles: the streams are the two tiles, over the same
+// keys, and every key and value tile in shared memory serves 256 rows.  Narrow
+// work is one row tile: the streams take its keys in turn, and at the end
+// warpgroup 0 adds up both.  One thread issues all products, in the order
+//     S_0 S_1 | P_0 V  S_0 | P_1 V  S_1 | P_0 V  S_0 ...
+// so that one stream's products run while the other one's P is worked out.
 //
-// A row's m follows its maximum only when that leads by more than 2^kLead in p;
+// A thread has a whole row: no shuffles, and its statistics stay in registers.
+// It reads its scores twice, for the maximum and for P, rather than hold 128 of
+// them.  m follows the maximum only when that leads by more than 2^kLead in p;
 // then the thread scales its row of O, which the order above leaves alone: S_t's
 // commit covers the product with V before it.
 //
 // Work that is cut along the keys leaves records (each row's m, sum of p and
-// sums of p v, in 32 bits); the CTA that finishes a row tile pair's last piece adds
-// them up in the pieces' order, whoever comes last.
+// sums of p v, in 32 bits); the CTA that finishes the last piece of a work
+// adds them up in the pieces' order, whoever comes last.
 #pragma once
 
 #include <cuda.h>
@@ -37,6 +41,7 @@ constexpr int kBlock = 16384;         // bytes of 128 rows x 64 channels of 16 b
 constexpr float kLead = 8.f;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kTmemCols = 512;        // S_0, S_1 (128 each), O_0, O_1 (d each)
+constexpr int kParts = 2;             // P is handed over in halves of a key tile
 
 // ------------------------------------------------------------------- PTX forms
 
@@ -150,7 +155,7 @@ struct Work {
     int j0, j1;       // key tiles of this piece
     int pieces, p;    // the pair's pieces, and which this is
     int rec;          // the first piece's place among one head's records
-    int spare;
+    int narrow;       // one row tile, whose keys the streams take in turn
 };
 static_assert(sizeof(Work) == 48, "three 16-byte loads");
 
@@ -183,7 +188,8 @@ template <int STAGES>
 struct Bars {
     uint64_t q_full, q_empty;
     uint64_t full[STAGES], empty[STAGES];   // a stage holds one key or one value tile
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][kParts], o_full[2];
+    uint64_t ready, taken;                  // narrow work: stream 1 is done; it has been added to stream 0
     uint64_t written, told;                 // a record is written; whether it was the last
     uint64_t drain;
 };
@@ -197,9 +203,11 @@ __device__ __forceinline__ void init_bars(Bars<STAGES> &b, int q_writers, int wr
     }
     for (int t = 0; t < 2; ++t) {
         mbar_init(&b.s_full[t], 1);
-        mbar_init(&b.p_full[t], kTile);
+        for (int i = 0; i < kParts; ++i) mbar_init(&b.p_full[t][i], kTile);
         mbar_init(&b.o_full[t], 1);
     }
+    mbar_init(&b.ready, kTile);
+    mbar_init(&b.taken, kTile);
     mbar_init(&b.written, kPair);
     mbar_init(&b.told, 1);
     mbar_init(&b.drain, 1);
@@ -217,81 +225,125 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint32
     return __all_sync(kFull, wait(bar, parity, err));
 }
 
-// The key tiles of row tile t in this piece end where its last token's keys do.
-struct Span {
-    int toks, end;   // tokens of the tile; key tiles [j0, end), none if end <= j0
+// A work's streams: stream t has key tiles first[t], first[t] + step, ... below end[t]; last: the end of both.
+struct Streams {
+    int first[2], end[2], step, last;
 };
-__device__ __forceinline__ Span span_of(const Work &w, int t, int per, int step) {
-    Span s;
-    s.toks = min(per, w.toks - t * per);
-    const int lim = s.toks > 0 ? min(max(w.lim0 + step * (t * per + s.toks - 1), 0), w.n_k) : 0;
-    s.end = min(w.j1, (lim + kTile - 1) / kTile);
+// ends: where row tile t's keys end (at most j1)
+__device__ __forceinline__ Streams streams_of(const Work &w, int end0, int end1) {
+    Streams s;
+    s.first[0] = w.j0;
+    s.first[1] = w.narrow ? w.j0 + 1 : w.j0;
+    s.end[0] = end0;
+    s.end[1] = w.narrow ? end0 : end1;
+    s.step = w.narrow ? 2 : 1;
+    s.last = max(s.end[0], s.end[1]);
     return s;
+}
+
+// The order in which a work's key and value tiles are used: every key tile, and after it the value tile `ahead` key tiles
+// back, so that a stream's next scores come right behind its product with V.
+template <typename F>
+__device__ __forceinline__ bool tiles_in_order(const Streams &s, F tile) {
+    const int ahead = s.step;
+    for (int j = s.first[0]; j < s.last + ahead; ++j) {
+        if (j - ahead >= s.first[0] && !tile(true, j - ahead)) return false;
+        if (j < s.last && !tile(false, j)) return false;
+    }
+    return true;
 }
 
 // ------------------------------------------------------------- the products' warp
 
-// Issues a work's products; one thread.  it: key and value tiles so far (a ring of STAGES), n_p: P tiles so far.
+// Issues a work's products; one thread.
 struct MmaState {
-    uint32_t it = 0, n_q = 0, n_p[2] = {0, 0};
+    uint32_t it = 0, n_q = 0, n_p[2] = {0, 0};   // key and value tiles (a ring of STAGES), works, P tiles so far
 };
 template <int D, bool BF16, int STAGES>
-__device__ __forceinline__ bool issue_work(const Work &w, const int (&end)[2], Bars<STAGES> &b, uint32_t tmem, uint32_t q_at, uint32_t ring,
+__device__ __forceinline__ bool issue_work(const Streams &w, bool narrow, Bars<STAGES> &b, uint32_t tmem, uint32_t q_at, uint32_t ring,
                                            MmaState &st, uint32_t *err) {
     constexpr uint32_t kS = mma_desc(BF16, false, kTile), kO = mma_desc(BF16, true, D);
-    constexpr int DB = D / 64;
-    const int last = max(end[0], end[1]);
-    if (last <= w.j0) return true;
-    auto scores = [&](int t, uint32_t stage) {
+    constexpr int DB = D / 64, STEPS = kTile / 16 / kParts;
+    const int first = w.first[0];
+    if (w.last <= first) return true;
+    uint32_t stage = 0, parity = 0;
+    auto next = [&]() {
+        stage = st.it % STAGES;
+        parity = st.it / STAGES & 1;
+        ++st.it;
+        return wait(&b.full[stage], parity, err);
+    };
+    auto scores = [&](int t) {
+        const uint64_t q = mat_desc(q_at + (narrow ? 0 : t) * DB * kBlock, 16, 1024), k = mat_desc(ring + stage * DB * kBlock, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t in = (kk >> 2) * kBlock + (kk & 3) * 32;
-            mma_ss(tmem + t * kTile, mat_desc(q_at + t * DB * kBlock + in, 16, 1024), mat_desc(ring + stage * DB * kBlock + in, 16, 1024),
-                   kS, kk > 0);
+            const uint32_t in = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + t * kTile, q + in, k + in, kS, kk > 0);
         }
         mma_commit(&b.s_full[t]);
     };
+    auto values = [&](int t, int j) {
+        const uint64_t v = mat_desc(ring + stage * DB * kBlock, kBlock, 1024);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if (!wait(&b.p_full[t][i], st.n_p[t] & 1, err)) return false;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                const int kk = i * STEPS + k;
+                mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8, v + (kk * 2048 >> 4), kO, j > w.first[t] || kk > 0);
+            }
+        }
+        ++st.n_p[t];
+        if (j + w.step >= w.end[t]) mma_commit(&b.o_full[t]);
+        return true;
+    };
     if (!wait(&b.q_full, st.n_q & 1, err)) return false;
     ++st.n_q;
-    uint32_t ks = st.it % STAGES;
-    if (!wait(&b.full[ks], st.it / STAGES & 1, err)) return false;
+    if (narrow) {
+        for (int j = first; j < w.last + 2; ++j) {
+            const int t = (j - first) & 1;
+            if (j - 2 >= first) {
+                if (!next() || !values(t, j - 2)) return false;
+                mma_commit(&b.empty[stage]);
+            }
+            if (j < w.last) {
+                if (!next()) return false;
+                tc_after();
+                scores(t);
+                mma_commit(&b.empty[stage]);
+                if (j + 1 == w.last) mma_commit(&b.q_empty);
+            }
+        }
+        return true;
+    }
+    if (!next()) return false;
     tc_after();
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-        if (w.j0 < end[t]) scores(t, ks);
-    mma_commit(&b.empty[ks]);
-    if (w.j0 + 1 == last) mma_commit(&b.q_empty);
-    ++st.it;
-    for (int j = w.j0; j < last; ++j) {
-        const uint32_t vs = st.it % STAGES, vp = st.it / STAGES & 1;
-        ++st.it;
-        const bool more = j + 1 < last;
-        uint32_t kp = 0;
+        if (first < w.end[t]) scores(t);
+    mma_commit(&b.empty[stage]);
+    if (first + 1 == w.last) mma_commit(&b.q_empty);
+    for (int j = first; j < w.last; ++j) {
+        if (!next()) return false;
+        const uint32_t vs = stage;
+        uint32_t ks = 0;
+        const bool more = j + 1 < w.last;
         if (more) {
-            ks = st.it % STAGES;
-            kp = st.it / STAGES & 1;
-            ++st.it;
+            if (!next()) return false;
+            ks = stage;
         }
-        if (!wait(&b.full[vs], vp, err)) return false;
-        if (more && !wait(&b.full[ks], kp, err)) return false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (j >= end[t]) continue;
-            if (!wait(&b.p_full[t], st.n_p[t] & 1, err)) return false;
-            ++st.n_p[t];
-            tc_after();
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8,
-                       mat_desc(ring + vs * DB * kBlock + kk * 2048, kBlock, 1024), kO, j > w.j0 || kk > 0);
-            if (j + 1 == end[t]) mma_commit(&b.o_full[t]);
-            if (j + 1 < end[t]) scores(t, ks);
+            if (j >= w.end[t]) continue;
+            stage = vs;
+            if (!values(t, j)) return false;
+            stage = ks;
+            if (j + 1 < w.end[t]) scores(t);
         }
         mma_commit(&b.empty[vs]);
-        if (more) {
-            mma_commit(&b.empty[ks]);
-            if (j + 2 == last) mma_commit(&b.q_empty);
-        }
+        if (more) mma_commit(&b.empty[ks]);
+        if (j + 2 == w.last) mma_commit(&b.q_empty);
     }
     return true;
 }
@@ -300,7 +352,7 @@ __device__ __forceinline__ bool issue_work(const Work &w, const int (&end)[2], B
 
 struct RowState {
     float m, l;   // the maximum that p is taken against (-inf: none yet), the sum of p
-    uint32_t n_s = 0, n_o = 0, n_rec = 0;   // waits so far
+    uint32_t n_s = 0, n_o = 0, n_join = 0, n_rec = 0;   // waits so far
 };
 
 // fp16's p are taken 2^7 larger, so that those of 2^-31 of the largest are still there: with m following
@@ -308,38 +360,44 @@ struct RowState {
 template <bool BF16>
 constexpr float kShift = BF16 ? 0.f : 7.f;
 
-// A row tile's key tiles [j0, end): its rows' statistics in r, their sums of p v in tensor memory.  mask(j, s): what the
-// row does not see becomes -inf.
+// Stream t's key tiles first, first + step, ... below end: its rows' statistics in r, their sums of p v in tensor memory.
+// mask(j, w): whether the rows of the warp see not all keys of tile j, and then the bits of those that this row sees.
 template <int D, bool BF16, int STAGES, typename Mask>
-__device__ __forceinline__ bool softmax_rows(RowState &r, int j0, int end, int t, Bars<STAGES> &b, uint32_t tmem, float c, bool neg,
-                                             uint32_t *err, Mask mask) {
+__device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, int step, int t, Bars<STAGES> &b, uint32_t tmem, float c,
+                                             bool neg, uint32_t *err, Mask mask) {
     const uint32_t lane = ((threadIdx.x & 127) & ~31u) << 16;
     const uint32_t s_at = tmem + lane + t * kTile, o_at = tmem + lane + 2 * kTile + t * D;
     r.m = -INFINITY;
     r.l = 0.f;
     float base = 0.f, lead = -INFINITY;   // m, or 0 where that is -inf; a score beyond `lead` moves m
-    for (int j = j0; j < end; ++j) {
+    for (int j = first; j < end; j += step) {
+        uint32_t w[4];
+        const bool masked = mask(j, w);
         if (!wait_warp(&b.s_full[t], r.n_s & 1, err)) return false;
         ++r.n_s;
         tc_after();
-        float s[kTile];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+            float s[2][32];
+            tm_ld32(s_at, s[0]);
+            tm_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tm_ld32(s_at + 32 * i, s + 32 * i);
-        tm_wait_ld();
-        if (neg) {
+            for (int i = 0; i < 4; ++i) {
+                float (&x)[32] = s[i & 1];
+                if (i < 3) tm_ld32(s_at + 32 * (i + 1), s[(i + 1) & 1]);
+                if (masked || neg) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i) s[i] = -s[i];
+                    for (int e = 0; e < 32; ++e) x[e] = masked && !(w[i] >> e & 1u) ? -INFINITY : neg ? -x[e] : x[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], x[e + 4 + q]);
+                if (i < 3) tm_wait_ld();
+                if (masked || neg) tm_st32(s_at + 32 * i, x);
+            }
+            if (masked || neg) tm_wait_st();
         }
-        mask(j, s);
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = max3(s[i], s[4 + i], s[8 + i]);
-#pragma unroll
-        for (int i = 12; i + 8 <= kTile; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (__any_sync(kFull, top > lead)) {
             const float m = top > lead ? top : r.m;
@@ -348,8 +406,8 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int j0, int end, int t
             base = m == -INFINITY ? 0.f : m;
             lead = m == -INFINITY ? -INFINITY : m + kLead / c;
             r.l *= keep;
-            if (j > j0) {
-#pragma unroll
+            if (j > first) {
+#pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
                     float o[32];
                     tm_ld32(o_at + 32 * i, o);
@@ -362,31 +420,106 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int j0, int end, int t
         }
         const float add = fmaf(-base, c, kShift<BF16>);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float s[2][32];
+        tm_ld32(s_at, s[0]);
+        tm_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            float (&v)[32] = s[i & 1];
+            if (i < 3) tm_ld32(s_at + 32 * (i + 1), s[(i + 1) & 1]);
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                float &x = s[32 * i + 2 * e], &y = s[32 * i + 2 * e + 1];
+                float &x = v[2 * e], &y = v[2 * e + 1];
                 fma2(x, y, c, add);
                 x = ex2(x);
                 y = ex2(y);
                 p[e] = pack2<BF16>(x, y);
                 add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], x, y);
             }
+            // P's columns 16 i .. are scores that have been read: of tile i / 2
+            if (i < 3) tm_wait_ld();
             tm_st16(s_at + 16 * i, p);
+            if ((i + 1) % (4 / kParts) == 0) {
+                tm_wait_st();
+                tc_before();
+                mbar_arrive(&b.p_full[t][(i + 1) / (4 / kParts) - 1]);
+            }
         }
         r.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tm_wait_st();
-        tc_before();
-        mbar_arrive(&b.p_full[t]);
     }
-    if (j0 < end) {
+    if (first < end) {
         if (!wait_warp(&b.o_full[t], r.n_o & 1, err)) return false;
         ++r.n_o;
         tc_after();
     }
     return true;
+}
+
+// What a warpgroup has to do with a work's sums when its stream is done.
+struct Sums {
+    float f0, f1;        // factors of this row's sums of stream t, and of stream 1 for narrow work
+    bool some, other;    // whether there are such sums
+};
+
+// Narrow work: warpgroup 0 takes stream 1's statistics over into r, and gets the streams' factors.
+template <int STAGES>
+__device__ __forceinline__ bool join_streams(RowState &r, const Streams &w, int t, Bars<STAGES> &b, float2 *stat, float c, Sums &s, uint32_t *err) {
+    const int row = threadIdx.x & 127;
+    s.some = w.first[t] < w.end[t];
+    s.f0 = s.f1 = 1.f;
+    s.other = false;
+    if (w.step == 1) return true;
+    if (t == 1) {
+        stat[row] = make_float2(r.m, r.l);
+        tc_before();
+        mbar_arrive(&b.ready);
+        return true;
+    }
+    if (!wait_warp(&b.ready, r.n_join & 1, err)) return false;
+    tc_after();
+    const float2 o = stat[row];
+    s.other = w.first[1] < w.end[1];
+    if (!s.other) return true;
+    const float m = fmaxf(r.m, o.x), base = m == -INFINITY ? 0.f : m;
+    s.f0 = ex2((r.m - base) * c);
+    s.f1 = ex2((o.x - base) * c);
+    r.l = fmaf(s.f0, r.l, s.f1 * o.y);
+    r.m = m;
+    return true;
+}
+// The end of narrow work: stream 1's tensor memory is free again.
+template <int STAGES>
+__device__ __forceinline__ bool leave_streams(RowState &r, const Streams &w, int t, Bars<STAGES> &b, uint32_t *err) {
+    if (w.step == 1) return true;
+    const uint32_t parity = r.n_join++ & 1;
+    if (t == 0) {
+        tc_before();
+        mbar_arrive(&b.taken);
+        return true;
+    }
+    if (!wait_warp(&b.taken, parity, err)) return false;
+    tc_after();
+    return true;
+}
+
+// 32 columns of a row's sums, of both streams.
+template <int D>
+__device__ __forceinline__ void load_sums(uint32_t o_at, int i, const Sums &s, float (&o)[32]) {
+    if (s.some) {
+        tm_ld32(o_at + 32 * i, o);
+        tm_wait_ld();
+        if (s.other) {
+            float x[32];
+            tm_ld32(o_at + D + 32 * i, x);
+            tm_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(s.f1, x[e], s.f0 * o[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+    }
 }
 
 // After a piece's record is written: whether this CTA's is the pair's last piece (-1: a wait gave up).  All 256 threads of

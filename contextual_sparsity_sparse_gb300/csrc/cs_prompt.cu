@@ -22,7 +22,7 @@ namespace cs {
 namespace {
 
 constexpr int kMaxGroup = 128;         // query heads of one key/value head
-constexpr int kPromptThreads = 384;    // two warpgroups of rows, and one of which two warps issue products and loads
+constexpr int kPromptThreads = 320;    // two warpgroups of rows, the products' warp, the loads' warp
 constexpr int kPlanThreads = 1024;
 constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in records than they win
 
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Pl
         w.k0 = ks[b];
         w.pieces = pieces;
         w.rec = pieces > 1 ? atomicAdd(&works, pieces) : 0;
-        w.spare = 0;
+        w.narrow = w.toks <= a.per;
         const int to = atomicAdd(&hist[bin_of((tiles + pieces - 1) / pieces)], pieces);
         for (int p = 0; p < pieces; ++p) {
             w.j0 = (int)((long long)tiles * p / pieces);
@@ -234,6 +234,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
     extern __shared__ uint8_t dsm[];
     __shared__ Bars<C::STAGES> bars;
+    __shared__ float2 stat[kTile];
     __shared__ uint32_t tmem_at;
     __shared__ int flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -248,9 +249,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     pdl_launch_dependents();
     const int total = ld_dep(plan.count) * a.kv, recs = ld_dep(plan.count + 1), step = a.causal;
 
-    // Registers: 168 a thread at launch, 3 x 168 = 2 x 232 + 40.
+    // where a row tile's keys end in a work
+    auto end_of = [&](const Work &w, int t) {
+        const int toks = min(a.per, w.toks - t * a.per);
+        const int lim = toks > 0 ? min(max(w.lim0 + step * (t * a.per + toks - 1), 0), w.n_k) : 0;
+        return min(w.j1, (lim + kTile - 1) / kTile);
+    };
+
     if (warp < 8) {
-        regs_up<232>();
         const int t = warp >> 2, row = tid & 127, tok = row / a.group, g = row - tok * a.group;
         const bool neg = a.scale < 0.f;
         const float c = fabsf(a.scale) * 1.44269504088896341f;
@@ -259,82 +265,83 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             const int x = nth_work(i);
             if (x >= total) break;
             const Work w = load_work(plan.work + x / a.kv);
-            const int h = x % a.kv;
-            const Span sp = span_of(w, t, a.per, step);
-            const bool valid = tok < sp.toks;
-            const int token = w.tok0 + t * a.per + tok;
-            const int lim = valid ? min(max(w.lim0 + step * (t * a.per + tok), 0), w.n_k) : 0;
+            const int h = x % a.kv, rt = w.narrow ? 0 : t, at = rt * a.per + tok;
+            const Streams st = streams_of(w, end_of(w, 0), end_of(w, 1));
+            const bool valid = tok < a.per && at < w.toks;
+            const int token = w.tok0 + at;
+            const int lim = valid ? min(max(w.lim0 + step * at, 0), w.n_k) : 0;
             const int all = __reduce_min_sync(kFull, valid ? lim : INT_MAX);   // keys that all of the warp's rows see
-            if (!softmax_rows<D, BF16>(r, w.j0, sp.end, t, bars, tmem, c, neg, a.err, [&](int j, float (&s)[kTile]) {
-                    if (all >= (j + 1) * kTile) return;
-                    const int off = lim - j * kTile;
+            if (!softmax_rows<D, BF16>(r, st.first[t], st.end[t], st.step, t, bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
+                    if (all >= (j + 1) * kTile) return false;
 #pragma unroll
-                    for (int e = 0; e < kTile; ++e) s[e] = e < off ? s[e] : -INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        const int n = lim - j * kTile - 32 * e;
+                        m[e] = n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u;
+                    }
+                    return true;
                 }))
                 break;
-            const bool some = w.j0 < sp.end;
-            const uint32_t o_at = tmem + (((uint32_t)row & ~31u) << 16) + 2 * kTile + t * D;
+            Sums sums;
+            if (!join_streams(r, st, t, bars, stat, c, sums, a.err)) break;
+            const bool mine = !(w.narrow && t == 1);   // whose rows these are
             T *out = reinterpret_cast<T *>(a.out.p) + token * a.out.ldt + (int64_t)(h * a.group + g) * a.out.ldh;
             float *rec = w.pieces > 1 ? plan.rec + (int64_t)(h * recs + w.rec) * rec_floats(D) : nullptr;
-            float *my = w.pieces > 1 ? rec + w.p * rec_floats(D) + t * kTile + row : nullptr;
-            const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-            if (my) {
-                __stcg(my, r.m);
-                __stcg(my + kPair, r.l);
-            }
-            float odd = r.l * 0.f;   // NaN, if anything is not finite
-#pragma unroll
-            for (int b = 0; b < D / 32; ++b) {
-                float o[32];
-                if (some) {
-                    tm_ld32(o_at + 32 * b, o);
-                    tm_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) odd = fmaf(o[e], 0.f, odd);
+            if (mine) {
+                const uint32_t o_at = tmem + (((uint32_t)row & ~31u) << 16) + 2 * kTile + t * D;
+                float *my = rec ? rec + w.p * rec_floats(D) + rt * kTile + row : nullptr;
+                const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
                 if (my) {
-                    if (some && valid) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) __stcg(my + (2 + 32 * b + e) * kPair, o[e]);
-                    }
-                } else if (valid) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= inv;
-                    store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o);
+                    __stcg(my, r.m);
+                    __stcg(my + kPair, r.l);
                 }
-            }
-            uint32_t again = __ballot_sync(kFull, valid && some && !(odd == 0.f));
-            while (again) {
-                const int from = __ffs(again) - 1;
-                again &= again - 1;
-                const int rt = __shfl_sync(kFull, token, from), rg = __shfl_sync(kFull, g, from), rl = __shfl_sync(kFull, lim, from);
-                float m, l, o[D / 32];
-                prompt_row<T, D>(a, rt, h * a.group + rg, w.k0, w.j0 * kTile, min(w.j1 * kTile, rl), c, kShift<BF16>, m, l, o);
-                T *to = reinterpret_cast<T *>(a.out.p) + rt * a.out.ldt + (int64_t)(h * a.group + rg) * a.out.ldh;
-                float *ro = my ? my - lane + from : nullptr;
-#pragma unroll
+                float odd = r.l * 0.f;   // NaN, if anything is not finite
+#pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
-                    if (my) __stcg(ro + (2 + 32 * b + lane) * kPair, o[b]);
-                    else to[32 * b + lane] = (T)(l == 0.f ? 0.f : o[b] / l);
+                    float o[32];
+                    load_sums<D>(o_at, b, sums, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) odd = fmaf(o[e], 0.f, odd);
+                    if (my) {
+                        if (sums.some && valid) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) __stcg(my + (2 + 32 * b + e) * kPair, o[e]);
+                        }
+                    } else if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= inv;
+                        store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o);
+                    }
                 }
-                if (my && lane == 0) {
-                    __stcg(ro, m);
-                    __stcg(ro + kPair, l);
+                uint32_t again = __ballot_sync(kFull, valid && sums.some && !(odd == 0.f));
+                while (again) {
+                    const int from = __ffs(again) - 1;
+                    again &= again - 1;
+                    const int rt = __shfl_sync(kFull, token, from), rg = __shfl_sync(kFull, g, from), rl = __shfl_sync(kFull, lim, from);
+                    float m, l, o[D / 32];
+                    prompt_row<T, D>(a, rt, h * a.group + rg, w.k0, w.j0 * kTile, min(w.j1 * kTile, rl), c, kShift<BF16>, m, l, o);
+                    T *to = reinterpret_cast<T *>(a.out.p) + rt * a.out.ldt + (int64_t)(h * a.group + rg) * a.out.ldh;
+                    float *ro = my ? my - lane + from : nullptr;
+#pragma unroll
+                    for (int b = 0; b < D / 32; ++b) {
+                        if (my) __stcg(ro + (2 + 32 * b + lane) * kPair, o[b]);
+                        else to[32 * b + lane] = (T)(l == 0.f ? 0.f : o[b] / l);
+                    }
+                    if (my && lane == 0) {
+                        __stcg(ro, m);
+                        __stcg(ro + kPair, l);
+                    }
                 }
             }
-            if (my) {
+            if (!leave_streams(r, st, t, bars, a.err)) break;
+            if (rec) {
                 const int last = last_piece(bars, plan.arrived + h * recs + w.rec, w.pieces, &flag, r.n_rec++, a.err);
                 if (last < 0) break;
-                if (last && valid)
-                    join_pieces<D>(rec, w.pieces, t * kTile + row, c,
+                if (last && valid && mine)
+                    join_pieces<D>(rec, w.pieces, rt * kTile + row, c,
                                    [&](int b, const float *o) { store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o); });
             }
         }
     } else if (warp == 8) {
-        regs_down<40>();
         if (lane == 0) {
             MmaState st;
             bool ok = true;
@@ -342,8 +349,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const int x = nth_work(i);
                 if (x >= total) break;
                 const Work w = load_work(plan.work + x / a.kv);
-                const int end[2] = {span_of(w, 0, a.per, step).end, span_of(w, 1, a.per, step).end};
-                ok = issue_work<D, BF16, C::STAGES>(w, end, bars, tmem, q_at, ring, st, a.err);
+                ok = issue_work<D, BF16, C::STAGES>(streams_of(w, end_of(w, 0), end_of(w, 1)), w.narrow, bars, tmem, q_at, ring, st, a.err);
             }
             if (!ok) {
                 mma_commit(&bars.drain);
@@ -351,41 +357,38 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (warp == 9) {
-        regs_down<40>();
+    } else {
         if (lane == 0) {
             uint32_t it = 0, n_q = 0;
             bool ok = true;
-            auto tile = [&](const CUtensorMap *m, int h, int row) {
-                const uint32_t s = it % C::STAGES;
-                if (it >= C::STAGES && !wait(&bars.empty[s], (it / C::STAGES - 1) & 1, a.err)) return false;
-                mbar_arrive_expect_tx(&bars.full[s], C::DB * kBlock);
-#pragma unroll
-                for (int b = 0; b < C::DB; ++b) load_box(ring + (s * C::DB + b) * kBlock, m, 64 * b, h, row, &bars.full[s]);
-                ++it;
-                return true;
-            };
             for (int i = 0; ok; ++i) {
                 const int x = nth_work(i);
                 if (x >= total) break;
                 const Work w = load_work(plan.work + x / a.kv);
                 const int h = x % a.kv;
-                const int end[2] = {span_of(w, 0, a.per, step).end, span_of(w, 1, a.per, step).end};
-                const int last = max(end[0], end[1]);
-                if (last <= w.j0) continue;
+                const Streams st = streams_of(w, end_of(w, 0), end_of(w, 1));
+                if (st.last <= w.j0) continue;
                 if (n_q > 0 && !wait(&bars.q_empty, (n_q - 1) & 1, a.err)) {
                     ok = false;
                     break;
                 }
                 ++n_q;
-                const uint32_t bytes = C::DB * a.per * a.group * 128;
-                mbar_arrive_expect_tx(&bars.q_full, bytes * ((w.j0 < end[0]) + (w.j0 < end[1])));
+                const int q0 = w.j0 < end_of(w, 0), q1 = !w.narrow && w.j0 < st.end[1];
+                mbar_arrive_expect_tx(&bars.q_full, C::DB * a.per * a.group * 128 * (q0 + q1));
                 for (int t = 0; t < 2; ++t)
-                    if (w.j0 < end[t])
+                    if (t == 0 ? q0 : q1)
                         for (int b = 0; b < C::DB; ++b)
                             load_box(q_at + (t * C::DB + b) * kBlock, &mq, 64 * b, h * a.group, w.tok0 + t * a.per, &bars.q_full);
-                for (int j = w.j0; ok && j < last; ++j)
-                    ok = tile(&mk, h, w.k0 + j * kTile) && tile(&mv, h, w.k0 + j * kTile);
+                ok = tiles_in_order(st, [&](bool value, int j) {
+                    const uint32_t s = it % C::STAGES;
+                    if (it >= C::STAGES && !wait(&bars.empty[s], (it / C::STAGES - 1) & 1, a.err)) return false;
+                    mbar_arrive_expect_tx(&bars.full[s], C::DB * kBlock);
+#pragma unroll
+                    for (int b = 0; b < C::DB; ++b)
+                        load_box(ring + (s * C::DB + b) * kBlock, value ? &mv : &mk, 64 * b, h, w.k0 + j * kTile, &bars.full[s]);
+                    ++it;
+                    return true;
+                });
             }
             if (!ok) {
                 // what is under way lands before the memory is given back
@@ -395,8 +398,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else {
-        regs_down<40>();
     }
     tc_before();
     __syncthreads();
