@@ -12,7 +12,7 @@
 // Wide work is a pair of row tiles: the streams are the two tiles, over the same
 // keys, and every key and value tile in shared memory serves 256 rows.  Narrow
 // work is one row tile: the streams take its keys in turn, and at the end
-// warpgroup 0 adds up both.  One thread issues all products, in the order
+// warpgroup 0 adds up both.  One warp issues all products, in the order
 //     S_0 S_1 | P_0 V  S_0 | P_1 V  S_1 | P_0 V  S_0 ...
 // so that one stream's products run while the other one's P is worked out.
 //
@@ -56,18 +56,23 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool b_mn, int n) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kTile >> 4) << 24);
 }
+// Products and commits are issued by one thread, but by a warp that stays together, so that the compiler knows descriptors and
+// addresses to be the same in all its threads: with one thread in a branch of its own each product took 70 cycles to
+// issue, and the 16 products of a key tile and stream were what bounded the kernel.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+    asm volatile("{\n\t.reg .pred p, one;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(desc), "r"(acc ? 1u : 0u));
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+    asm volatile("{\n\t.reg .pred p, one;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
                  "r"(a), "l"(b), "r"(desc), "r"(acc ? 1u : 0u));
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+    asm volatile("{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+                 "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -214,15 +219,19 @@ __device__ __forceinline__ void init_bars(Bars<STAGES> &b, int q_writers, int wr
     mbar_fence_init();
 }
 
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint32_t *err) {
+// Waits that are not over at the first look; kept out of the loops, whose code the streams' warps fetch side by side.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint32_t *err) {
     if (mbar_wait(bar, parity, kWaitNs)) return true;
     atomicOr(err, CS_DEVERR_TIMEOUT);
     return false;
 }
-
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint32_t *err) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, err);
+}
 // The same for a whole warp, which goes on or gives up together.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint32_t *err) {
-    return __all_sync(kFull, wait(bar, parity, err));
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(kFull, wait_long(bar, parity, err));
 }
 
 // A work's streams: stream t has key tiles first[t], first[t] + step, ... below end[t]; last: the end of both.
@@ -241,6 +250,9 @@ __device__ __forceinline__ Streams streams_of(const Work &w, int end0, int end1)
     return s;
 }
 
+// The same value in all of a warp's threads, as the compiler can see.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFull, x, 0); }
+
 // The order in which a work's key and value tiles are used: every key tile, and after it the value tile `ahead` key tiles
 // back, so that a stream's next scores come right behind its product with V.
 template <typename F>
@@ -255,25 +267,31 @@ __device__ __forceinline__ bool tiles_in_order(const Streams &s, F tile) {
 
 // ------------------------------------------------------------- the products' warp
 
-// Issues a work's products; one thread.
+// Issues a work's products; a whole warp, whose arguments are the same in all threads.  (With a warp for each stream both
+// streams' products share the tensor cores, and each stream waits twice as long for its own: 8,192 tokens of 16 heads 541 us
+// instead of 412.)
 struct MmaState {
-    uint32_t it = 0, n_q = 0, n_p[2] = {0, 0};   // key and value tiles (a ring of STAGES), works, P tiles so far
+    uint32_t stage = 0, parity = 0, n_q = 0, n_p[2] = {0, 0};   // the ring's next tile; works and P tiles so far
 };
 template <int D, bool BF16, int STAGES>
-__device__ __forceinline__ bool issue_work(const Streams &w, bool narrow, Bars<STAGES> &b, uint32_t tmem, uint32_t q_at, uint32_t ring,
-                                           MmaState &st, uint32_t *err) {
+__device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, uint32_t tmem, uint32_t q_at, uint32_t ring, MmaState &st,
+                                           uint32_t *err) {
     constexpr uint32_t kS = mma_desc(BF16, false, kTile), kO = mma_desc(BF16, true, D);
     constexpr int DB = D / 64, STEPS = kTile / 16 / kParts;
     const int first = w.first[0];
+    const bool narrow = w.step == 2;
     if (w.last <= first) return true;
-    uint32_t stage = 0, parity = 0;
+    uint32_t stage = 0;
     auto next = [&]() {
-        stage = st.it % STAGES;
-        parity = st.it / STAGES & 1;
-        ++st.it;
-        return wait(&b.full[stage], parity, err);
+        stage = st.stage;
+        const uint32_t parity = st.parity;
+        if (++st.stage == STAGES) {
+            st.stage = 0;
+            st.parity ^= 1;
+        }
+        return wait_warp(&b.full[stage], parity, err);
     };
-    auto scores = [&](int t) {
+    auto scores = [&](int t, uint32_t stage) {
         const uint64_t q = mat_desc(q_at + (narrow ? 0 : t) * DB * kBlock, 16, 1024), k = mat_desc(ring + stage * DB * kBlock, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -282,68 +300,51 @@ __device__ __forceinline__ bool issue_work(const Streams &w, bool narrow, Bars<S
         }
         mma_commit(&b.s_full[t]);
     };
-    auto values = [&](int t, int j) {
+    auto values = [&](int t, uint32_t stage, bool fresh, bool done) {
         const uint64_t v = mat_desc(ring + stage * DB * kBlock, kBlock, 1024);
+        const uint32_t n = t ? st.n_p[1]++ : st.n_p[0]++;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-            if (!wait(&b.p_full[t][i], st.n_p[t] & 1, err)) return false;
+            if (!wait_warp(&b.p_full[t][i], n & 1, err)) return false;
             tc_after();
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
                 const int kk = i * STEPS + k;
-                mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8, v + (kk * 2048 >> 4), kO, j > w.first[t] || kk > 0);
+                mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + kk * 8, v + (kk * 2048 >> 4), kO, !fresh || kk > 0);
             }
         }
-        ++st.n_p[t];
-        if (j + w.step >= w.end[t]) mma_commit(&b.o_full[t]);
+        if (done) mma_commit(&b.o_full[t]);
         return true;
     };
-    if (!wait(&b.q_full, st.n_q & 1, err)) return false;
+    if (!wait_warp(&b.q_full, st.n_q & 1, err)) return false;
     ++st.n_q;
-    if (narrow) {
-        for (int j = first; j < w.last + 2; ++j) {
-            const int t = (j - first) & 1;
-            if (j - 2 >= first) {
-                if (!next() || !values(t, j - 2)) return false;
-                mma_commit(&b.empty[stage]);
+    uint32_t vs = 0, ks = 0;
+    // the streams in turn: scores of key tile j, behind the product with the value tile that lies a step back
+    const int turns = narrow ? w.last - first + 2 : 2 * (w.last - first + 1);
+#pragma unroll 1
+    for (int i = 0; i < turns; ++i) {
+        const int t = i & 1, j = first + (narrow ? i : i >> 1), jv = j - w.step, end = t ? w.end[1] : w.end[0];
+        if (narrow || t == 0) {
+            if (jv >= first) {
+                if (!next()) return false;
+                vs = stage;
             }
             if (j < w.last) {
                 if (!next()) return false;
-                tc_after();
-                scores(t);
-                mma_commit(&b.empty[stage]);
-                if (j + 1 == w.last) mma_commit(&b.q_empty);
+                ks = stage;
             }
         }
-        return true;
-    }
-    if (!next()) return false;
-    tc_after();
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-        if (first < w.end[t]) scores(t);
-    mma_commit(&b.empty[stage]);
-    if (first + 1 == w.last) mma_commit(&b.q_empty);
-    for (int j = first; j < w.last; ++j) {
-        if (!next()) return false;
-        const uint32_t vs = stage;
-        uint32_t ks = 0;
-        const bool more = j + 1 < w.last;
-        if (more) {
-            if (!next()) return false;
-            ks = stage;
+        if (jv >= first && jv < end) {
+            if (!values(t, vs, jv == (narrow ? first + t : first), jv + w.step >= end)) return false;
+        } else {
+            tc_after();
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if (j >= w.end[t]) continue;
-            stage = vs;
-            if (!values(t, j)) return false;
-            stage = ks;
-            if (j + 1 < w.end[t]) scores(t);
+        if (j < end) scores(t, ks);
+        if (narrow || t == 1) {
+            if (jv >= first) mma_commit(&b.empty[vs]);
+            if (j < w.last) mma_commit(&b.empty[ks]);
+            if (j == w.last - 1) mma_commit(&b.q_empty);
         }
-        mma_commit(&b.empty[vs]);
-        if (more) mma_commit(&b.empty[ks]);
-        if (j + 2 == w.last) mma_commit(&b.q_empty);
     }
     return true;
 }

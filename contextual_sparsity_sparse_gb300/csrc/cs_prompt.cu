@@ -237,17 +237,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __shared__ float2 stat[kTile];
     __shared__ uint32_t tmem_at;
     __shared__ int flag;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const uint32_t q_at = (smem_addr(dsm) + 1023u) & ~1023u, ring = q_at + 2 * C::DB * kBlock;
     if (warp == 8) tm_alloc(&tmem_at);
     if (tid == 288) init_bars(bars, 1, 1);
     tc_before();
     __syncthreads();
     tc_after();
-    const uint32_t tmem = tmem_at;
+    const uint32_t tmem = uniform(tmem_at);
     pdl_wait();
     pdl_launch_dependents();
-    const int total = ld_dep(plan.count) * a.kv, recs = ld_dep(plan.count + 1), step = a.causal;
+    const int total = uniform(ld_dep(plan.count) * a.kv), recs = ld_dep(plan.count + 1), step = a.causal;
 
     // where a row tile's keys end in a work
     auto end_of = [&](const Work &w, int t) {
@@ -342,21 +342,21 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             }
         }
     } else if (warp == 8) {
-        if (lane == 0) {
-            MmaState st;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                const int x = nth_work(i);
-                if (x >= total) break;
-                const Work w = load_work(plan.work + x / a.kv);
-                ok = issue_work<D, BF16, C::STAGES>(streams_of(w, end_of(w, 0), end_of(w, 1)), w.narrow, bars, tmem, q_at, ring, st, a.err);
-            }
-            if (!ok) {
-                mma_commit(&bars.drain);
-                mbar_wait(&bars.drain, 0, kWaitNs);
-            }
+        MmaState ms;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int x = nth_work(i);
+            if (x >= total) break;
+            Work w = load_work(plan.work + x / a.kv);
+            const int end0 = uniform(end_of(w, 0)), end1 = uniform(end_of(w, 1));
+            w.j0 = uniform(w.j0);
+            w.narrow = uniform(w.narrow);
+            ok = issue_work<D, BF16, C::STAGES>(streams_of(w, end0, end1), bars, tmem, q_at, ring, ms, a.err);
         }
-        __syncwarp();
+        if (!ok) {
+            mma_commit(&bars.drain);
+            mbar_wait(&bars.drain, 0, kWaitNs);
+        }
     } else {
         if (lane == 0) {
             uint32_t it = 0, n_q = 0;
