@@ -114,12 +114,6 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *r) {
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A warpgroup's registers per thread, out of what the block was launched with.
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -180,6 +174,89 @@ __device__ __forceinline__ Work load_work(const Work *w) {
     Work r;
     memcpy(&r, v, sizeof r);
     return r;
+}
+
+constexpr int kPlanThreads = 1024;
+constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in records than they win
+
+// Lists the works of `pairs` pairs of row tiles for kv heads: those of many key tiles first, cut along the keys so that no
+// piece is longer than an SM's share of all.  find(i, w): pair i's key tiles, and in w all of its work but the piece.  One
+// CTA of kPlanThreads; places within a size differ from run to run, what a work is does not.
+template <typename Find>
+__device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find find) {
+    constexpr int BINS = 256;
+    __shared__ int scan[32], hist[BINS], longest, recs, placed;
+    __shared__ unsigned long long units;
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        longest = recs = placed = 0;
+        units = 0;
+    }
+    if (tid < BINS) hist[tid] = 0;
+    for (int i = tid; i < plan.recs; i += kPlanThreads) plan.arrived[i] = 0;
+    __syncthreads();
+    unsigned long long sum = 0;
+    int most = 0;
+    Work w;
+    for (int i = tid; i < pairs; i += kPlanThreads) {
+        const int tiles = find(i, w);
+        sum += tiles;
+        most = max(most, tiles);
+    }
+    most = __reduce_max_sync(kFull, most);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if ((tid & 31) == 0 && sum) {
+        atomicMax(&longest, most);
+        atomicAdd(&units, sum);
+    }
+    __syncthreads();
+    // with a pair's pieces fewer than twice its tiles / chunk, all pieces of cut pairs are fewer than 2 SMs' number
+    const int chunk = (int)max((unsigned long long)kLeastPiece, (units * kv + sms - 1) / sms);
+    const int big = min(longest, chunk);
+    auto pieces_of = [&](int tiles) { return tiles > chunk && plan.recs > 0 ? (tiles + chunk - 1) / chunk : 1; };
+    auto bin_of = [&](int tiles, int pieces) {
+        return BINS - 1 - (int)((long long)min((tiles + pieces - 1) / pieces, big) * (BINS - 1) / max(big, 1));
+    };
+    for (int i = tid; i < pairs; i += kPlanThreads) {
+        const int tiles = find(i, w), pieces = pieces_of(tiles);
+        atomicAdd(&hist[bin_of(tiles, pieces)], pieces);
+        if (pieces > 1) atomicAdd(&recs, pieces);
+    }
+    __syncthreads();
+    const int mine = tid < BINS ? hist[tid] : 0;
+    int all;
+    const int place = block_excl_scan(mine, scan, &all);
+    if (tid < BINS) hist[tid] = place;
+    if (tid == 0) {
+        plan.count[0] = all;
+        plan.count[1] = recs;
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += kPlanThreads) {
+        const int tiles = find(i, w), pieces = pieces_of(tiles);
+        w.pieces = pieces;
+        w.rec = pieces > 1 ? atomicAdd(&placed, pieces) : 0;
+        const int to = atomicAdd(&hist[bin_of(tiles, pieces)], pieces);
+        for (int p = 0; p < pieces; ++p) {
+            w.j0 = (int)((long long)tiles * p / pieces);
+            w.j1 = (int)((long long)tiles * (p + 1) / pieces);
+            w.p = p;
+            plan.work[to + p] = w;
+        }
+    }
+}
+
+// A list's place: its works' number and how many records there are; returns the bytes.
+inline size_t plan_scratch(size_t works, int recs, int d, char *at, Plan *plan) {
+    const size_t list = align256((works + recs) * sizeof(Work)), arrived = align256((size_t)recs * sizeof(unsigned));
+    if (plan) {
+        plan->count = reinterpret_cast<int *>(at);
+        plan->work = reinterpret_cast<Work *>(at + 256);
+        plan->arrived = reinterpret_cast<unsigned *>(at + 256 + list);
+        plan->rec = reinterpret_cast<float *>(at + 256 + list + arrived);
+        plan->recs = recs;
+    }
+    return 256 + list + arrived + (size_t)recs * rec_floats(d) * sizeof(float);
 }
 
 // This CTA's i-th work of `total`, which are in the order of falling size: there and back over the CTAs.

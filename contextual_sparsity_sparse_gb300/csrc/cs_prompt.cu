@@ -23,8 +23,6 @@ namespace {
 
 constexpr int kMaxGroup = 128;         // query heads of one key/value head
 constexpr int kPromptThreads = 320;    // two warpgroups of rows, the products' warp, the loads' warp
-constexpr int kPlanThreads = 1024;
-constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in records than they win
 
 struct PromptK {
     QRowsK q, k, v, out;
@@ -77,19 +75,11 @@ __device__ void plan_starts(const int32_t *start, int batch, int total, int *at,
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Plan plan) {
     extern __shared__ int starts[];
-    constexpr int BINS = 256;
-    __shared__ int scan[32], hist[BINS], longest, recs, works;
-    __shared__ unsigned long long units;
+    __shared__ int scan[32];
     int *qs = starts, *ks = qs + a.batch + 1, *first = ks + a.batch + 1;
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) {
-        longest = recs = works = 0;
-        units = 0;
-    }
-    if (tid < BINS) hist[tid] = 0;
-    for (int i = tid; i < plan.recs; i += kPlanThreads) plan.arrived[i] = 0;
     plan_starts(a.q_start, a.batch, a.q_total, qs, scan, a.err);
     if (a.k_start == a.q_start) ks = qs;
     else plan_starts(a.k_start, a.batch, a.k_total, ks, scan, a.err);
@@ -106,79 +96,24 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Pl
         at += (qs[b + 1] - qs[b] + pair - 1) / pair;
     }
     __syncthreads();
-    // pair i: its sequence, its first token there, and the key tiles that it sees
-    auto find = [&](int i, int &b, int &t) {
-        int lo = 0, hi = a.batch;
+    plan_list(total, a.kv, a.sms, plan, [&](int i, Work &w) {
+        int lo = 0, hi = a.batch;   // the last sequence whose first pair is not behind i
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (first[mid] <= i) lo = mid;
             else hi = mid;
         }
-        b = lo;
-        t = (i - first[lo]) * pair;
-        const int n_q = qs[b + 1] - qs[b], n_k = ks[b + 1] - ks[b];
+        const int t = (i - first[lo]) * pair, n_q = qs[lo + 1] - qs[lo], n_k = ks[lo + 1] - ks[lo];
         const int lim = a.causal ? min(max(n_k - n_q + min(t + pair, n_q), 0), n_k) : n_k;
-        return (lim + kTile - 1) / kTile;
-    };
-    unsigned long long sum = 0;
-    int most = 0;
-    for (int i = tid; i < total; i += kPlanThreads) {
-        int b, t;
-        const int tiles = find(i, b, t);
-        sum += tiles;
-        most = max(most, tiles);
-    }
-    most = __reduce_max_sync(kFull, most);
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if ((tid & 31) == 0) {
-        atomicMax(&longest, most);
-        atomicAdd(&units, sum);
-    }
-    __syncthreads();
-    // No piece is longer than an SM's share of all; and with a pair's pieces fewer than twice its tiles / chunk, all
-    // pieces of cut pairs are fewer than 2 SMs' number.
-    const int chunk = (int)max((unsigned long long)kLeastPiece, (units * a.kv + a.sms - 1) / a.sms);
-    const int big = min(longest, chunk);
-    auto pieces_of = [&](int tiles) { return tiles > chunk && plan.recs > 0 ? (tiles + chunk - 1) / chunk : 1; };
-    auto bin_of = [&](int len) { return BINS - 1 - (int)((long long)min(len, big) * (BINS - 1) / max(big, 1)); };
-    for (int i = tid; i < total; i += kPlanThreads) {
-        int b, t;
-        const int tiles = find(i, b, t), pieces = pieces_of(tiles);
-        atomicAdd(&hist[bin_of((tiles + pieces - 1) / pieces)], pieces);
-        if (pieces > 1) atomicAdd(&recs, pieces);
-    }
-    __syncthreads();
-    const int mine = tid < BINS ? hist[tid] : 0;
-    int all;
-    const int place = block_excl_scan(mine, scan, &all);
-    if (tid < BINS) hist[tid] = place;
-    if (tid == 0) {
-        plan.count[0] = all;
-        plan.count[1] = recs;
-    }
-    __syncthreads();
-    for (int i = tid; i < total; i += kPlanThreads) {
-        int b, t;
-        const int tiles = find(i, b, t), pieces = pieces_of(tiles);
-        const int n_q = qs[b + 1] - qs[b], n_k = ks[b + 1] - ks[b];
-        Work w;
-        w.tok0 = qs[b] + t;
+        w.tok0 = qs[lo] + t;
         w.toks = min(pair, n_q - t);
-        w.seq = b;
+        w.seq = lo;
         w.lim0 = a.causal ? n_k - n_q + t + 1 : n_k;
         w.n_k = n_k;
-        w.k0 = ks[b];
-        w.pieces = pieces;
-        w.rec = pieces > 1 ? atomicAdd(&works, pieces) : 0;
+        w.k0 = ks[lo];
         w.narrow = w.toks <= a.per;
-        const int to = atomicAdd(&hist[bin_of((tiles + pieces - 1) / pieces)], pieces);
-        for (int p = 0; p < pieces; ++p) {
-            w.j0 = (int)((long long)tiles * p / pieces);
-            w.j1 = (int)((long long)tiles * (p + 1) / pieces);
-            w.p = p;
-            plan.work[to + p] = w;
-        }
-    }
+        return (lim + kTile - 1) / kTile;
+    });
 }
 
 // -------------------------------------------------------------- the attention
@@ -416,16 +351,7 @@ bool prompt_sizes(int batch, int n_heads, int kv_heads, int d_head, int q_total,
 size_t prompt_scratch(int batch, int n_heads, int kv_heads, int d, int q_total, int k_total, int sms, char *at, Plan *plan) {
     const int per = kTile / (n_heads / kv_heads);
     const int recs = k_total > kLeastPiece * kTile ? 2 * sms : 0;
-    const size_t works = (size_t)q_total / (2 * per) + batch + recs;
-    const size_t list = align256(works * sizeof(Work)), arrived = align256((size_t)recs * sizeof(unsigned));
-    if (plan) {
-        plan->count = reinterpret_cast<int *>(at);
-        plan->work = reinterpret_cast<Work *>(at + 256);
-        plan->arrived = reinterpret_cast<unsigned *>(at + 256 + list);
-        plan->rec = reinterpret_cast<float *>(at + 256 + list + arrived);
-        plan->recs = recs;
-    }
-    return 256 + list + arrived + (size_t)recs * rec_floats(d) * sizeof(float);
+    return plan_scratch((size_t)q_total / (2 * per) + batch, recs, d, at, plan);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,

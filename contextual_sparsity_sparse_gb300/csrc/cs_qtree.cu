@@ -1,25 +1,43 @@
 // Attention for a tree of drafted tokens over the 4-bit KV cache.
-#include "cs_qcache.cuh"
+//
+// The streams of cs_attn_tc.cuh over key tiles that a warpgroup makes from the
+// codes: a tile's 128 slots become fp16 values, offset + scale * code with one
+// rounding, in the layout that the products take.  The tile behind the last slot
+// holds the drafted tokens themselves, and there a row sees its own ancestors.
+// Codes come as 8 nibbles to a word, of which an AND and an OR make two fp16
+// numbers 1024 + n with n four channels apart: within 8 channels, the products
+// run in the order 0 4 1 5 2 6 3 7.  q is written in that order too, and the
+// outputs are put back when they are written.
+//
+// q's rows are scaled by powers of two to [2^14, 2^15), which fp16 holds with all
+// bits of fp16 and bf16 inputs down to 2^-29 of a row's largest.
+#include <cstddef>
+
+#include "cs_attn_tc.cuh"
 
 namespace cs {
 
 namespace {
 
-constexpr int kMaxTree = 128;   // drafted tokens of a sequence
+constexpr int kMaxTree = 128;         // drafted tokens of a sequence: one key tile
+constexpr int kTreeThreads = 512;     // two warpgroups of rows, one that makes tiles, one of which a warp issues the products
+constexpr int kMakers = 128;
+constexpr int kTreeStages = 5;
+constexpr int kSeenRing = 8;          // tiles by which the makers can be ahead of the rows, and more
+constexpr int kParentRing = 4;        // works likewise
 
 struct TreeK {
     QCacheK c;
     QRowsK q, k, v, out;
-    int heads, group, n;
+    int heads, group, n, per, kv;
     const int32_t *length, *parent, *n_new;
     float scale;
     uint32_t *err;
+    int sms;
 };
 
 // Drafted rows as the cache would take them: within fp16's range, NaN as 0.
-__device__ __forceinline__ float as_drafted(float x) {
-    return x != x ? 0.f : __half2float(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
-}
+__device__ __forceinline__ float as_drafted(float x) { return x != x ? 0.f : fminf(fmaxf(x, -65504.f), 65504.f); }
 
 __device__ __forceinline__ int tree_count(const TreeK &a, int b) {
     if (!a.n_new) return a.n;
@@ -28,70 +46,449 @@ __device__ __forceinline__ int tree_count(const TreeK &a, int b) {
     return min(max(n, 0), a.n);
 }
 
-__device__ __forceinline__ int tree_parent(const TreeK &a, int b, int t) {
-    if (!a.parent) return t - 1;
-    const int p = ld_dep(a.parent + (int64_t)b * a.n + t);
-    if (p >= -1 && p < t) return p;
-    atomicOr(a.err, CS_DEVERR_INDEX);
-    return -1;
+// Work: tok0 is a token of the tree, toks how many of the pair's the sequence has (the others' rows are zeros), n_k its slots,
+// k0 how many drafted tokens it has.
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreeK a, Plan plan) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int pair = 2 * a.per, each = (a.n + pair - 1) / pair;
+    plan_list(a.c.batch * each, a.kv, a.sms, plan, [&](int i, Work &w) {
+        const int b = i / each, t = (i - b * each) * pair;
+        w.n_k = q_length(a.length, b, a.c.cap, a.err);
+        w.tok0 = t;
+        w.k0 = tree_count(a, b);
+        w.toks = min(pair, w.k0 - t);
+        w.seq = b;
+        w.lim0 = 0;
+        w.narrow = w.toks <= a.per;
+        return w.toks > 0 ? (w.n_k + kTile - 1) / kTile + 1 : 0;
+    });
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) tree_kernel(TreeK a) {
+struct TreeCfg {
+    static constexpr int DB = D / 64;
+    static constexpr size_t smem = (size_t)(2 + kTreeStages) * DB * kBlock + 1024;
+};
+
+struct TreeShared {
+    Bars<kTreeStages> bars;
+    uint64_t seen_full[kSeenRing];
+    alignas(16) uint32_t seen[kSeenRing][4];    // of a tile of slots, those that are there
+    uint8_t parents[kParentRing][kMaxTree];     // parent + 1 of every drafted token of a work's sequence
+    float2 stat[kTile];
+    uint32_t tmem;
+    int flag;
+};
+
+static_assert(offsetof(TreeShared, seen) % 16 == 0, "read by 16 bytes");
+
+// 16-byte chunk c of row r of a 128-byte swizzled tile of 64 channels
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+__device__ __forceinline__ void sts16(uint32_t at, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) { return pack2<false>(lo, hi); }
+
+// 8 codes as fp16 values, in the products' order.
+__device__ __forceinline__ void decode8(uint32_t w, __half2 s, __half2 z, uint32_t (&v)[4]) {
+    const __half2 k1024 = __float2half2_rn(1024.f), k16th = __float2half2_rn(0.0625f), k64 = __float2half2_rn(-64.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = w >> 8 * i;
+        const __half2 a = __hsub2(u2h((x & 0x000f000fu) | 0x64006400u), k1024);        // n, exact
+        const __half2 b = __hfma2(u2h((x & 0x00f000f0u) | 0x64006400u), k16th, k64);   // (1024 + 16 n) / 16 - 64
+        v[2 * i] = h2u(__hfma2(a, s, z));
+        v[2 * i + 1] = h2u(__hfma2(b, s, z));
+    }
+}
+
+// 8 channels of a row of any of the call's types, in order.
+__device__ __forceinline__ void load8(const QRowsK &r, int64_t i, float (&x)[8]) {
+    if (r.vec) {
+        const uint4 v = ld_dep(reinterpret_cast<const uint4 *>(r.p + 2 * i));
+        if (r.dt == CS_F16) unpack<__half>(v, x);
+        else unpack<__nv_bfloat16>(v, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = q_load1(r, i + e);
+    }
+}
+
+// Codes are read once by a CTA; an append before this kernel may have written them.
+__device__ __forceinline__ uint4 load_codes(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
+// A tile's codes on their way: this thread's chunk of 32 channels of CH slots.
+template <int CH>
+struct RawTile {
+    uint4 code[CH];
+    uint32_t scale[CH];
+    int pos;              // of slot threadIdx % 128 (key tiles)
+    int entry;            // its work's place in the list, times the heads, plus the head; -1: no more tiles
+    uint32_t what;        // bit 0: values, 1: the drafted tokens, 2 ..: the key tile's place in the ring of `seen`, 5: that
+                          // place's parity, 6 ..: the work's place in the ring of parents
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan plan) {
+    using C = TreeCfg<D>;
+    constexpr int CH = D / 32, GR = D / kQGroup;
+    extern __shared__ uint8_t dsm[];
+    __shared__ TreeShared sh;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    const uint32_t q_at = (smem_addr(dsm) + 1023u) & ~1023u, ring = q_at + 2 * C::DB * kBlock;
+    if (warp == 12) tm_alloc(&sh.tmem);
+    if (tid == 416) {
+        init_bars(sh.bars, kPair, kMakers);
+        for (int i = 0; i < kSeenRing; ++i) mbar_init(&sh.seen_full[i], kMakers);
+        mbar_fence_init();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = uniform(sh.tmem);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (row >= (int64_t)a.c.batch * a.n * a.heads) return;
-    const int lane = threadIdx.x & 31, head = (int)(row % a.heads), t = (int)(row / a.heads % a.n);
-    const int b = (int)(row / a.heads / a.n), h = head / a.group;
-    const int len = q_length(a.length, b, a.c.cap, a.err), n = tree_count(a, b);
-    float x[D / 32], o[D / 32], m = -INFINITY, l = 0.f;
+    const int total = uniform(ld_dep(plan.count) * a.kv), recs = ld_dep(plan.count + 1);
+    auto streams = [&](const Work &w) { return streams_of(w, w.toks > 0 ? w.j1 : w.j0, w.toks > a.per ? w.j1 : w.j0); };
+
+    if (warp < 8) {
+        const int t = warp >> 2, row = tid & 127, tok = row / a.group, g = row - tok * a.group;
+        const bool neg = a.scale < 0.f;
+        RowState r;
+        uint32_t tiles = 0, works = 0;   // of this CTA, before this work
+        for (int i = 0;; ++i) {
+            const int x = nth_work(i);
+            if (x >= total) break;
+            const Work w = load_work(plan.work + x / a.kv);
+            const int h = x % a.kv, rt = w.narrow ? 0 : t, at = rt * a.per + tok;
+            const Streams st = streams(w);
+            const bool valid = tok < a.per && at < w.toks, there = tok < a.per && w.tok0 + at < a.n;
+            const int token = w.tok0 + at, head = h * a.group + g;
+            float c = fabsf(a.scale) * 1.44269504088896341f;
+            if (st.last > w.j0) {
+                // the row's q, twice: for its power of two, and scaled
+                const int64_t src = w.seq * a.q.ldb + token * a.q.ldt + (int64_t)head * a.q.ldh;
+                float big = 0.f;
+                if (valid) {
+#pragma unroll 4
+                    for (int e = 0; e < D; e += 8) {
+                        float v[8];
+                        load8(a.q, src + e, v);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        x[i] = a.scale * q_load1(a.q, b * a.q.ldb + t * a.q.ldt + head * a.q.ldh + lane + 32 * i);
-        o[i] = 0.f;
-    }
-    auto add = [&](const float (&k)[D / 32], const float (&v)[D / 32]) {
-        float s = 0.f;
+                        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(v[k]));
+                    }
+                }
+                const int eb = (int)(__float_as_uint(big) >> 23);
+                const int up = big > 0.f && eb < 255 ? min(141 - eb, 127) : 0;
+                const float f1 = __uint_as_float((uint32_t)(127 + up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+                // kept where c stays in fp32's range (beyond, one slot takes all as well)
+                c = fminf(fmaxf(c * exp2f((float)-up), 1.2e-38f), 1.2e30f);
+                if (rt == t) {
+#pragma unroll 2
+                    for (int e = 0; e < D; e += 8) {
+                        float v[8] = {};
+                        if (valid) load8(a.q, src + e, v);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) s = fmaf(x[i], k[i], s);
-        s = warp_sum(s);
-        const float up = fmaxf(m, s), base = up == -INFINITY ? 0.f : up;
-        const float keep = expf(m - base), p = expf(s - base);
-        m = up;
-        l = fmaf(l, keep, p);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], keep, p * v[i]);
-    };
-    if (t < n) {
-        const int64_t slot0 = a.c.slot0(b, h);
-        for (int j = 0; j < len; ++j) {
-            if (a.c.pos && ld_dep(a.c.pos + slot0 + j) < 0) continue;
-            float k[D / 32], v[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int ch = lane + 32 * i;
-                float s, z;
-                half2x(ld_dep(a.c.ks + (slot0 + j) * (D / kQGroup) + ch / kQGroup), s, z);
-                k[i] = fmaf(s, (float)(ld_dep(a.c.k + (slot0 + j) * (D / 2) + ch / 2) >> (ch & 1) * 4 & 15), z);
-                half2x(ld_dep(a.c.vs + (slot0 + j) * (D / kQGroup) + ch / kQGroup), s, z);
-                v[i] = fmaf(s, (float)(ld_dep(a.c.v + (slot0 + j) * (D / 2) + ch / 2) >> (ch & 1) * 4 & 15), z);
+                        for (int k = 0; k < 8; ++k) v[k] = v[k] * f1 * f2;
+                        const uint32_t p[4] = {half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])};
+                        sts16(q_at + (t * C::DB + e / 64) * kBlock + chunk_at(row, e / 8 % 8), p);
+                    }
+                    fence_async();
+                }
+                mbar_arrive(&sh.bars.q_full);
             }
-            add(k, v);
-        }
-        for (int u = t; u >= 0; u = tree_parent(a, b, u)) {
-            float k[D / 32], v[D / 32];
+            const int drafted = (w.n_k + kTile - 1) / kTile;   // the tile of the drafted tokens
+            if (!softmax_rows<D, false>(r, st.first[t], st.end[t], st.step, t, sh.bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
+                    const uint32_t n = tiles + (j - w.j0), s = n % kSeenRing;
+                    wait_warp(&sh.seen_full[s], n / kSeenRing & 1, a.err);
+                    if (j < drafted) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(sh.seen[s]);
+                        m[0] = v.x;
+                        m[1] = v.y;
+                        m[2] = v.z;
+                        m[3] = v.w;
+                        return (v.x & v.y & v.z & v.w) != kFull;
+                    }
+                    m[0] = m[1] = m[2] = m[3] = 0;
+                    if (valid) {
+                        const uint8_t *parent = sh.parents[works % kParentRing];
+                        if (!a.parent) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                k[i] = as_drafted(q_load1(a.k, b * a.k.ldb + u * a.k.ldt + h * a.k.ldh + lane + 32 * i));
-                v[i] = as_drafted(q_load1(a.v, b * a.v.ldb + u * a.v.ldt + h * a.v.ldh + lane + 32 * i));
+                            for (int e = 0; e < 4; ++e) {
+                                const int n = token + 1 - 32 * e;
+                                m[e] = n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u;
+                            }
+                        } else {
+                            for (int u = token; u >= 0; u = (int)parent[u] - 1) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (u >> 5 == e) m[e] |= 1u << (u & 31);
+                            }
+                        }
+                    }
+                    return true;
+                }))
+                break;
+            if (st.last > w.j0) {
+                tiles += st.last - w.j0;
+                ++works;
             }
-            add(k, v);
+            Sums sums;
+            if (!join_streams(r, st, t, sh.bars, sh.stat, c, sums, a.err)) break;
+            const bool mine = !(w.narrow && t == 1);   // whose rows these are
+            auto put = [&](int b, const float *o) {
+                const int64_t to = w.seq * a.out.ldb + token * a.out.ldt + (int64_t)head * a.out.ldh + 32 * b;
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = o[(e & ~7) + (e & 3) * 2 + (e >> 2 & 1)];
+                if (a.out.vec) {
+                    store32<BF16>(a.out.p + 2 * to, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) q_store1(a.out, to + e, v[e]);
+                }
+            };
+            float *rec = w.pieces > 1 ? plan.rec + (int64_t)(h * recs + w.rec) * rec_floats(D) : nullptr;
+            if (mine) {
+                const uint32_t o_at = tmem + (((uint32_t)row & ~31u) << 16) + 2 * kTile + t * D;
+                float *my = rec ? rec + w.p * rec_floats(D) + rt * kTile + row : nullptr;
+                const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+                if (my) {
+                    __stcg(my, r.m);
+                    __stcg(my + kPair, r.l);
+                }
+#pragma unroll 1
+                for (int b = 0; b < D / 32; ++b) {
+                    float o[32];
+                    load_sums<D>(o_at, b, sums, o);
+                    if (my) {
+                        if (sums.some && valid) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) __stcg(my + (2 + 32 * b + e) * kPair, o[e]);
+                        }
+                    } else if (there) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = valid ? o[e] * inv : 0.f;
+                        put(b, o);
+                    }
+                }
+            } else if (w.p == 0 && tok < a.per && w.tok0 + a.per + tok < a.n) {
+                // the pair's second row tile has no tokens: zeros
+                const int64_t to = w.seq * a.out.ldb + (token + a.per) * a.out.ldt + (int64_t)head * a.out.ldh;
+                for (int e = 0; e < D; ++e) q_store1(a.out, to + e, 0.f);
+            }
+            if (!leave_streams(r, st, t, sh.bars, a.err)) break;
+            if (rec) {
+                const int last = last_piece(sh.bars, plan.arrived + h * recs + w.rec, w.pieces, &sh.flag, r.n_rec++, a.err);
+                if (last < 0) break;
+                if (last && mine && there) {
+                    if (valid) {
+                        join_pieces<D>(rec, w.pieces, rt * kTile + row, c, put);
+                    } else {
+                        const float zero[32] = {};
+                        for (int b = 0; b < D / 32; ++b) put(b, zero);
+                    }
+                }
+            }
+        }
+    } else if (warp < 12) {
+        const int me = tid - 256, chunk = me % CH, row0 = me / CH;   // rows row0 + i STEP
+        constexpr int STEP = kMakers / CH;
+        // the loads' side, which runs ahead: the next work, and the place in the order of its tiles
+        int at = 0, place = 0, places = 0, entry = 0;
+        uint32_t f_tiles = 0, f_works = 0;
+        Work w{};
+        Streams st{};
+        auto load = [&](RawTile<CH> &x) {
+            while (place == places) {
+                if (places) {
+                    f_tiles += st.last - w.j0;
+                    ++f_works;
+                }
+                place = places = 0;
+                const int n = nth_work(at++);
+                if (n >= total) {
+                    x.entry = -1;
+                    --at;
+                    return;
+                }
+                w = load_work(plan.work + n / a.kv);
+                entry = n;
+                st = streams(w);
+                places = 2 * max(st.last - w.j0, 0);
+            }
+            // the place's tile, as tiles_in_order has them
+            const int n = places / 2, step = min(st.step, n);
+            int j;
+            bool value = true;
+            if (place < step) {
+                value = false;
+                j = place;
+            } else if (place < 2 * n - step) {
+                value = ((place - step) & 1) == 0;
+                j = (place - step) / 2 + (value ? 0 : step);
+            } else {
+                j = place - n;
+            }
+            ++place;
+            const uint32_t tile = f_tiles + j;
+            j += w.j0;
+            const bool drafted = j == (w.n_k + kTile - 1) / kTile;
+            x.entry = entry;
+            x.what = (value ? 1u : 0u) | (drafted ? 2u : 0u) | tile % kSeenRing << 2 | (tile / kSeenRing & 1) << 5 | f_works % kParentRing << 6;
+            if (drafted) return;
+            const int64_t slot0 = a.c.slot0(w.seq, entry % a.kv) + (int64_t)j * kTile;
+            const int left = w.n_k - j * kTile;
+            const uint8_t *codes = value ? a.c.v : a.c.k;
+            const uint32_t *scales = value ? a.c.vs : a.c.ks;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int r = row0 + i * STEP;
+                x.code[i] = make_uint4(0, 0, 0, 0);
+                x.scale[i] = 0;
+                if (r < left) {
+                    x.code[i] = load_codes(codes + (slot0 + r) * (D / 2) + chunk * 16);
+                    x.scale[i] = ld_dep(scales + (slot0 + r) * GR + chunk / 2);
+                }
+            }
+            if (!value) x.pos = me < left ? (a.c.pos ? ld_dep(a.c.pos + slot0 + me) : 0) : -1;
+        };
+
+        uint32_t it = 0;
+        auto make = [&](RawTile<CH> &x) {
+            if (x.entry < 0) return false;
+            const uint32_t stage = it % kTreeStages, slot = x.what >> 2 & 7;
+            const bool value = x.what & 1;
+            static_assert(kSeenRing == 8 && kParentRing == 4, "as they are packed");
+            if (it >= kTreeStages && !wait_warp(&sh.bars.empty[stage], (it / kTreeStages - 1) & 1, a.err)) return false;
+            ++it;
+            const uint32_t to = ring + (stage * C::DB + chunk / 2) * kBlock;
+            const int c0 = (chunk & 1) * 4;
+            if (x.what & 2) {
+                const QRowsK &rows = value ? a.v : a.k;
+                const Work d = load_work(plan.work + x.entry / a.kv);
+                const int64_t src = d.seq * rows.ldb + (x.entry % a.kv) * rows.ldh + chunk * 32;
+                if (!value) {
+                    if (a.parent && me < d.k0) {
+                        int p = ld_dep(a.parent + (int64_t)d.seq * a.n + me);
+                        if (p < -1 || p >= me) {
+                            atomicOr(a.err, CS_DEVERR_INDEX);
+                            p = -1;
+                        }
+                        sh.parents[x.what >> 6][me] = (uint8_t)(p + 1);
+                    }
+                    mbar_arrive(&sh.seen_full[slot]);
+                }
+#pragma unroll 1
+                for (int i = 0; i < CH; ++i) {
+                    const int r = row0 + i * STEP;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float v[8] = {};
+                        if (r < d.k0) load8(rows, src + r * rows.ldt + k * 8, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = as_drafted(v[e]);
+                        const uint32_t p[4] = {half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])};
+                        sts16(to + chunk_at(r, c0 + k), p);
+                    }
+                }
+            } else {
+                if (!value) {
+                    const uint32_t there = __ballot_sync(kFull, x.pos >= 0);
+                    if (lane == 0) sh.seen[slot][warp & 3] = there;
+                    mbar_arrive(&sh.seen_full[slot]);
+                } else if (!wait_warp(&sh.seen_full[slot], x.what >> 5 & 1, a.err)) {
+                    return false;
+                }
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int r = row0 + i * STEP;
+                    uint32_t sz = x.scale[i];
+                    // a slot that is not there may hold anything: its value counts with 0, and its key's scores are not looked at
+                    if (value && !(sh.seen[slot][r >> 5] >> (r & 31) & 1u)) sz = 0;
+                    const __half2 h = u2h(sz), s = __low2half2(h), z = __high2half2(h);
+                    // the words of a chunk in an order that keeps 8 lanes' stores in different banks
+                    const uint4 cw = x.code[i];
+                    const bool swap = D == 128 && (chunk & 2);
+                    const uint32_t word[4] = {swap ? cw.z : cw.x, swap ? cw.w : cw.y, swap ? cw.x : cw.z, swap ? cw.y : cw.w};
+                    float sf, zf;
+                    half2x(sz, sf, zf);
+                    const bool beyond = fmaf(15.f, sf, zf) > 65504.f;   // a group that spans nearly all of fp16's range
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[4];
+                        decode8(word[k], s, z, v);
+                        if (beyond) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = h2u(__hmin2(u2h(v[e]), __float2half2_rn(65504.f)));
+                        }
+                        sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v);
+                    }
+                }
+            }
+            fence_async();
+            mbar_arrive(&sh.bars.full[stage]);
+            load(x);
+            return true;
+        };
+        RawTile<CH> raw[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) load(raw[i]);
+        while (make(raw[0]) && make(raw[1]) && make(raw[2])) {}
+    } else {
+        if (warp == 12) {
+            MmaState ms;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const int x = nth_work(i);
+                if (x >= total) break;
+                Work w = load_work(plan.work + x / a.kv);
+                w.toks = uniform(w.toks);
+                w.j0 = uniform(w.j0);
+                w.j1 = uniform(w.j1);
+                w.narrow = uniform(w.narrow);
+                ok = issue_work<D, false, kTreeStages>(streams(w), sh.bars, tmem, q_at, ring, ms, a.err);
+            }
+            if (!ok) {
+                mma_commit(&sh.bars.drain);
+                mbar_wait(&sh.bars.drain, 0, kWaitNs);
+            }
         }
     }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        q_store1(a.out, b * a.out.ldb + t * a.out.ldt + head * a.out.ldh + lane + 32 * i, l == 0.f ? 0.f : o[i] / l);
+    tc_before();
+    __syncthreads();
+    if (warp == 12) tm_free(tmem);
+}
+
+// ------------------------------------------------------------------- host side
+
+bool tree_sizes(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n) {
+    return batch >= 1 && batch <= kQMaxBatch && kv_heads >= 1 && kv_heads <= kMaxHeads && capacity >= 1 && capacity <= kMaxCapacity &&
+           (d_head == 64 || d_head == 128) && n_heads >= kv_heads && n_heads % kv_heads == 0 && n >= 1 && n <= kMaxTree &&
+           n_heads / kv_heads <= kTile && (int64_t)n_heads / kv_heads * n <= kQMaxRows;
+}
+
+// The list's place behind the control words; returns the bytes.
+size_t tree_scratch(int batch, int capacity, int d, int group, int n, int sms, char *at, Plan *plan) {
+    const int pair = 2 * (kTile / group), recs = capacity > (kLeastPiece - 1) * kTile ? 2 * sms : 0;
+    return plan_scratch((size_t)batch * ((n + pair - 1) / pair), recs, d, at, plan);
+}
+
+template <int D, bool BF16>
+cudaError_t run_tree(const TreeK &a, const Plan &plan, cudaStream_t s) {
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&tree_kernel<D, BF16>));
+    if (e == cudaSuccess) e = launch(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, pdl_enabled(), a, plan);
+    if (e != cudaSuccess) return e;
+    const int64_t most = ((int64_t)a.c.batch * ((a.n + 2 * a.per - 1) / (2 * a.per)) + plan.recs) * a.kv;
+    return launch(tree_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kTreeThreads), TreeCfg<D>::smem, s,
+                  pdl_enabled(), a, plan);
 }
 
 }  // namespace
@@ -103,11 +500,8 @@ using namespace cs;
 extern "C" {
 
 size_t cs_qcache_tree_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n) {
-    if (batch < 1 || batch > kQMaxBatch || kv_heads < 1 || kv_heads > kMaxHeads || capacity < 1 || capacity > kMaxCapacity ||
-        (d_head != 64 && d_head != 128) || n_heads < kv_heads || n_heads % kv_heads || n < 1 || n > kMaxTree ||
-        (int64_t)n_heads / kv_heads * n > kQMaxRows)
-        return 0;
-    return kControlBytes;
+    if (!tree_sizes(batch, kv_heads, capacity, d_head, n_heads, n)) return 0;
+    return kControlBytes + tree_scratch(batch, capacity, d_head, n_heads / kv_heads, n, device_sm_count(), nullptr, nullptr);
 }
 
 cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q, const cs_head_rows *k,
@@ -131,30 +525,33 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
         set_error("%s: takes fp16 and bf16, and d_head 64 or 128 (%d)", who, cache->d_head);
         return CS_ERR_UNSUPPORTED;
     }
-    if (n > kMaxTree || (int64_t)n_heads / cache->n_heads * n > kQMaxRows) {
-        set_error("%s: n=%d above %d, or %lld query rows per cache head above %d", who, n, kMaxTree,
-                  (long long)n_heads / cache->n_heads * n, kQMaxRows);
+    if (!tree_sizes(cache->batch, cache->n_heads, cache->capacity, cache->d_head, n_heads, n)) {
+        set_error("%s: n=%d above %d, n_heads / the cache's above %d (%d), or %lld query rows per cache head above %d", who, n, kMaxTree,
+                  kTile, n_heads / cache->n_heads, (long long)n_heads / cache->n_heads * n, kQMaxRows);
         return CS_ERR_UNSUPPORTED;
     }
     CS_CHECK(length && aligned(length, 4), "%s: length is null or misaligned", who);
     CS_CHECK(aligned(parent, 4) && aligned(n_new, 4), "%s: parent and n_new must be 4-byte aligned", who);
     CS_CHECK(scale == scale && scale - scale == 0.f, "%s: scale must be finite", who);
-    st = check_qws(ws, ws_bytes,
-                   cs_qcache_tree_workspace_size(cache->batch, cache->n_heads, cache->capacity, cache->d_head, n_heads, n), who);
-    if (st != CS_OK) return st;
     a.heads = n_heads;
     a.group = n_heads / cache->n_heads;
+    a.sms = device_sm_count();
+    Plan plan;
+    const size_t need = kControlBytes + tree_scratch(a.c.batch, a.c.cap, a.c.d, a.group, n, a.sms, static_cast<char *>(ws) + kControlBytes, &plan);
+    st = check_qws(ws, ws_bytes, need, who);
+    if (st != CS_OK) return st;
     a.n = n;
+    a.per = kTile / a.group;
+    a.kv = a.c.heads;
     a.length = length;
     a.parent = parent;
     a.n_new = n_new;
     a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)cache->d_head);
     a.err = static_cast<uint32_t *>(ws);
-    const int64_t rows = (int64_t)a.c.batch * n * n_heads;
-    auto go = [&](auto kernel) {
-        return launch(kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, (cudaStream_t)stream, pdl_enabled(), a);
-    };
-    const cudaError_t e = a.c.d == 64 ? go(tree_kernel<64>) : go(tree_kernel<128>);
+    auto go = [&](auto run) { return run(a, plan, (cudaStream_t)stream); };
+    const bool h = q->dtype == CS_F16;
+    const cudaError_t e = a.c.d == 64 ? (h ? go(run_tree<64, false>) : go(run_tree<64, true>))
+                                      : (h ? go(run_tree<128, false>) : go(run_tree<128, true>));
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
