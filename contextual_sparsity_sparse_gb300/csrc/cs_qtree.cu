@@ -1,8 +1,9 @@
 // Attention for a tree of drafted tokens over the 4-bit KV cache.
 //
-// The streams of cs_attn_tc.cuh over key tiles that a warpgroup makes from the
-// codes: a tile's 128 slots become fp16 values, offset + scale * code with one
-// rounding, in the layout that the products take.  The tile behind the last slot
+// The streams of cs_attn_tc.cuh over tiles that six warps make from the codes: a
+// tile's 128 slots become fp16 values, offset + scale * code with one rounding,
+// in the layout that the products take.  A seventh warp copies codes, scales
+// and positions into a ring ahead of them.  The tile behind the last slot
 // holds the drafted tokens themselves, and there a row sees its own ancestors.
 // Codes come as 8 nibbles to a word, of which an AND and an OR make two fp16
 // numbers 1024 + n with n four channels apart: within 8 channels, the products
@@ -20,9 +21,10 @@ namespace cs {
 namespace {
 
 constexpr int kMaxTree = 128;         // drafted tokens of a sequence: one key tile
-constexpr int kTreeThreads = 512;     // two warpgroups of rows, one that makes tiles, one of which a warp issues the products
-constexpr int kMakers = 128;
-constexpr int kTreeStages = 5;
+constexpr int kTreeThreads = 512;     // two warpgroups of rows, kMakers warps that make tiles, one that loads codes, one for the products
+constexpr int kMakers = 6, kLoader = 14, kIssuer = 15;
+constexpr int kTreeStages = 4;
+constexpr int kRaw = 3;               // tiles of codes under way
 constexpr int kSeenRing = 8;          // tiles by which the makers can be ahead of the rows, and more
 constexpr int kParentRing = 4;        // works likewise
 
@@ -68,12 +70,16 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreeK a, Plan p
 template <int D>
 struct TreeCfg {
     static constexpr int DB = D / 64;
-    static constexpr size_t smem = (size_t)(2 + kTreeStages) * DB * kBlock + 1024;
+    static constexpr int CH = D / 32;                 // 16-byte chunks of a slot's codes
+    static constexpr int ROWS = 32 / CH;              // slots of a unit: a warp's chunks
+    static constexpr int UNITS = kTile / ROWS;        // of a tile
+    static constexpr int CODES = kTile * D / 2, SCALES = kTile * 4 * DB, RAW = CODES + SCALES + 4 * kTile;
+    static constexpr size_t smem = (size_t)(2 + kTreeStages) * DB * kBlock + kRaw * RAW + 1024;
 };
 
 struct TreeShared {
     Bars<kTreeStages> bars;
-    uint64_t seen_full[kSeenRing];
+    uint64_t seen_full[kSeenRing], raw_full[kRaw], raw_empty[kRaw];
     alignas(16) uint32_t seen[kSeenRing][4];    // of a tile of slots, those that are there
     uint8_t parents[kParentRing][kMaxTree];     // parent + 1 of every drafted token of a work's sequence
     float2 stat[kTile];
@@ -117,36 +123,28 @@ __device__ __forceinline__ void load8(const QRowsK &r, int64_t i, float (&x)[8])
     }
 }
 
-// Codes are read once by a CTA; an append before this kernel may have written them.
-__device__ __forceinline__ uint4 load_codes(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
-    return r;
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
-
-// A tile's codes on their way: this thread's chunk of 32 channels of CH slots.
-template <int CH>
-struct RawTile {
-    uint4 code[CH];
-    uint32_t scale[CH];
-    int pos;              // of slot threadIdx % 128 (key tiles)
-    int entry;            // its work's place in the list, times the heads, plus the head; -1: no more tiles
-    uint32_t what;        // bit 0: values, 1: the drafted tokens, 2 ..: the key tile's place in the ring of `seen`, 5: that
-                          // place's parity, 6 ..: the work's place in the ring of parents
-};
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan plan) {
     using C = TreeCfg<D>;
-    constexpr int CH = D / 32, GR = D / kQGroup;
+    constexpr int CH = C::CH;
     extern __shared__ uint8_t dsm[];
     __shared__ TreeShared sh;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const uint32_t q_at = (smem_addr(dsm) + 1023u) & ~1023u, ring = q_at + 2 * C::DB * kBlock;
-    if (warp == 12) tm_alloc(&sh.tmem);
-    if (tid == 416) {
-        init_bars(sh.bars, kPair, kMakers);
-        for (int i = 0; i < kSeenRing; ++i) mbar_init(&sh.seen_full[i], kMakers);
+    const uint32_t raw = ring + kTreeStages * C::DB * kBlock;
+    if (warp == kIssuer) tm_alloc(&sh.tmem);
+    if (tid == 32 * kLoader) {
+        init_bars(sh.bars, kPair, C::UNITS);
+        for (int i = 0; i < kSeenRing; ++i) mbar_init(&sh.seen_full[i], C::UNITS);
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&sh.raw_full[i], 33);
+            mbar_init(&sh.raw_empty[i], C::UNITS);
+        }
         mbar_fence_init();
     }
     tc_before();
@@ -298,173 +296,174 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 }
             }
         }
-    } else if (warp < 12) {
-        const int me = tid - 256, chunk = me % CH, row0 = me / CH;   // rows row0 + i STEP
-        constexpr int STEP = kMakers / CH;
-        // the loads' side, which runs ahead: the next work, and the place in the order of its tiles
-        int at = 0, place = 0, places = 0, entry = 0;
-        uint32_t f_tiles = 0, f_works = 0;
-        Work w{};
-        Streams st{};
-        auto load = [&](RawTile<CH> &x) {
-            while (place == places) {
-                if (places) {
-                    f_tiles += st.last - w.j0;
-                    ++f_works;
-                }
-                place = places = 0;
-                const int n = nth_work(at++);
-                if (n >= total) {
-                    x.entry = -1;
-                    --at;
-                    return;
-                }
-                w = load_work(plan.work + n / a.kv);
-                entry = n;
-                st = streams(w);
-                places = 2 * max(st.last - w.j0, 0);
-            }
-            // the place's tile, as tiles_in_order has them
-            const int n = places / 2, step = min(st.step, n);
-            int j;
-            bool value = true;
-            if (place < step) {
-                value = false;
-                j = place;
-            } else if (place < 2 * n - step) {
-                value = ((place - step) & 1) == 0;
-                j = (place - step) / 2 + (value ? 0 : step);
-            } else {
-                j = place - n;
-            }
-            ++place;
-            const uint32_t tile = f_tiles + j;
-            j += w.j0;
-            const bool drafted = j == (w.n_k + kTile - 1) / kTile;
-            x.entry = entry;
-            x.what = (value ? 1u : 0u) | (drafted ? 2u : 0u) | tile % kSeenRing << 2 | (tile / kSeenRing & 1) << 5 | f_works % kParentRing << 6;
-            if (drafted) return;
-            const int64_t slot0 = a.c.slot0(w.seq, entry % a.kv) + (int64_t)j * kTile;
-            const int left = w.n_k - j * kTile;
-            const uint8_t *codes = value ? a.c.v : a.c.k;
-            const uint32_t *scales = value ? a.c.vs : a.c.ks;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int r = row0 + i * STEP;
-                x.code[i] = make_uint4(0, 0, 0, 0);
-                x.scale[i] = 0;
-                if (r < left) {
-                    x.code[i] = load_codes(codes + (slot0 + r) * (D / 2) + chunk * 16);
-                    x.scale[i] = ld_dep(scales + (slot0 + r) * GR + chunk / 2);
-                }
-            }
-            if (!value) x.pos = me < left ? (a.c.pos ? ld_dep(a.c.pos + slot0 + me) : 0) : -1;
-        };
-
-        uint32_t it = 0;
-        auto make = [&](RawTile<CH> &x) {
-            if (x.entry < 0) return false;
-            const uint32_t stage = it % kTreeStages, slot = x.what >> 2 & 7;
-            const bool value = x.what & 1;
-            static_assert(kSeenRing == 8 && kParentRing == 4, "as they are packed");
-            if (it >= kTreeStages && !wait_warp(&sh.bars.empty[stage], (it / kTreeStages - 1) & 1, a.err)) return false;
-            ++it;
-            const uint32_t to = ring + (stage * C::DB + chunk / 2) * kBlock;
-            const int c0 = (chunk & 1) * 4;
-            if (x.what & 2) {
-                const QRowsK &rows = value ? a.v : a.k;
-                const Work d = load_work(plan.work + x.entry / a.kv);
-                const int64_t src = d.seq * rows.ldb + (x.entry % a.kv) * rows.ldh + chunk * 32;
-                if (!value) {
-                    if (a.parent && me < d.k0) {
-                        int p = ld_dep(a.parent + (int64_t)d.seq * a.n + me);
-                        if (p < -1 || p >= me) {
-                            atomicOr(a.err, CS_DEVERR_INDEX);
-                            p = -1;
+    } else if (warp < 8 + kMakers) {
+        const int chunk = lane % CH, in_unit = lane / CH, c0 = (chunk & 1) * 4;
+        uint32_t it = 0, cached = 0, tiles = 0, works = 0, units = warp - 8;   // units: until this warp's next one
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int x = nth_work(i);
+            if (x >= total) break;
+            const Work w = load_work(plan.work + x / a.kv);
+            const int h = x % a.kv, drafted = (w.n_k + kTile - 1) / kTile;
+            const Streams st = streams(w);
+            if (st.last <= w.j0) continue;
+            ok = tiles_in_order(st, [&](bool value, int j) {
+                const uint32_t stage = it % kTreeStages, tile = tiles + (j - w.j0), slot = tile % kSeenRing;
+                if (it >= kTreeStages && !wait_warp(&sh.bars.empty[stage], (it / kTreeStages - 1) & 1, a.err)) return false;
+                ++it;
+                const uint32_t to = ring + (stage * C::DB + chunk / 2) * kBlock;
+                if (j == drafted) {
+                    const QRowsK &rows = value ? a.v : a.k;
+                    const int64_t src = w.seq * rows.ldb + h * rows.ldh + chunk * 32;
+                    for (; units < C::UNITS; units += kMakers) {
+                        if (!value && units == 0 && a.parent) {
+                            for (int t = lane; t < w.k0; t += 32) {
+                                int p = ld_dep(a.parent + (int64_t)w.seq * a.n + t);
+                                if (p < -1 || p >= t) {
+                                    atomicOr(a.err, CS_DEVERR_INDEX);
+                                    p = -1;
+                                }
+                                sh.parents[works % kParentRing][t] = (uint8_t)(p + 1);
+                            }
                         }
-                        sh.parents[x.what >> 6][me] = (uint8_t)(p + 1);
+                        const int r = units * C::ROWS + in_unit;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float v[8] = {};
+                            if (r < w.k0) load8(rows, src + r * rows.ldt + k * 8, v);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = as_drafted(v[e]);
+                            const uint32_t p[4] = {half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])};
+                            sts16(to + chunk_at(r, c0 + k), p);
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (!value) mbar_arrive(&sh.seen_full[slot]);
+                            mbar_arrive(&sh.bars.full[stage]);
+                        }
                     }
-                    mbar_arrive(&sh.seen_full[slot]);
-                }
-#pragma unroll 1
-                for (int i = 0; i < CH; ++i) {
-                    const int r = row0 + i * STEP;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float v[8] = {};
-                        if (r < d.k0) load8(rows, src + r * rows.ldt + k * 8, v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = as_drafted(v[e]);
-                        const uint32_t p[4] = {half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])};
-                        sts16(to + chunk_at(r, c0 + k), p);
-                    }
-                }
-            } else {
-                if (!value) {
-                    const uint32_t there = __ballot_sync(kFull, x.pos >= 0);
-                    if (lane == 0) sh.seen[slot][warp & 3] = there;
-                    mbar_arrive(&sh.seen_full[slot]);
-                } else if (!wait_warp(&sh.seen_full[slot], x.what >> 5 & 1, a.err)) {
-                    return false;
-                }
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int r = row0 + i * STEP;
-                    uint32_t sz = x.scale[i];
-                    // a slot that is not there may hold anything: its value counts with 0, and its key's scores are not looked at
-                    if (value && !(sh.seen[slot][r >> 5] >> (r & 31) & 1u)) sz = 0;
-                    const __half2 h = u2h(sz), s = __low2half2(h), z = __high2half2(h);
+                } else {
+                    const uint32_t from = cached % kRaw, codes = raw + from * C::RAW;
+                    if (!wait_warp(&sh.raw_full[from], cached / kRaw & 1, a.err)) return false;
+                    ++cached;
+                    const int left = w.n_k - j * kTile;
                     // the words of a chunk in an order that keeps 8 lanes' stores in different banks
-                    const uint4 cw = x.code[i];
                     const bool swap = D == 128 && (chunk & 2);
-                    const uint32_t word[4] = {swap ? cw.z : cw.x, swap ? cw.w : cw.y, swap ? cw.x : cw.z, swap ? cw.y : cw.w};
-                    float sf, zf;
-                    half2x(sz, sf, zf);
-                    const bool beyond = fmaf(15.f, sf, zf) > 65504.f;   // a group that spans nearly all of fp16's range
+                    for (; units < C::UNITS; units += kMakers) {
+                        const int r = units * C::ROWS + in_unit;
+                        uint4 cw;
+                        uint32_t sz;
+                        int pos;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(cw.x), "=r"(cw.y), "=r"(cw.z), "=r"(cw.w)
+                                     : "r"(codes + r * (D / 2) + chunk * 16));
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sz) : "r"(codes + C::CODES + (r * C::DB + chunk / 2) * 4));
+                        asm volatile("ld.shared.s32 %0, [%1];" : "=r"(pos) : "r"(codes + C::CODES + C::SCALES + r * 4));
+                        const bool there = r < left && (!a.c.pos || pos >= 0);
+                        if (!value) {
+                            uint32_t bits = __ballot_sync(kFull, there && chunk == 0);   // every CH-th
+                            if (lane == 0) {
+                                uint32_t v = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t v[4];
-                        decode8(word[k], s, z, v);
-                        if (beyond) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = h2u(__hmin2(u2h(v[e]), __float2half2_rn(65504.f)));
+                                for (int e = 0; e < C::ROWS; ++e) v |= (bits >> e * CH & 1u) << e;
+                                if (C::ROWS == 8) reinterpret_cast<uint8_t *>(sh.seen[slot])[units] = (uint8_t)v;
+                                else reinterpret_cast<uint16_t *>(sh.seen[slot])[units] = (uint16_t)v;
+                            }
+                        } else if (!there) {
+                            sz = 0;   // it may hold anything: its value counts with 0 (and its key's scores are not looked at)
                         }
-                        sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v);
+                        const __half2 hz = u2h(sz), s = __low2half2(hz), z = __high2half2(hz);
+                        const uint32_t word[4] = {swap ? cw.z : cw.x, swap ? cw.w : cw.y, swap ? cw.x : cw.z, swap ? cw.y : cw.w};
+                        float sf, zf;
+                        half2x(sz, sf, zf);
+                        const bool beyond = fmaf(15.f, sf, zf) > 65504.f;   // a group that spans nearly all of fp16's range
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t v[4];
+                            decode8(word[k], s, z, v);
+                            if (beyond) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[e] = h2u(__hmin2(u2h(v[e]), __float2half2_rn(65504.f)));
+                            }
+                            sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v);
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (!value) mbar_arrive(&sh.seen_full[slot]);
+                            mbar_arrive(&sh.raw_empty[from]);
+                            mbar_arrive(&sh.bars.full[stage]);
+                        }
                     }
                 }
-            }
-            fence_async();
-            mbar_arrive(&sh.bars.full[stage]);
-            load(x);
-            return true;
-        };
-        RawTile<CH> raw[3];
+                units -= C::UNITS;
+                return true;
+            });
+            tiles += st.last - w.j0;
+            ++works;
+        }
+    } else if (warp == kLoader) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int x = nth_work(i);
+            if (x >= total) break;
+            const Work w = load_work(plan.work + x / a.kv);
+            const int h = x % a.kv, drafted = (w.n_k + kTile - 1) / kTile;
+            const Streams st = streams(w);
+            if (st.last <= w.j0) continue;
+            ok = tiles_in_order(st, [&](bool value, int j) {
+                if (j == drafted) return true;
+                const uint32_t to = it % kRaw, codes = raw + to * C::RAW, bytes = min(kTile, w.n_k - j * kTile) * (D / 2);
+                if (it >= kRaw && !wait_warp(&sh.raw_empty[to], (it / kRaw - 1) & 1, a.err)) return false;
+                ++it;
+                const int64_t slot0 = a.c.slot0(w.seq, h) + (int64_t)j * kTile;
+                const int left = w.n_k - j * kTile;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.raw_full[to], bytes);
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(codes),
+                                 "l"((value ? a.c.v : a.c.k) + slot0 * (D / 2)), "r"(bytes), "r"(smem_addr(&sh.raw_full[to]))
+                                 : "memory");
+                }
+                const uint32_t *scales = (value ? a.c.vs : a.c.ks) + slot0 * C::DB;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) load(raw[i]);
-        while (make(raw[0]) && make(raw[1]) && make(raw[2])) {}
+                for (int e = 0; e < kTile; e += 32) {
+                    const int r = e + lane;
+                    if (r >= left) break;
+                    copy_async<4 * C::DB>(codes + C::CODES + r * 4 * C::DB, scales + r * C::DB);
+                    if (a.c.pos) copy_async<4>(codes + C::CODES + C::SCALES + r * 4, a.c.pos + slot0 + r);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.raw_full[to])) : "memory");
+                return true;
+            });
+        }
+        if (!ok) {
+            // what is under way lands before the memory is given back
+            cp_async_commit();
+            cp_async_wait<0>();
+            for (uint32_t n = it > kRaw ? it - kRaw : 0; n < it; ++n) mbar_wait(&sh.raw_full[n % kRaw], n / kRaw & 1, kWaitNs);
+        }
     } else {
-        if (warp == 12) {
-            MmaState ms;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                const int x = nth_work(i);
-                if (x >= total) break;
-                Work w = load_work(plan.work + x / a.kv);
-                w.toks = uniform(w.toks);
-                w.j0 = uniform(w.j0);
-                w.j1 = uniform(w.j1);
-                w.narrow = uniform(w.narrow);
-                ok = issue_work<D, false, kTreeStages>(streams(w), sh.bars, tmem, q_at, ring, ms, a.err);
-            }
-            if (!ok) {
-                mma_commit(&sh.bars.drain);
-                mbar_wait(&sh.bars.drain, 0, kWaitNs);
-            }
+        MmaState ms;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int x = nth_work(i);
+            if (x >= total) break;
+            Work w = load_work(plan.work + x / a.kv);
+            w.toks = uniform(w.toks);
+            w.j0 = uniform(w.j0);
+            w.j1 = uniform(w.j1);
+            w.narrow = uniform(w.narrow);
+            ok = issue_work<D, false, kTreeStages>(streams(w), sh.bars, tmem, q_at, ring, ms, a.err);
+        }
+        if (!ok) {
+            mma_commit(&sh.bars.drain);
+            mbar_wait(&sh.bars.drain, 0, kWaitNs);
         }
     }
     tc_before();
     __syncthreads();
-    if (warp == 12) tm_free(tmem);
+    if (warp == kIssuer) tm_free(tmem);
 }
 
 // ------------------------------------------------------------------- host side
