@@ -395,14 +395,14 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
     };
     if (!wait_warp(&b.q_full, st.n_q & 1, err)) return false;
     ++st.n_q;
+    // The streams in turn, t known at compile time: the product with the value tile that lies a step back, then scores of
+    // key tile j.
     uint32_t vs = 0, ks = 0;
-    // the streams in turn: scores of key tile j, behind the product with the value tile that lies a step back
-    const int turns = narrow ? w.last - first + 2 : 2 * (w.last - first + 1);
-#pragma unroll 1
-    for (int i = 0; i < turns; ++i) {
-        const int t = i & 1, j = first + (narrow ? i : i >> 1), jv = j - w.step, end = t ? w.end[1] : w.end[0];
+    auto turn = [&](auto stream, int j) {
+        constexpr int t = decltype(stream)::value;
+        const int jv = j - w.step, end = w.end[t];
         if (narrow || t == 0) {
-            if (jv >= first) {
+            if (jv >= first && jv < w.last) {
                 if (!next()) return false;
                 vs = stage;
             }
@@ -412,17 +412,21 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
             }
         }
         if (jv >= first && jv < end) {
-            if (!values(t, vs, jv == (narrow ? first + t : first), jv + w.step >= end)) return false;
+            if (!values(t, vs, jv == w.first[t], jv + w.step >= end)) return false;
         } else {
             tc_after();
         }
         if (j < end) scores(t, ks);
         if (narrow || t == 1) {
-            if (jv >= first) mma_commit(&b.empty[vs]);
+            if (jv >= first && jv < w.last) mma_commit(&b.empty[vs]);
             if (j < w.last) mma_commit(&b.empty[ks]);
             if (j == w.last - 1) mma_commit(&b.q_empty);
         }
-    }
+        return true;
+    };
+#pragma unroll 1
+    for (int j = first; j < w.last + w.step; j += w.step)
+        if (!turn(std::integral_constant<int, 0>(), j) || !turn(std::integral_constant<int, 1>(), narrow ? j + 1 : j)) return false;
     return true;
 }
 

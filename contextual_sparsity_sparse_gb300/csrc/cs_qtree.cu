@@ -139,11 +139,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
     const uint32_t raw = ring + kTreeStages * C::DB * kBlock;
     if (warp == kIssuer) tm_alloc(&sh.tmem);
     if (tid == 32 * kLoader) {
-        init_bars(sh.bars, kPair, C::UNITS);
-        for (int i = 0; i < kSeenRing; ++i) mbar_init(&sh.seen_full[i], C::UNITS);
+        init_bars(sh.bars, kPair, kMakers);
+        for (int i = 0; i < kSeenRing; ++i) mbar_init(&sh.seen_full[i], kMakers);
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(&sh.raw_full[i], 33);
-            mbar_init(&sh.raw_empty[i], C::UNITS);
+            mbar_init(&sh.raw_empty[i], kMakers);
         }
         mbar_fence_init();
     }
@@ -336,12 +336,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                             const uint32_t p[4] = {half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])};
                             sts16(to + chunk_at(r, c0 + k), p);
                         }
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (!value) mbar_arrive(&sh.seen_full[slot]);
-                            mbar_arrive(&sh.bars.full[stage]);
-                        }
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (!value) mbar_arrive(&sh.seen_full[slot]);
+                        mbar_arrive(&sh.bars.full[stage]);
                     }
                 } else {
                     const uint32_t from = cached % kRaw, codes = raw + from * C::RAW;
@@ -350,50 +350,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                     const int left = w.n_k - j * kTile;
                     // the words of a chunk in an order that keeps 8 lanes' stores in different banks
                     const bool swap = D == 128 && (chunk & 2);
+#pragma unroll 1
                     for (; units < C::UNITS; units += kMakers) {
-                        const int r = units * C::ROWS + in_unit;
+                        const int r = units * C::ROWS + in_unit, mine = units * C::ROWS + (lane & (C::ROWS - 1));
                         uint4 cw;
                         uint32_t sz;
-                        int pos;
+                        int pos = 0;
+                        if (a.c.pos) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(pos) : "r"(codes + C::CODES + C::SCALES + mine * 4));
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sz) : "r"(codes + C::CODES + (r * C::DB + chunk / 2) * 4));
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(cw.x), "=r"(cw.y), "=r"(cw.z), "=r"(cw.w)
                                      : "r"(codes + r * (D / 2) + chunk * 16));
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sz) : "r"(codes + C::CODES + (r * C::DB + chunk / 2) * 4));
-                        asm volatile("ld.shared.s32 %0, [%1];" : "=r"(pos) : "r"(codes + C::CODES + C::SCALES + r * 4));
-                        const bool there = r < left && (!a.c.pos || pos >= 0);
+                        const uint32_t bits = __ballot_sync(kFull, pos >= 0 && mine < left);
                         if (!value) {
-                            uint32_t bits = __ballot_sync(kFull, there && chunk == 0);   // every CH-th
-                            if (lane == 0) {
-                                uint32_t v = 0;
-#pragma unroll
-                                for (int e = 0; e < C::ROWS; ++e) v |= (bits >> e * CH & 1u) << e;
-                                if (C::ROWS == 8) reinterpret_cast<uint8_t *>(sh.seen[slot])[units] = (uint8_t)v;
-                                else reinterpret_cast<uint16_t *>(sh.seen[slot])[units] = (uint16_t)v;
-                            }
-                        } else if (!there) {
+                            if (C::ROWS == 8 && lane == 0) reinterpret_cast<uint8_t *>(sh.seen[slot])[units] = (uint8_t)bits;
+                            if (C::ROWS == 16 && lane == 0) reinterpret_cast<uint16_t *>(sh.seen[slot])[units] = (uint16_t)bits;
+                        } else if (!(bits >> in_unit & 1u)) {
                             sz = 0;   // it may hold anything: its value counts with 0 (and its key's scores are not looked at)
                         }
                         const __half2 hz = u2h(sz), s = __low2half2(hz), z = __high2half2(hz);
                         const uint32_t word[4] = {swap ? cw.z : cw.x, swap ? cw.w : cw.y, swap ? cw.x : cw.z, swap ? cw.y : cw.w};
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) decode8(word[k], s, z, v[k]);
                         float sf, zf;
                         half2x(sz, sf, zf);
-                        const bool beyond = fmaf(15.f, sf, zf) > 65504.f;   // a group that spans nearly all of fp16's range
+                        if (fmaf(15.f, sf, zf) > 65504.f) {   // a group that spans nearly all of fp16's range
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t v[4];
-                            decode8(word[k], s, z, v);
-                            if (beyond) {
+                            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) v[e] = h2u(__hmin2(u2h(v[e]), __float2half2_rn(65504.f)));
-                            }
-                            sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v);
+                                for (int e = 0; e < 4; ++e) v[k][e] = h2u(__hmin2(u2h(v[k][e]), __float2half2_rn(65504.f)));
                         }
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (!value) mbar_arrive(&sh.seen_full[slot]);
-                            mbar_arrive(&sh.raw_empty[from]);
-                            mbar_arrive(&sh.bars.full[stage]);
-                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v[k]);
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (!value) mbar_arrive(&sh.seen_full[slot]);
+                        mbar_arrive(&sh.raw_empty[from]);
+                        mbar_arrive(&sh.bars.full[stage]);
                     }
                 }
                 units -= C::UNITS;
