@@ -111,6 +111,34 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *r) {
                  "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
                  : "memory");
 }
+__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t)
+                 : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t t, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(t));
+}
+// N fp32 columns, or N / 2 of pairs.
+template <int N>
+__device__ __forceinline__ void tm_ld(uint32_t t, float *v) {
+    if (N == 32) tm_ld32(t, v);
+    else tm_ld16(t, v);
+}
+template <int N>
+__device__ __forceinline__ void tm_st(uint32_t t, const float *v) {
+    if (N == 32) tm_st32(t, v);
+    else tm_st16(t, reinterpret_cast<const uint32_t *>(v));
+}
+template <int N>
+__device__ __forceinline__ void tm_st_pairs(uint32_t t, const uint32_t *v) {
+    if (N == 32) tm_st16(t, v);
+    else tm_st8(t, v);
+}
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -311,6 +339,14 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint32
     return __all_sync(kFull, wait_long(bar, parity, err));
 }
 
+// Two waits in one: half of the warp's threads look at one barrier, half at the other.
+__device__ __forceinline__ bool wait_both(uint64_t *a, uint32_t parity_a, uint64_t *b, uint32_t parity_b, uint32_t *err) {
+    uint64_t *bar = threadIdx.x & 1 ? b : a;
+    const uint32_t parity = threadIdx.x & 1 ? parity_b : parity_a;
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(kFull, wait_long(bar, parity, err));
+}
+
 // A work's streams: stream t has key tiles first[t], first[t] + step, ... below end[t]; last: the end of both.
 struct Streams {
     int first[2], end[2], step, last;
@@ -334,10 +370,10 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFull, x, 0);
 // back, so that a stream's next scores come right behind its product with V.
 template <typename F>
 __device__ __forceinline__ bool tiles_in_order(const Streams &s, F tile) {
-    const int ahead = s.step;
-    for (int j = s.first[0]; j < s.last + ahead; ++j) {
-        if (j - ahead >= s.first[0] && !tile(true, j - ahead)) return false;
-        if (j < s.last && !tile(false, j)) return false;
+    int key = s.first[0], val = key;   // one place for both, so that the tile's code is there once
+    while (val < s.last) {
+        const bool value = key - val >= s.step || key == s.last;
+        if (!tile(value, value ? val++ : key++)) return false;
     }
     return true;
 }
@@ -444,7 +480,8 @@ constexpr float kShift = BF16 ? 0.f : 7.f;
 
 // Stream t's key tiles first, first + step, ... below end: its rows' statistics in r, their sums of p v in tensor memory.
 // mask(j, w): whether the rows of the warp see not all keys of tile j, and then the bits of those that this row sees.
-template <int D, bool BF16, int STAGES, typename Mask>
+// CK: scores read at a time (16: fewer registers).
+template <int D, bool BF16, int CK, int STAGES, typename Mask>
 __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, int step, int t, Bars<STAGES> &b, uint32_t tmem, float c,
                                              bool neg, uint32_t *err, Mask mask) {
     const uint32_t lane = ((threadIdx.x & 127) & ~31u) << 16;
@@ -459,27 +496,25 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
         ++r.n_s;
         tc_after();
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        {
-            float s[2][32];
-            tm_ld32(s_at, s[0]);
+#pragma unroll
+        for (int i = 0; i < kTile; i += 64) {
+            float x[64];
+            tm_ld32(s_at + i, x);
+            tm_ld32(s_at + i + 32, x + 32);
             tm_wait_ld();
+            if (masked || neg) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float (&x)[32] = s[i & 1];
-                if (i < 3) tm_ld32(s_at + 32 * (i + 1), s[(i + 1) & 1]);
-                if (masked || neg) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = masked && !(w[i] >> e & 1u) ? -INFINITY : neg ? -x[e] : x[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], x[e + 4 + q]);
-                if (i < 3) tm_wait_ld();
-                if (masked || neg) tm_st32(s_at + 32 * i, x);
+                for (int e = 0; e < 64; ++e) x[e] = masked && !(w[(i + e) / 32] >> e % 32 & 1u) ? -INFINITY : neg ? -x[e] : x[e];
+                tm_st32(s_at + i, x);
+                tm_st32(s_at + i + 32, x + 32);
             }
-            if (masked || neg) tm_wait_st();
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], x[e + 4 + q]);
         }
+        if (masked || neg) tm_wait_st();
+        constexpr int N = kTile / CK;
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (__any_sync(kFull, top > lead)) {
             const float m = top > lead ? top : r.m;
@@ -502,16 +537,16 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
         }
         const float add = fmaf(-base, c, kShift<BF16>);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        float s[2][32];
-        tm_ld32(s_at, s[0]);
+        float s[2][CK];
+        tm_ld<CK>(s_at, s[0]);
         tm_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float (&v)[32] = s[i & 1];
-            if (i < 3) tm_ld32(s_at + 32 * (i + 1), s[(i + 1) & 1]);
-            uint32_t p[16];
+        for (int i = 0; i < N; ++i) {
+            float (&v)[CK] = s[i & 1];
+            if (i < N - 1) tm_ld<CK>(s_at + CK * (i + 1), s[(i + 1) & 1]);
+            uint32_t p[CK / 2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < CK / 2; ++e) {
                 float &x = v[2 * e], &y = v[2 * e + 1];
                 fma2(x, y, c, add);
                 x = ex2(x);
@@ -519,13 +554,13 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
                 p[e] = pack2<BF16>(x, y);
                 add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], x, y);
             }
-            // P's columns 16 i .. are scores that have been read: of tile i / 2
-            if (i < 3) tm_wait_ld();
-            tm_st16(s_at + 16 * i, p);
-            if ((i + 1) % (4 / kParts) == 0) {
+            // P's columns are half as many: they are of scores that have been read
+            if (i < N - 1) tm_wait_ld();
+            tm_st_pairs<CK>(s_at + CK / 2 * i, p);
+            if ((i + 1) % (N / kParts) == 0) {
                 tm_wait_st();
                 tc_before();
-                mbar_arrive(&b.p_full[t][(i + 1) / (4 / kParts) - 1]);
+                mbar_arrive(&b.p_full[t][(i + 1) / (N / kParts) - 1]);
             }
         }
         r.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);

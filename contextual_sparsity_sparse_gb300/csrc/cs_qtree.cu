@@ -2,7 +2,7 @@
 //
 // The streams of cs_attn_tc.cuh over tiles that six warps make from the codes: a
 // tile's 128 slots become fp16 values, offset + scale * code with one rounding,
-// in the layout that the products take.  A seventh warp copies codes, scales
+// in the layout that the products take.  Another warp copies codes, scales
 // and positions into a ring ahead of them.  The tile behind the last slot
 // holds the drafted tokens themselves, and there a row sees its own ancestors.
 // Codes come as 8 nibbles to a word, of which an AND and an OR make two fp16
@@ -71,7 +71,7 @@ template <int D>
 struct TreeCfg {
     static constexpr int DB = D / 64;
     static constexpr int CH = D / 32;                 // 16-byte chunks of a slot's codes
-    static constexpr int ROWS = 32 / CH;              // slots of a unit: a warp's chunks
+    static constexpr int ROWS = 2 * 32 / CH;          // slots of a unit: a warp's chunks, two to a thread
     static constexpr int UNITS = kTile / ROWS;        // of a tile
     static constexpr int CODES = kTile * D / 2, SCALES = kTile * 4 * DB, RAW = CODES + SCALES + 4 * kTile;
     static constexpr size_t smem = (size_t)(2 + kTreeStages) * DB * kBlock + kRaw * RAW + 1024;
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 mbar_arrive(&sh.bars.q_full);
             }
             const int drafted = (w.n_k + kTile - 1) / kTile;   // the tile of the drafted tokens
-            if (!softmax_rows<D, false>(r, st.first[t], st.end[t], st.step, t, sh.bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
+            if (!softmax_rows<D, false, 32>(r, st.first[t], st.end[t], st.step, t, sh.bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
                     const uint32_t n = tiles + (j - w.j0), s = n % kSeenRing;
                     wait_warp(&sh.seen_full[s], n / kSeenRing & 1, a.err);
                     if (j < drafted) {
@@ -309,7 +309,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
             if (st.last <= w.j0) continue;
             ok = tiles_in_order(st, [&](bool value, int j) {
                 const uint32_t stage = it % kTreeStages, tile = tiles + (j - w.j0), slot = tile % kSeenRing;
-                if (it >= kTreeStages && !wait_warp(&sh.bars.empty[stage], (it / kTreeStages - 1) & 1, a.err)) return false;
+                // the stage is free, and the codes are there (a parity of 1 is that of the phase before the first)
+                const uint32_t free = (it / kTreeStages & 1) ^ 1, from = cached % kRaw, codes = raw + from * C::RAW;
+                if (!(j == drafted ? wait_warp(&sh.bars.empty[stage], free, a.err)
+                                   : wait_both(&sh.bars.empty[stage], free, &sh.raw_full[from], cached / kRaw & 1, a.err)))
+                    return false;
                 ++it;
                 const uint32_t to = ring + (stage * C::DB + chunk / 2) * kBlock;
                 if (j == drafted) {
@@ -326,9 +330,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                                 sh.parents[works % kParentRing][t] = (uint8_t)(p + 1);
                             }
                         }
-                        const int r = units * C::ROWS + in_unit;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+#pragma unroll 1
+                        for (int ik = 0; ik < 8; ++ik) {
+                            const int r = units * C::ROWS + in_unit + (ik >> 2) * (C::ROWS / 2), k = ik & 3;
                             float v[8] = {};
                             if (r < w.k0) load8(rows, src + r * rows.ldt + k * 8, v);
 #pragma unroll
@@ -344,44 +348,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                         mbar_arrive(&sh.bars.full[stage]);
                     }
                 } else {
-                    const uint32_t from = cached % kRaw, codes = raw + from * C::RAW;
-                    if (!wait_warp(&sh.raw_full[from], cached / kRaw & 1, a.err)) return false;
                     ++cached;
                     const int left = w.n_k - j * kTile;
                     // the words of a chunk in an order that keeps 8 lanes' stores in different banks
                     const bool swap = D == 128 && (chunk & 2);
 #pragma unroll 1
                     for (; units < C::UNITS; units += kMakers) {
-                        const int r = units * C::ROWS + in_unit, mine = units * C::ROWS + (lane & (C::ROWS - 1));
-                        uint4 cw;
-                        uint32_t sz;
+                        const int r0 = units * C::ROWS + in_unit, mine = units * C::ROWS + (lane & (C::ROWS - 1));
+                        uint4 cw[2];
+                        uint32_t sz[2];
                         int pos = 0;
                         if (a.c.pos) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(pos) : "r"(codes + C::CODES + C::SCALES + mine * 4));
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sz) : "r"(codes + C::CODES + (r * C::DB + chunk / 2) * 4));
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(cw.x), "=r"(cw.y), "=r"(cw.z), "=r"(cw.w)
-                                     : "r"(codes + r * (D / 2) + chunk * 16));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = r0 + i * (C::ROWS / 2);
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sz[i]) : "r"(codes + C::CODES + (r * C::DB + chunk / 2) * 4));
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(cw[i].x), "=r"(cw[i].y), "=r"(cw[i].z), "=r"(cw[i].w)
+                                         : "r"(codes + r * (D / 2) + chunk * 16));
+                        }
                         const uint32_t bits = __ballot_sync(kFull, pos >= 0 && mine < left);
-                        if (!value) {
-                            if (C::ROWS == 8 && lane == 0) reinterpret_cast<uint8_t *>(sh.seen[slot])[units] = (uint8_t)bits;
-                            if (C::ROWS == 16 && lane == 0) reinterpret_cast<uint16_t *>(sh.seen[slot])[units] = (uint16_t)bits;
-                        } else if (!(bits >> in_unit & 1u)) {
-                            sz = 0;   // it may hold anything: its value counts with 0 (and its key's scores are not looked at)
-                        }
-                        const __half2 hz = u2h(sz), s = __low2half2(hz), z = __high2half2(hz);
-                        const uint32_t word[4] = {swap ? cw.z : cw.x, swap ? cw.w : cw.y, swap ? cw.x : cw.z, swap ? cw.y : cw.w};
-                        uint32_t v[4][4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) decode8(word[k], s, z, v[k]);
-                        float sf, zf;
-                        half2x(sz, sf, zf);
-                        if (fmaf(15.f, sf, zf) > 65504.f) {   // a group that spans nearly all of fp16's range
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) v[k][e] = h2u(__hmin2(u2h(v[k][e]), __float2half2_rn(65504.f)));
+                        if (!value && lane == 0) {
+                            if (C::ROWS == 16) reinterpret_cast<uint16_t *>(sh.seen[slot])[units] = (uint16_t)bits;
+                            else sh.seen[slot][units & 3] = bits;
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v[k]);
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = r0 + i * (C::ROWS / 2);
+                            // a slot that is not there may hold anything: its value counts with 0 (and its key's scores are not looked at)
+                            if (value && !(bits >> (in_unit + i * (C::ROWS / 2)) & 1u)) sz[i] = 0;
+                            const __half2 hz = u2h(sz[i]), s = __low2half2(hz), z = __high2half2(hz);
+                            const uint32_t word[4] = {swap ? cw[i].z : cw[i].x, swap ? cw[i].w : cw[i].y, swap ? cw[i].x : cw[i].z,
+                                                      swap ? cw[i].y : cw[i].w};
+                            uint32_t v[4][4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) decode8(word[k], s, z, v[k]);
+                            float sf, zf;
+                            half2x(sz[i], sf, zf);
+                            if (fmaf(15.f, sf, zf) > 65504.f) {   // a group that spans nearly all of fp16's range
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) v[k][e] = h2u(__hmin2(u2h(v[k][e]), __float2half2_rn(65504.f)));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v[k]);
+                        }
                     }
                     fence_async();
                     __syncwarp();
