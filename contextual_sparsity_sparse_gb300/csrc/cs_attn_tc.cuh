@@ -123,6 +123,9 @@ __device__ __forceinline__ void tm_ld16(uint32_t t, float *v) {
                    "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(t));
 }
+__device__ __forceinline__ void tm_st1(uint32_t t, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "f"(v) : "memory");
+}
 // N fp32 columns, or N / 2 of pairs.
 template <int N>
 __device__ __forceinline__ void tm_ld(uint32_t t, float *v) {
@@ -478,8 +481,11 @@ struct RowState {
 template <bool BF16>
 constexpr float kShift = BF16 ? 0.f : 7.f;
 
+// What the rows of a warp see of a key tile: all of it, all the same keys, or each row keys of its own.
+enum Sight { SEE_ALL, SEE_SAME, SEE_OWN };
+
 // Stream t's key tiles first, first + step, ... below end: its rows' statistics in r, their sums of p v in tensor memory.
-// mask(j, w): whether the rows of the warp see not all keys of tile j, and then the bits of those that this row sees.
+// mask(j, w): what the warp's rows see of tile j, and unless it is all the bits of those keys.
 // CK: scores read at a time (16: fewer registers).
 template <int D, bool BF16, int CK, int STAGES, typename Mask>
 __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, int step, int t, Bars<STAGES> &b, uint32_t tmem, float c,
@@ -491,10 +497,27 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
     float base = 0.f, lead = -INFINITY;   // m, or 0 where that is -inf; a score beyond `lead` moves m
     for (int j = first; j < end; j += step) {
         uint32_t w[4];
-        const bool masked = mask(j, w);
+        const Sight sight = mask(j, w);
         if (!wait_warp(&b.s_full[t], r.n_s & 1, err)) return false;
         ++r.n_s;
         tc_after();
+        if (sight == SEE_SAME && !neg) {
+            // keys that nobody sees are columns, most often few: written over one by one (128 selections and their way back to
+            // tensor memory took 1,400 cycles of a tile's 5,300)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t out = ~w[i];
+                if (out == kFull) {
+                    float none[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) none[e] = -INFINITY;
+                    tm_st32(s_at + 32 * i, none);
+                } else {
+                    for (uint32_t b = out; b; b &= b - 1) tm_st1(s_at + 32 * i + __ffs(b) - 1, -INFINITY);
+                }
+            }
+            tm_wait_st();
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < kTile; i += 64) {
@@ -502,9 +525,9 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
             tm_ld32(s_at + i, x);
             tm_ld32(s_at + i + 32, x + 32);
             tm_wait_ld();
-            if (masked || neg) {
+            if (sight == SEE_OWN || neg) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] = masked && !(w[(i + e) / 32] >> e % 32 & 1u) ? -INFINITY : neg ? -x[e] : x[e];
+                for (int e = 0; e < 64; ++e) x[e] = sight != SEE_ALL && !(w[(i + e) / 32] >> e % 32 & 1u) ? -INFINITY : neg ? -x[e] : x[e];
                 tm_st32(s_at + i, x);
                 tm_st32(s_at + i + 32, x + 32);
             }
@@ -513,7 +536,7 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], x[e + 4 + q]);
         }
-        if (masked || neg) tm_wait_st();
+        if (sight == SEE_OWN || neg) tm_wait_st();
         constexpr int N = kTile / CK;
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (__any_sync(kFull, top > lead)) {

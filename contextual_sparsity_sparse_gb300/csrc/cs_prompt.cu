@@ -207,13 +207,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             const int lim = valid ? min(max(w.lim0 + step * at, 0), w.n_k) : 0;
             const int all = __reduce_min_sync(kFull, valid ? lim : INT_MAX);   // keys that all of the warp's rows see
             if (!softmax_rows<D, BF16, 32>(r, st.first[t], st.end[t], st.step, t, bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
-                    if (all >= (j + 1) * kTile) return false;
+                    if (all >= (j + 1) * kTile) return SEE_ALL;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int n = lim - j * kTile - 32 * e;
                         m[e] = n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u;
                     }
-                    return true;
+                    return SEE_OWN;
                 }))
                 break;
             Sums sums;

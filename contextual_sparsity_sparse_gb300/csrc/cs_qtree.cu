@@ -208,11 +208,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                     wait_warp(&sh.seen_full[s], n / kSeenRing & 1, a.err);
                     if (j < drafted) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(sh.seen[s]);
-                        m[0] = v.x;
-                        m[1] = v.y;
-                        m[2] = v.z;
-                        m[3] = v.w;
-                        return (v.x & v.y & v.z & v.w) != kFull;
+                        m[0] = uniform(v.x);
+                        m[1] = uniform(v.y);
+                        m[2] = uniform(v.z);
+                        m[3] = uniform(v.w);
+                        return (m[0] & m[1] & m[2] & m[3]) != kFull ? SEE_SAME : SEE_ALL;
                     }
                     m[0] = m[1] = m[2] = m[3] = 0;
                     if (valid) {
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                             }
                         }
                     }
-                    return true;
+                    return SEE_OWN;
                 }))
                 break;
             if (st.last > w.j0) {
