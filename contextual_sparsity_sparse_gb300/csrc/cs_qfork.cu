@@ -3,9 +3,14 @@
 //
 // Bound by memory: every copy is written once, and a source that several take is
 // read once from memory and then found in the second-level cache.  A CTA has a
-// range of slots of one head in all sequences, so that in place it can read
-// what all of them take before it writes any: only such a range has to fit
-// shared memory, whatever the lengths.
+// range of slots of one head and sequence; its threads take the range's six
+// arrays as one list of steps, all loads before the stores.  (One CTA for eight
+// sequences, array by array, waited for memory 48 times in a row: 65 us for 15
+// copies of 5 MB, 35 of a 32-sequence cache's beams 43 us.)
+//
+// In place, a sequence that is read may be written, too.  Then a range's first
+// CTA does all of its sequences, in pieces of which it reads what they take into
+// shared memory before it writes any, whatever the lengths.
 #include "cs_qcache.cuh"
 
 namespace cs {
@@ -13,8 +18,10 @@ namespace cs {
 namespace {
 
 constexpr int kForkThreads = 256;
+constexpr int kForkSteps = 5;            // of a thread, under way together
+constexpr int kForkHeld = 32 * 1024;     // bytes read ahead in place
 
-// One of a cache's six arrays: bytes of a slot, and how wide it can be copied.
+// One of a cache's six arrays: bytes of a slot, and of a copy's step (16, 8 or 4, by what all rows start on).
 struct ForkArray {
     const char *src;
     char *dst;
@@ -23,7 +30,8 @@ struct ForkArray {
 struct ForkK {
     ForkArray part[6];
     const int32_t *source, *length;
-    int from, to, heads, cap_src, cap_dst, slots, parts;
+    int begin[7];                        // the arrays' first steps in a range's list
+    int from, to, cap_src, cap_dst, slots, parts;
     int64_t ldb_src, ldh_src, ldb_dst, ldh_dst;
     int in_place;
     uint32_t *err;
@@ -43,52 +51,104 @@ __device__ __forceinline__ int fork_source(const ForkK &a, int i, int &len) {
     return a.in_place && s == i ? -1 : s;
 }
 
+__device__ __forceinline__ const char *fork_from(const ForkK &a, const ForkArray &p, int s, int h) {
+    return p.src + (s * a.ldb_src + h * a.ldh_src) * p.row;
+}
+__device__ __forceinline__ char *fork_to(const ForkK &a, const ForkArray &p, int i, int h) {
+    return p.dst + (i * a.ldb_dst + h * a.ldh_dst) * p.row;
+}
+
 template <typename V>
-__device__ __forceinline__ void fork_copy(const ForkK &a, const ForkArray &p, int h, int t0) {
-    const int units = a.slots * p.row / (int)sizeof(V);   // of the range
-    for (int u = threadIdx.x; u < units; u += kForkThreads) {
-        const int slot = t0 + u * (int)sizeof(V) / p.row;
-        for (int i = 0; i < a.to; ++i) {
-            int len;
-            const int s = fork_source(a, i, len);
-            if (s < 0 || slot >= len) continue;
-            const int64_t at = ((int64_t)t0 * p.row) / (int)sizeof(V) + u;
-            reinterpret_cast<V *>(p.dst + (i * a.ldb_dst + h * a.ldh_dst) * p.row)[at] =
-                ld_dep(reinterpret_cast<const V *>(p.src + (s * a.ldb_src + h * a.ldh_src) * p.row) + at);
+__device__ __forceinline__ void fork_load(uint4 &v, const char *p) { *reinterpret_cast<V *>(&v) = ld_dep(reinterpret_cast<const V *>(p)); }
+template <typename V>
+__device__ __forceinline__ void fork_store(const uint4 &v, char *p) { *reinterpret_cast<V *>(p) = *reinterpret_cast<const V *>(&v); }
+
+// Slots t0 .. of head h of sequence s, of which it has len, to sequence i.
+__device__ __forceinline__ void fork_copy(const ForkK &a, int i, int s, int len, int h, int t0) {
+    const int total = a.begin[a.parts];
+    for (int u0 = threadIdx.x; u0 < total; u0 += kForkSteps * kForkThreads) {
+        uint4 v[kForkSteps];
+        char *to[kForkSteps];
+        int bytes[kForkSteps];   // of the step: 0 none, less than its width at a source's end
+#pragma unroll
+        for (int k = 0; k < kForkSteps; ++k) {
+            const int u = u0 + k * kForkThreads;
+            bytes[k] = 0;
+            if (u >= total) continue;
+            int x = 0;
+#pragma unroll
+            for (int e = 1; e < 6; ++e) x += e < a.parts && u >= a.begin[e];
+            const ForkArray &p = a.part[x];
+            const int64_t at = (int64_t)t0 * p.row + (int64_t)(u - a.begin[x]) * p.wide;
+            bytes[k] = (int)max((int64_t)0, min((int64_t)p.wide, (int64_t)len * p.row - at));
+            if (bytes[k] == 0) continue;
+            const char *from = fork_from(a, p, s, h) + at;
+            to[k] = fork_to(a, p, i, h) + at;
+            if (bytes[k] == 16) fork_load<uint4>(v[k], from);
+            else if (bytes[k] == 8) fork_load<uint2>(v[k], from);
+            else if (bytes[k] == 4) fork_load<uint32_t>(v[k], from);
+            else {
+                fork_load<uint2>(v[k], from);
+                v[k].z = ld_dep(reinterpret_cast<const uint32_t *>(from) + 2);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kForkSteps; ++k) {
+            if (bytes[k] == 16) fork_store<uint4>(v[k], to[k]);
+            else if (bytes[k] == 8) fork_store<uint2>(v[k], to[k]);
+            else if (bytes[k] == 4) fork_store<uint32_t>(v[k], to[k]);
+            else if (bytes[k]) {
+                fork_store<uint2>(v[k], to[k]);
+                reinterpret_cast<uint32_t *>(to[k])[2] = v[k].z;
+            }
         }
     }
 }
 
-// One thread's sequences in order, so this is for copies between caches alone.
-__global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkK a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int h = blockIdx.y, t0 = blockIdx.x * a.slots;
-    for (int x = 0; x < a.parts; ++x) fork_copy<uint32_t>(a, a.part[x], h, t0);
-}
-
-// In place: words of all sequences, then written.
-__global__ void __launch_bounds__(kForkThreads) fork_in_place_kernel(ForkK a) {
-    extern __shared__ uint32_t held[];   // [to, slots x words of a slot]
-    pdl_wait();
-    pdl_launch_dependents();
-    const int h = blockIdx.y, t0 = blockIdx.x * a.slots;
-    for (int x = 0; x < a.parts; ++x) {
-        const ForkArray &p = a.part[x];
-        const int words = a.slots * p.row / 4;
+// In place, a sequence that is read is written, too: what a piece's sequences take is read before any of it is written.
+__device__ __forceinline__ void fork_held(const ForkK &a, const ForkArray &p, int h, int t0, int t1, uint32_t *held) {
+    const int fit = max(kForkHeld / (a.to * p.row), 1);   // slots of a piece
+    for (; t0 < t1; t0 += fit) {
+        const int words = min(fit, t1 - t0) * p.row / 4;
+#pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
             for (int64_t e = threadIdx.x; e < (int64_t)words * a.to; e += kForkThreads) {
-                const int i = (int)(e / words), u = (int)(e % words);
+                const int i = (int)(e / words), u = (int)(e - (int64_t)i * words);
                 int len;
                 const int s = fork_source(a, i, len);
                 if (s < 0 || t0 + u * 4 / p.row >= len) continue;
                 const int64_t at = (int64_t)t0 * p.row / 4 + u;
-                if (pass == 0) held[e] = ld_dep(reinterpret_cast<const uint32_t *>(p.src + (s * a.ldb_src + h * a.ldh_src) * p.row) + at);
-                else reinterpret_cast<uint32_t *>(p.dst + (i * a.ldb_dst + h * a.ldh_dst) * p.row)[at] = held[e];
+                if (pass == 0) held[e] = ld_dep(reinterpret_cast<const uint32_t *>(fork_from(a, p, s, h)) + at);
+                else reinterpret_cast<uint32_t *>(fork_to(a, p, i, h))[at] = held[e];
             }
             __syncthreads();
         }
     }
+}
+
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kForkThreads, 5) fork_kernel(ForkK a) {
+    extern __shared__ uint32_t held[];   // in place: kForkHeld bytes, or one slot's rows of all sequences
+    pdl_wait();
+    pdl_launch_dependents();
+    const int h = blockIdx.y, t0 = blockIdx.x * a.slots, i = blockIdx.z;
+    int len;
+    const int s = fork_source(a, i, len);
+    if (IN_PLACE) {
+        bool both = false;   // whether some sequence is read and written
+        for (int j = threadIdx.x; j < a.to; j += kForkThreads) {
+            const int x = ld_dep(a.source + j);
+            if (x < 0 || x >= a.to || x == j) continue;
+            const int y = ld_dep(a.source + x);
+            both |= y >= 0 && y < a.to && y != x;
+        }
+        if (__syncthreads_or(both)) {
+            if (i == 0)
+                for (int x = 0; x < a.parts; ++x) fork_held(a, a.part[x], h, t0, min(t0 + a.slots, a.cap_src), held);
+            return;
+        }
+    }
+    if (s >= 0 && t0 < len) fork_copy(a, i, s, len, h, t0);
 }
 
 }  // namespace
@@ -119,21 +179,10 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
     st = check_qws(ws, ws_bytes, kControlBytes, who);
     if (st != CS_OK) return st;
     ForkK a{};
-    const int g4 = c.d / kQGroup * 4;
-    auto put = [&](const void *s, void *d, int row) {
-        if (s) a.part[a.parts++] = ForkArray{static_cast<const char *>(s), static_cast<char *>(d), row, 4};
-    };
-    put(c.k, to.k, c.d / 2);
-    put(c.v, to.v, c.d / 2);
-    put(c.ks, to.ks, g4);
-    put(c.vs, to.vs, g4);
-    put(c.weight, to.weight, 4);
-    put(c.pos, to.pos, 4);
     a.source = source;
     a.length = length;
     a.from = c.batch;
     a.to = to.batch;
-    a.heads = c.heads;
     a.cap_src = c.cap;
     a.cap_dst = to.cap;
     a.ldb_src = c.ldb;
@@ -142,22 +191,40 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
     a.ldh_dst = to.ldh;
     a.in_place = same == all;
     a.err = static_cast<uint32_t *>(ws);
-    a.slots = 64;
-    cudaError_t e;
+    int widest = 0;
+    auto put = [&](const void *src_at, void *dst_at, int row) {
+        if (!src_at) return;
+        // steps as wide as everything that starts a row of the array allows
+        uint64_t bits = reinterpret_cast<uintptr_t>(src_at) | reinterpret_cast<uintptr_t>(dst_at) | 16;
+        if (c.batch > 1) bits |= (uint64_t)c.ldb * row;
+        if (to.batch > 1) bits |= (uint64_t)to.ldb * row;
+        if (c.heads > 1) bits |= (uint64_t)c.ldh * row | (uint64_t)to.ldh * row;
+        a.part[a.parts++] = ForkArray{static_cast<const char *>(src_at), static_cast<char *>(dst_at), row, (int)(bits & -bits)};
+        widest = row > widest ? row : widest;
+    };
+    put(c.k, to.k, c.d / 2);
+    put(c.v, to.v, c.d / 2);
+    put(c.ks, to.ks, c.d / kQGroup * 4);
+    put(c.vs, to.vs, c.d / kQGroup * 4);
+    put(c.weight, to.weight, 4);
+    put(c.pos, to.pos, 4);
+    // ranges of 16 slots at least, so that every array's starts a step; of 128 a thread has five steps (d_head 128)
+    const int sms = device_sm_count(), most = c.cap < to.cap ? c.cap : to.cap;
+    a.slots = 128;
+    while (a.slots > 16 && (int64_t)((most + a.slots - 1) / a.slots) * c.heads * a.to < 8 * (int64_t)sms) a.slots /= 2;
+    for (int x = 0; x < a.parts; ++x) a.begin[x + 1] = a.begin[x] + a.slots * a.part[x].row / a.part[x].wide;
+    const dim3 grid((most + a.slots - 1) / a.slots, c.heads, a.to);
+    cudaError_t e = cudaSuccess;
     if (a.in_place) {
-        a.slots = 1;
-        e = allow_smem(reinterpret_cast<const void *>(&fork_in_place_kernel));
-        const size_t smem = (size_t)a.to * a.slots * (c.d / 2);
-        if (smem > 200 * 1024) {
-            set_error("%s: %d sequences in place are too many", who, a.to);
+        const size_t smem = (size_t)a.to * widest > kForkHeld ? (size_t)a.to * widest : kForkHeld;
+        if (smem > 224 * 1024) {
+            set_error("%s: %d sequences of d_head %d in place are too many", who, a.to, c.d);
             return CS_ERR_UNSUPPORTED;
         }
-        if (e == cudaSuccess)
-            e = launch(fork_in_place_kernel, dim3((c.cap + a.slots - 1) / a.slots, c.heads), dim3(kForkThreads), smem,
-                       (cudaStream_t)stream, pdl_enabled(), a);
+        if (smem > 48 * 1024) e = allow_smem(reinterpret_cast<const void *>(&fork_kernel<true>));
+        if (e == cudaSuccess) e = launch(fork_kernel<true>, grid, dim3(kForkThreads), smem, (cudaStream_t)stream, pdl_enabled(), a);
     } else {
-        e = launch(fork_kernel, dim3((c.cap + a.slots - 1) / a.slots, c.heads), dim3(kForkThreads), 0, (cudaStream_t)stream,
-                   pdl_enabled(), a);
+        e = launch(fork_kernel<false>, grid, dim3(kForkThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
     }
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
