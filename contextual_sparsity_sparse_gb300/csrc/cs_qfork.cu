@@ -1,16 +1,18 @@
 // Sequences of a 4-bit KV cache taken over by others: samples from one prompt,
 // beams that change places.
 //
-// Bound by memory: every copy is written once, and a source that several take is
-// read once from memory and then found in the second-level cache.  A CTA has a
-// range of slots of one head and sequence; its threads take the range's six
-// arrays as one list of steps, all loads before the stores.  (One CTA for eight
-// sequences, array by array, waited for memory 48 times in a row: 65 us for 15
-// copies of 5 MB, 35 of a 32-sequence cache's beams 43 us.)
+// Bound by memory and the way to it: every copy is written once, and a source read
+// once however many take it.  All ranges of kForkSlots slots of the heads of the
+// sources that somebody takes are one list, which the CTAs go through; a CTA's
+// threads take a range's six arrays as one list of steps, all loads before the
+// stores, and store to every sequence that takes the source.  15 copies of 5 MB
+// (a copy of 80 MB takes 27 us, its writing alone 12): with a CTA for each copy and range, which
+// reads a source again for each, 24 us; with one for each source and range, most of which
+// nobody takes, 35.
 //
-// In place, a sequence that is read may be written, too.  Then a range's first
-// CTA does all of its sequences, in pieces of which it reads what they take into
-// shared memory before it writes any, whatever the lengths.
+// In place, a sequence that is read may be written, too.  Then a CTA does a range
+// of all sequences, in pieces of which it reads what they take into shared memory
+// before it writes any, whatever the lengths.
 #include "cs_qcache.cuh"
 
 namespace cs {
@@ -18,7 +20,8 @@ namespace cs {
 namespace {
 
 constexpr int kForkThreads = 256;
-constexpr int kForkSteps = 5;            // of a thread, under way together
+constexpr int kForkSlots = 64;           // of a range: a multiple of 16, so that every array's part starts a step
+constexpr int kForkSteps = 3;            // of a thread, under way together
 constexpr int kForkHeld = 32 * 1024;     // bytes read ahead in place
 
 // One of a cache's six arrays: bytes of a slot, and of a copy's step (16, 8 or 4, by what all rows start on).
@@ -31,24 +34,19 @@ struct ForkK {
     ForkArray part[6];
     const int32_t *source, *length;
     int begin[7];                        // the arrays' first steps in a range's list
-    int from, to, cap_src, cap_dst, slots, parts;
+    int from, to, heads, cap_src, cap_dst, parts;
     int64_t ldb_src, ldh_src, ldb_dst, ldh_dst;
     int in_place;
     uint32_t *err;
 };
 
-// The sequence that i takes, or -1: none, or its own in place; and its slots.
-__device__ __forceinline__ int fork_source(const ForkK &a, int i, int &len) {
+// The sequence that i takes, or -1: none, or its own in place.
+__device__ __forceinline__ int fork_source(const ForkK &a, int i) {
     const int s = ld_dep(a.source + i);
-    len = 0;
-    if (s < 0 || s >= a.from) {
-        if (s != -1) atomicOr(a.err, CS_DEVERR_INDEX);
-        return -1;
-    }
-    const int n = ld_dep(a.length + s);
-    len = min(max(n, 0), min(a.cap_src, a.cap_dst));
-    if (n != len) atomicOr(a.err, CS_DEVERR_COUNT);
-    return a.in_place && s == i ? -1 : s;
+    return s < 0 || s >= a.from || (a.in_place && s == i) ? -1 : s;
+}
+__device__ __forceinline__ int fork_length(const ForkK &a, int s) {
+    return min(max(ld_dep(a.length + s), 0), min(a.cap_src, a.cap_dst));
 }
 
 __device__ __forceinline__ const char *fork_from(const ForkK &a, const ForkArray &p, int s, int h) {
@@ -63,13 +61,13 @@ __device__ __forceinline__ void fork_load(uint4 &v, const char *p) { *reinterpre
 template <typename V>
 __device__ __forceinline__ void fork_store(const uint4 &v, char *p) { *reinterpret_cast<V *>(p) = *reinterpret_cast<const V *>(&v); }
 
-// Slots t0 .. of head h of sequence s, of which it has len, to sequence i.
-__device__ __forceinline__ void fork_copy(const ForkK &a, int i, int s, int len, int h, int t0) {
+// Slots t0 .. of head h of sequence s, of which it has len, to the sequences of the chain that begins with `taker`.
+__device__ __forceinline__ void fork_copy(const ForkK &a, int s, int len, int h, int t0, int taker, const int *next) {
     const int total = a.begin[a.parts];
     for (int u0 = threadIdx.x; u0 < total; u0 += kForkSteps * kForkThreads) {
         uint4 v[kForkSteps];
-        char *to[kForkSteps];
-        int bytes[kForkSteps];   // of the step: 0 none, less than its width at a source's end
+        char *to[kForkSteps];    // in sequence 0
+        int row[kForkSteps], bytes[kForkSteps];   // bytes of the step: 0 none, less than its width at a source's end
 #pragma unroll
         for (int k = 0; k < kForkSteps; ++k) {
             const int u = u0 + k * kForkThreads;
@@ -83,7 +81,8 @@ __device__ __forceinline__ void fork_copy(const ForkK &a, int i, int s, int len,
             bytes[k] = (int)max((int64_t)0, min((int64_t)p.wide, (int64_t)len * p.row - at));
             if (bytes[k] == 0) continue;
             const char *from = fork_from(a, p, s, h) + at;
-            to[k] = fork_to(a, p, i, h) + at;
+            to[k] = fork_to(a, p, 0, h) + at;
+            row[k] = p.row;
             if (bytes[k] == 16) fork_load<uint4>(v[k], from);
             else if (bytes[k] == 8) fork_load<uint2>(v[k], from);
             else if (bytes[k] == 4) fork_load<uint32_t>(v[k], from);
@@ -92,14 +91,18 @@ __device__ __forceinline__ void fork_copy(const ForkK &a, int i, int s, int len,
                 v[k].z = ld_dep(reinterpret_cast<const uint32_t *>(from) + 2);
             }
         }
+        for (int i = taker; i >= 0; i = next[i]) {
+            const int64_t slots = i * a.ldb_dst;
 #pragma unroll
-        for (int k = 0; k < kForkSteps; ++k) {
-            if (bytes[k] == 16) fork_store<uint4>(v[k], to[k]);
-            else if (bytes[k] == 8) fork_store<uint2>(v[k], to[k]);
-            else if (bytes[k] == 4) fork_store<uint32_t>(v[k], to[k]);
-            else if (bytes[k]) {
-                fork_store<uint2>(v[k], to[k]);
-                reinterpret_cast<uint32_t *>(to[k])[2] = v[k].z;
+            for (int k = 0; k < kForkSteps; ++k) {
+                char *at = to[k] + slots * row[k];
+                if (bytes[k] == 16) fork_store<uint4>(v[k], at);
+                else if (bytes[k] == 8) fork_store<uint2>(v[k], at);
+                else if (bytes[k] == 4) fork_store<uint32_t>(v[k], at);
+                else if (bytes[k]) {
+                    fork_store<uint2>(v[k], at);
+                    reinterpret_cast<uint32_t *>(at)[2] = v[k].z;
+                }
             }
         }
     }
@@ -114,9 +117,8 @@ __device__ __forceinline__ void fork_held(const ForkK &a, const ForkArray &p, in
         for (int pass = 0; pass < 2; ++pass) {
             for (int64_t e = threadIdx.x; e < (int64_t)words * a.to; e += kForkThreads) {
                 const int i = (int)(e / words), u = (int)(e - (int64_t)i * words);
-                int len;
-                const int s = fork_source(a, i, len);
-                if (s < 0 || t0 + u * 4 / p.row >= len) continue;
+                const int s = fork_source(a, i);
+                if (s < 0 || t0 + u * 4 / p.row >= fork_length(a, s)) continue;
                 const int64_t at = (int64_t)t0 * p.row / 4 + u;
                 if (pass == 0) held[e] = ld_dep(reinterpret_cast<const uint32_t *>(fork_from(a, p, s, h)) + at);
                 else reinterpret_cast<uint32_t *>(fork_to(a, p, i, h))[at] = held[e];
@@ -126,29 +128,65 @@ __device__ __forceinline__ void fork_held(const ForkK &a, const ForkArray &p, in
     }
 }
 
-template <bool IN_PLACE>
-__global__ void __launch_bounds__(kForkThreads, 5) fork_kernel(ForkK a) {
-    extern __shared__ uint32_t held[];   // in place: kForkHeld bytes, or one slot's rows of all sequences
+__global__ void __launch_bounds__(kForkThreads, 4) fork_kernel(ForkK a) {
+    // who takes a source, as chains; the sources that are taken, and their ranges' places in the list.  In place, where
+    // sequences are read and written, what is held (kForkHeld bytes, or one slot's rows of all sequences).
+    extern __shared__ uint32_t smem[];
+    __shared__ int scan[32], active, ranges;
+    int *taker = reinterpret_cast<int *>(smem), *next = taker + a.from, *taken = next + a.to, *place = taken + a.from;
+    const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    const int h = blockIdx.y, t0 = blockIdx.x * a.slots, i = blockIdx.z;
-    int len;
-    const int s = fork_source(a, i, len);
-    if (IN_PLACE) {
-        bool both = false;   // whether some sequence is read and written
-        for (int j = threadIdx.x; j < a.to; j += kForkThreads) {
-            const int x = ld_dep(a.source + j);
-            if (x < 0 || x >= a.to || x == j) continue;
-            const int y = ld_dep(a.source + x);
-            both |= y >= 0 && y < a.to && y != x;
+    for (int s = tid; s < a.from; s += kForkThreads) taker[s] = -1;
+    if (tid == 0) active = ranges = 0;
+    __syncthreads();
+    bool both = false;   // whether some sequence is read and written
+    for (int i = tid; i < a.to; i += kForkThreads) {
+        const int x = ld_dep(a.source + i), s = fork_source(a, i);
+        if (blockIdx.x == 0) {
+            // tell what is wrong
+            if (x != -1 && (x < 0 || x >= a.from)) atomicOr(a.err, CS_DEVERR_INDEX);
+            else if (x >= 0 && ld_dep(a.length + x) != fork_length(a, x)) atomicOr(a.err, CS_DEVERR_COUNT);
         }
-        if (__syncthreads_or(both)) {
-            if (i == 0)
-                for (int x = 0; x < a.parts; ++x) fork_held(a, a.part[x], h, t0, min(t0 + a.slots, a.cap_src), held);
-            return;
-        }
+        if (s < 0) continue;
+        next[i] = atomicExch(&taker[s], i);
+        if (a.in_place) both |= fork_source(a, s) >= 0;
     }
-    if (s >= 0 && t0 < len) fork_copy(a, i, s, len, h, t0);
+    if (__syncthreads_or(both)) {
+        const int parts = (a.cap_src + kForkSlots - 1) / kForkSlots;
+        for (int64_t x = blockIdx.x; x < (int64_t)parts * a.heads; x += gridDim.x) {
+            const int h = (int)(x / parts), t0 = (int)(x % parts) * kForkSlots;
+            for (int p = 0; p < a.parts; ++p) fork_held(a, a.part[p], h, t0, min(t0 + kForkSlots, a.cap_src), smem);
+        }
+        return;
+    }
+    for (int s0 = 0; s0 < a.from; s0 += kForkThreads) {
+        const int s = s0 + tid;
+        const bool some = s < a.from && taker[s] >= 0;
+        const int n = some ? (fork_length(a, s) + kForkSlots - 1) / kForkSlots * a.heads : 0;
+        int sum, count;
+        const int at = block_excl_scan(n, scan, &sum), index = block_excl_scan(some, scan, &count);
+        if (some) {
+            taken[active + index] = s;
+            place[active + index] = ranges + at;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            active += count;
+            ranges += sum;
+        }
+        __syncthreads();
+    }
+    for (int x = blockIdx.x; x < ranges; x += gridDim.x) {
+        int lo = 0, hi = active;   // the last source whose ranges do not begin behind x
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (place[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        const int s = taken[lo], len = fork_length(a, s), parts = (len + kForkSlots - 1) / kForkSlots, r = x - place[lo];
+        fork_copy(a, s, len, r / parts, r % parts * kForkSlots, taker[s], next);
+    }
 }
 
 }  // namespace
@@ -183,6 +221,7 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
     a.length = length;
     a.from = c.batch;
     a.to = to.batch;
+    a.heads = c.heads;
     a.cap_src = c.cap;
     a.cap_dst = to.cap;
     a.ldb_src = c.ldb;
@@ -208,24 +247,21 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
     put(c.vs, to.vs, c.d / kQGroup * 4);
     put(c.weight, to.weight, 4);
     put(c.pos, to.pos, 4);
-    // ranges of 16 slots at least, so that every array's starts a step; of 128 a thread has five steps (d_head 128)
-    const int sms = device_sm_count(), most = c.cap < to.cap ? c.cap : to.cap;
-    a.slots = 128;
-    while (a.slots > 16 && (int64_t)((most + a.slots - 1) / a.slots) * c.heads * a.to < 8 * (int64_t)sms) a.slots /= 2;
-    for (int x = 0; x < a.parts; ++x) a.begin[x + 1] = a.begin[x] + a.slots * a.part[x].row / a.part[x].wide;
-    const dim3 grid((most + a.slots - 1) / a.slots, c.heads, a.to);
-    cudaError_t e = cudaSuccess;
+    for (int x = 0; x < a.parts; ++x) a.begin[x + 1] = a.begin[x] + kForkSlots * a.part[x].row / a.part[x].wide;
+    size_t smem = (3 * (size_t)a.from + a.to) * sizeof(int);
     if (a.in_place) {
-        const size_t smem = (size_t)a.to * widest > kForkHeld ? (size_t)a.to * widest : kForkHeld;
-        if (smem > 224 * 1024) {
+        const size_t hold = (size_t)a.to * widest > kForkHeld ? (size_t)a.to * widest : kForkHeld;
+        if (hold > 224 * 1024) {
             set_error("%s: %d sequences of d_head %d in place are too many", who, a.to, c.d);
             return CS_ERR_UNSUPPORTED;
         }
-        if (smem > 48 * 1024) e = allow_smem(reinterpret_cast<const void *>(&fork_kernel<true>));
-        if (e == cudaSuccess) e = launch(fork_kernel<true>, grid, dim3(kForkThreads), smem, (cudaStream_t)stream, pdl_enabled(), a);
-    } else {
-        e = launch(fork_kernel<false>, grid, dim3(kForkThreads), 0, (cudaStream_t)stream, pdl_enabled(), a);
+        if (hold > smem) smem = hold;
     }
+    const int sms = device_sm_count();
+    cudaError_t e = cudaSuccess;
+    if (smem > 47 * 1024) e = allow_smem(reinterpret_cast<const void *>(&fork_kernel));
+    if (e == cudaSuccess)
+        e = launch(fork_kernel, dim3(4 * (sms > 0 ? sms : 1)), dim3(kForkThreads), smem, (cudaStream_t)stream, pdl_enabled(), a);
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 
