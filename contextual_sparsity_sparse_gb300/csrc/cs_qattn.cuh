@@ -243,6 +243,7 @@ __device__ __forceinline__ bool row_on(const QAttnK &k, int b, int h, int r) {
 
 // The last position that a row sees; past the largest there is, that.
 __device__ __forceinline__ int last_seen(const QAttnK &k, int b, int r) {
+    if (!k.a.q_pos) return INT_MAX;
     const int t = (k.row0 + r) / k.group;
     return min(ld_dep(k.a.q_pos + b), INT_MAX - t) + t;
 }
@@ -383,6 +384,13 @@ __device__ __forceinline__ int first_seq(const Axis &x, int B, int at) {
     return lo;
 }
 
+// A row's statistics: m and l of its pass, m in units of 1 / c1.
+__device__ __forceinline__ void put_stat(const QAttnK &k, int b, int head, int row, float m, float l, float c1) {
+    const int r = k.row0 + row;
+    k.a.stat[((int64_t)b * k.a.n_q + r / k.group) * k.a.heads + head * k.group + r % k.group] =
+        make_float2(m == -INFINITY ? -INFINITY : m * c1, l);
+}
+
 __device__ __forceinline__ int64_t out_at(const QAttnK &k, int b, int head, int row) {
     const int r = k.row0 + row;
     return b * k.a.out.ldb + r / k.group * k.a.out.ldt + (int64_t)(head * k.group + r % k.group) * k.a.out.ldh;
@@ -521,7 +529,7 @@ __device__ __forceinline__ void fetch(const QAttnK &k, uint32_t stage, int64_t s
                 cp_async_or0<SP>(sc + C::UT * C::G * 4 + i * SP, on ? vs + i * SP : reinterpret_cast<const char *>(c.vs), on);
             }
     }
-    if (k.a.q_pos && lane < C::UT)
+    if ((k.a.q_pos || k.a.taken) && lane < C::UT)
         cp_async_or0<4>(stage + C::UT * (2 * C::RB + C::G * 8) + lane * 4, lane < n ? c.pos + slot0 + lane : c.pos, lane < n);
 }
 
@@ -556,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
 
     const char *ring = smem + warp * C::ST * C::STAGE;
     const uint32_t ring_at = smem_addr(ring);
-    const bool by_pos = k.a.q_pos != nullptr, weighing = k.a.weight != nullptr;
+    const bool by_pos = k.a.q_pos || k.a.taken, weighing = k.a.weight != nullptr;
 
     // the fetching side runs ahead of the computing side, on across heads
     Seg s{};
@@ -1054,6 +1062,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MODE>::MINB) qattn_kernel(QAt
                         base[row] = m;
                         sum[row] = cols[row * C::CS + 2] != 0.f ? l : 0.f;   // a row that is not asked for has no sum
                         cc1[row] = c;
+                        if (k.a.stat && whole && row < k.rows) put_stat(k, s.b, head, row, m, sum[row], c);
                     }
                 }
                 __syncthreads();
@@ -1142,6 +1151,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_join_kernel(QAttnK k) {
             if (!idle(i)) continue;
             const int b = (int)(i / c.heads), h = (int)(i % c.heads);
             for (int e = tid; e < k.rows * D; e += kThreads) q_store1(k.a.out, out_at(k, b, h, e / D) + e % D, 0.f);
+            if (k.a.stat && tid < k.rows) put_stat(k, b, h, tid, -INFINITY, 0.f, 1.f);
             if (k.a.weight)
                 for (int e = tid; e < q_length(k.a.length, b, c.cap, nullptr); e += kThreads) {
                     const int64_t slot = c.slot0(b, h) + e;
@@ -1177,6 +1187,8 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_join_kernel(QAttnK k) {
             base[i / RP][row] = m;
             inv[i / RP][row] = l == 0.f ? 0.f : 1.f / l;
             cc1[i / RP][row] = c1;
+            // m is 0 for a row that saw nothing, whose l is 0 as well
+            if (k.a.stat && row < k.rows && sub == 0) put_stat(k, x.b, x.head, row, l == 0.f ? -INFINITY : m, l, c1);
         }
     }
     __syncthreads();

@@ -56,6 +56,8 @@ struct QAttnArgs {
     const uint32_t *mask;
     float scale, decay;
     float *weight;           // or null
+    bool taken = false;      // without q_pos: a slot counts where its position is not negative
+    float2 *stat = nullptr;  // [batch, n_q, heads] or null: log2 of a row's largest term, and the sum of its terms by that
     uint32_t *err;
     char *scratch;           // the workspace behind its control words
     int sms;

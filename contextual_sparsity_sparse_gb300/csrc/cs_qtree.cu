@@ -472,6 +472,69 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
     if (warp == kIssuer) tm_free(tmem);
 }
 
+// -------------------------------------------------------------------- few rows
+//
+// The products above work on 128 rows however few there are.  Up to kFewRows rows
+// of a cache head, which are one pass of the kernels of cs_qcache_attention, these
+// go over the slots instead, and leave outputs in 32 bits with each row's
+// statistics; a warp to a row then adds the drafted tokens on its path.  With 16 rows
+// 131,001 slots of 8 heads take 75 us so and 164 with the products above, 32 ragged sequences of up to
+// 8,192 106 and 142, 40 heads of 2,048 28 and 37; with 32 rows, two passes, 148 and 153, 207 and 143, 52 and 38.
+
+constexpr int kFewRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256) tree_path_kernel(TreeK a, const float *cached, const float2 *stat) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;   // [batch, n, heads]
+    if (row >= (int64_t)a.c.batch * a.n * a.heads) return;
+    const int lane = threadIdx.x & 31, head = (int)(row % a.heads), t = (int)(row / a.heads % a.n);
+    const int b = (int)(row / a.heads / a.n), h = head / a.group, n = tree_count(a, b);
+    float o[D / 32] = {};
+    if (t < n) {
+        const float c = a.scale * 1.44269504088896341f;
+        const float2 st = ld_dep(stat + row);
+        float m = st.x, l = st.y, x[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            x[i] = c * q_load1(a.q, b * a.q.ldb + t * a.q.ldt + (int64_t)head * a.q.ldh + lane + 32 * i);
+            o[i] = l * ld_dep(cached + row * D + lane + 32 * i);
+        }
+        for (int u = t; u >= 0;) {
+            float s = 0.f, v[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int ch = lane + 32 * i;
+                s = fmaf(x[i], as_drafted(q_load1(a.k, b * a.k.ldb + u * a.k.ldt + h * a.k.ldh + ch)), s);
+                v[i] = as_drafted(q_load1(a.v, b * a.v.ldb + u * a.v.ldt + h * a.v.ldh + ch));
+            }
+            int next = u - 1;
+            if (a.parent) {
+                next = ld_dep(a.parent + (int64_t)b * a.n + u);
+                if (next < -1 || next >= u) next = -1;   // flagged below
+            }
+            s = warp_sum(s);
+            const float up = fmaxf(m, s), base = up == -INFINITY ? 0.f : up;
+            const float keep = m == -INFINITY ? 0.f : exp2f(m - base), p = exp2f(s - base);
+            m = up;
+            l = fmaf(l, keep, p);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], keep, p * v[i]);
+            u = next;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
+        if (a.parent && head == 0 && lane == 0) {
+            const int p = ld_dep(a.parent + (int64_t)b * a.n + t);
+            if (p < -1 || p >= t) atomicOr(a.err, CS_DEVERR_INDEX);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        q_store1(a.out, b * a.out.ldb + t * a.out.ldt + (int64_t)head * a.out.ldh + lane + 32 * i, o[i]);
+}
+
 // ------------------------------------------------------------------- host side
 
 bool tree_sizes(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n) {
@@ -480,10 +543,49 @@ bool tree_sizes(int batch, int kv_heads, int capacity, int d_head, int n_heads, 
            n_heads / kv_heads <= kTile && (int64_t)n_heads / kv_heads * n <= kQMaxRows;
 }
 
+// For few rows: the slots' outputs, the rows' statistics, and the other kernels' own.
+struct FewScratch {
+    size_t out, stat, attn;
+};
+FewScratch few_scratch(int batch, int kv_heads, int capacity, int d, int n_heads, int n, int sms) {
+    const size_t rows = (size_t)batch * n * n_heads;
+    return FewScratch{align256(rows * d * sizeof(float)), align256(rows * sizeof(float2)),
+                      qattn_scratch(batch, kv_heads, capacity, d, n_heads, n, false, sms)};
+}
+
 // The list's place behind the control words; returns the bytes.
-size_t tree_scratch(int batch, int capacity, int d, int group, int n, int sms, char *at, Plan *plan) {
+size_t tree_scratch(int batch, int kv_heads, int capacity, int d, int n_heads, int n, int sms, char *at, Plan *plan) {
+    // what calls of fewer heads and tokens need is in it: for few rows, of as many as there can be
+    const int group = n_heads / kv_heads, few_rows = group * n < kFewRows ? group * n : kFewRows;
+    const FewScratch few = few_scratch(batch, kv_heads, capacity, d, kv_heads * few_rows, 1, sms);
     const int pair = 2 * (kTile / group), recs = capacity > (kLeastPiece - 1) * kTile ? 2 * sms : 0;
-    return plan_scratch((size_t)batch * ((n + pair - 1) / pair), recs, d, at, plan);
+    const size_t many = plan_scratch((size_t)batch * ((n + pair - 1) / pair), recs, d, at, plan), fewer = few.out + few.stat + few.attn;
+    return many > fewer ? many : fewer;
+}
+
+cudaError_t run_few(const TreeK &a, char *scratch, cudaStream_t s) {
+    const FewScratch need = few_scratch(a.c.batch, a.c.heads, a.c.cap, a.c.d, a.heads, a.n, a.sms);
+    float *out = reinterpret_cast<float *>(scratch);
+    float2 *stat = reinterpret_cast<float2 *>(scratch + need.out);
+    QAttnArgs q{};
+    q.c = a.c;
+    q.q = a.q;
+    q.out = QRowsK{scratch, (int64_t)a.n * a.heads * a.c.d, (int64_t)a.heads * a.c.d, a.c.d, CS_F32, 1};
+    q.heads = a.heads;
+    q.n_q = a.n;
+    q.length = a.length;
+    q.scale = a.scale;
+    q.taken = a.c.pos != nullptr;
+    q.stat = stat;
+    q.err = a.err;
+    q.scratch = scratch + need.out + need.stat;
+    q.sms = a.sms;
+    cudaError_t e = launch_qattn(q, s);
+    const dim3 grid((unsigned)(((int64_t)a.c.batch * a.n * a.heads + 7) / 8));
+    if (e == cudaSuccess)
+        e = a.c.d == 64 ? launch(tree_path_kernel<64>, grid, dim3(256), 0, s, pdl_enabled(), a, (const float *)out, (const float2 *)stat)
+                        : launch(tree_path_kernel<128>, grid, dim3(256), 0, s, pdl_enabled(), a, (const float *)out, (const float2 *)stat);
+    return e;
 }
 
 template <int D, bool BF16>
@@ -506,7 +608,7 @@ extern "C" {
 
 size_t cs_qcache_tree_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n) {
     if (!tree_sizes(batch, kv_heads, capacity, d_head, n_heads, n)) return 0;
-    return kControlBytes + tree_scratch(batch, capacity, d_head, n_heads / kv_heads, n, device_sm_count(), nullptr, nullptr);
+    return kControlBytes + tree_scratch(batch, kv_heads, capacity, d_head, n_heads, n, device_sm_count(), nullptr, nullptr);
 }
 
 cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q, const cs_head_rows *k,
@@ -542,7 +644,7 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
     a.group = n_heads / cache->n_heads;
     a.sms = device_sm_count();
     Plan plan;
-    const size_t need = kControlBytes + tree_scratch(a.c.batch, a.c.cap, a.c.d, a.group, n, a.sms, static_cast<char *>(ws) + kControlBytes, &plan);
+    const size_t need = kControlBytes + tree_scratch(a.c.batch, a.c.heads, a.c.cap, a.c.d, n_heads, n, a.sms, static_cast<char *>(ws) + kControlBytes, &plan);
     st = check_qws(ws, ws_bytes, need, who);
     if (st != CS_OK) return st;
     a.n = n;
@@ -553,6 +655,14 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
     a.n_new = n_new;
     a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)cache->d_head);
     a.err = static_cast<uint32_t *>(ws);
+    if (a.group * n <= kFewRows) {
+        if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16 + 32) >= INT32_MAX) {
+            set_error("%s: batch x n_heads x capacity is too large", who);
+            return CS_ERR_UNSUPPORTED;
+        }
+        const cudaError_t e = run_few(a, static_cast<char *>(ws) + kControlBytes, (cudaStream_t)stream);
+        return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
+    }
     auto go = [&](auto run) { return run(a, plan, (cudaStream_t)stream); };
     const bool h = q->dtype == CS_F16;
     const cudaError_t e = a.c.d == 64 ? (h ? go(run_tree<64, false>) : go(run_tree<64, true>))

@@ -566,7 +566,7 @@ cs_status cs_qcache_trim(const cs_qcache *src, const int32_t *length, int keep, 
  *   dst: a cache of the same n_heads and d_head, with weights (positions) if and
  *      only if src has them, and memory of its own; or NULL (or src): in place,
  *      as if all were read before any is written, so that sequences may change
- *      places.
+ *      places (batch x d_head at most 458,752, else CS_ERR_UNSUPPORTED).
  */
 cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int32_t *length, const cs_qcache *dst,
                          void *ws, size_t ws_bytes, cs_stream_t stream);
