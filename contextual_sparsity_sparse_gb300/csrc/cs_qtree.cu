@@ -297,7 +297,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
             }
         }
     } else if (warp < 8 + kMakers) {
-        const int chunk = lane % CH, in_unit = lane / CH, c0 = (chunk & 1) * 4;
+        // a thread's chunk and slot: 8 threads side by side, which store together, have chunks of the same 64 channels in 4 slots,
+        // so that their 16 bytes lie in different banks
+        const int chunk = CH == 2 ? lane & 1 : (lane & 1) | (lane >> 2 & 2), in_unit = CH == 2 ? lane >> 1 : (lane >> 1 & 3) | (lane >> 2 & 4);
+        const int c0 = (chunk & 1) * 4;
         uint32_t it = 0, cached = 0, tiles = 0, works = 0, units = warp - 8;   // units: until this warp's next one
         bool ok = true;
         for (int i = 0; ok; ++i) {
@@ -350,8 +353,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 } else {
                     ++cached;
                     const int left = w.n_k - j * kTile;
-                    // the words of a chunk in an order that keeps 8 lanes' stores in different banks
-                    const bool swap = D == 128 && (chunk & 2);
 #pragma unroll 1
                     for (; units < C::UNITS; units += kMakers) {
                         const int r0 = units * C::ROWS + in_unit, mine = units * C::ROWS + (lane & (C::ROWS - 1));
@@ -377,8 +378,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                             // a slot that is not there may hold anything: its value counts with 0 (and its key's scores are not looked at)
                             if (value && !(bits >> (in_unit + i * (C::ROWS / 2)) & 1u)) sz[i] = 0;
                             const __half2 hz = u2h(sz[i]), s = __low2half2(hz), z = __high2half2(hz);
-                            const uint32_t word[4] = {swap ? cw[i].z : cw[i].x, swap ? cw[i].w : cw[i].y, swap ? cw[i].x : cw[i].z,
-                                                      swap ? cw[i].y : cw[i].w};
+                            const uint32_t word[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w}, at = to + chunk_at(r, c0);
                             uint32_t v[4][4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) decode8(word[k], s, z, v[k]);
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                                     for (int e = 0; e < 4; ++e) v[k][e] = h2u(__hmin2(u2h(v[k][e]), __float2half2_rn(65504.f)));
                             }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) sts16(to + chunk_at(r, c0 + (swap ? k ^ 2 : k)), v[k]);
+                            for (int k = 0; k < 4; ++k) sts16(at ^ (k << 4), v[k]);   // chunk c0 + k, as c0 is 0 or 4
                         }
                     }
                     fence_async();
