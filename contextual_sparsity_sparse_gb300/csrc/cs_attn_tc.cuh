@@ -39,7 +39,7 @@ constexpr int kTile = 128;            // rows of a row tile, keys of a step
 constexpr int kPair = 2 * kTile;      // rows of a pair
 constexpr int kBlock = 16384;         // bytes of 128 rows x 64 channels of 16 bits
 constexpr float kLead = 8.f;
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull;   // a wait that is never over is given up then
 constexpr int kTmemCols = 512;        // S_0, S_1 (128 each), O_0, O_1 (d each)
 constexpr int kParts = 2;             // P is handed over in halves of a key tile
 

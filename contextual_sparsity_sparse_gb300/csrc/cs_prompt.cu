@@ -147,6 +147,7 @@ __device__ __noinline__ void prompt_row(const PromptK &a, int token, int head, i
         x[i] = a.scale < 0.f ? -(float)q[lane + 32 * i] : (float)q[lane + 32 * i];
         o[i] = 0.f;
     }
+#pragma unroll 4
     for (int64_t j = j0; j < j1; ++j) {
         float s = 0.f;
 #pragma unroll

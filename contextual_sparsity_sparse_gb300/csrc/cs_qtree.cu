@@ -41,6 +41,8 @@ struct TreeK {
 // Drafted rows as the cache would take them: within fp16's range, NaN as 0.
 __device__ __forceinline__ float as_drafted(float x) { return x != x ? 0.f : fminf(fmaxf(x, -65504.f), 65504.f); }
 
+__device__ __forceinline__ float half_drafted(float x) { return __half2float(__float2half_rn(as_drafted(x))); }
+
 __device__ __forceinline__ int tree_count(const TreeK &a, int b) {
     if (!a.n_new) return a.n;
     const int n = ld_dep(a.n_new + b);
@@ -506,8 +508,8 @@ __global__ void __launch_bounds__(256) tree_path_kernel(TreeK a, const float *ca
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const int ch = lane + 32 * i;
-                s = fmaf(x[i], as_drafted(q_load1(a.k, b * a.k.ldb + u * a.k.ldt + h * a.k.ldh + ch)), s);
-                v[i] = as_drafted(q_load1(a.v, b * a.v.ldb + u * a.v.ldt + h * a.v.ldh + ch));
+                s = fmaf(x[i], half_drafted(q_load1(a.k, b * a.k.ldb + u * a.k.ldt + h * a.k.ldh + ch)), s);
+                v[i] = half_drafted(q_load1(a.v, b * a.v.ldb + u * a.v.ldt + h * a.v.ldh + ch));
             }
             int next = u - 1;
             if (a.parent) {

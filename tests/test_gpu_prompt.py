@@ -201,3 +201,42 @@ def test_same_bits_again_captured_and_on_another_stream():
 @pytest.mark.parametrize("dt", DTS)
 def test_long_prompt(dt):
     check(*make([3001, 1500], [3001, 1500], 8, 1, 128, dt), [3001, 1500])
+
+
+def test_what_is_not_seen_has_no_influence_where_keys_are_cut():
+    """The same with records of pieces: few rows over many keys, NaN in the last values, which only the last row sees."""
+    q_lens, k_lens = [5], [20000]
+    q, k, v = make(q_lens, k_lens, 8, 1, 128, torch.bfloat16)
+    clean, _ = call(q, k, v, q_lens, k_lens)
+    v[-1] = float("nan")
+    out, _ = call(q, k, v, q_lens, k_lens)
+    want, bound = ref.prompt(q[:4], k[:-1], v[:-1], [4], [19999])
+    assert ((out[:4].double() - want).abs() <= bound).all()
+    assert torch.isnan(out[4]).all() and not torch.isnan(clean).any()
+
+
+def test_more_starts_than_sequences_and_sizes_of_a_larger_workspace():
+    """A workspace of larger sizes serves smaller calls; the same tensors, other sequences."""
+    q, k, v = make([300], [300], 4, 2, 64, torch.float16)
+    ws = cs.PromptWorkspace(9, 8, 2, 128, 1000, 5000)
+    for lens in ([300], [0, 300], [1] * 7, [150, 150], [299, 1]):
+        n = sum(lens)
+        out, _ = call(q, k, v, lens, ws=ws)
+        want, bound = ref.prompt(q, k, v, lens, lens)
+        assert ((out[:n].double() - want[:n]).abs() <= bound[:n]).all() and (out[n:] == 7.0).all()
+    assert cs.cs_get_device_error(ws) == 0
+
+
+def test_no_query_tokens_and_no_keys():
+    ws = cs.PromptWorkspace(2, 2, 1, 64, 10, 10)
+    empty = torch.empty(0, 2, 64, dtype=torch.float16, device="cuda")
+    cs.cs_prompt_attention(empty, empty[:, :1], empty[:, :1], empty.clone(), starts([0, 0]), ws)
+    q = torch.randn(10, 2, 64, device="cuda").half()
+    out = torch.full_like(q, 7.0)
+    cs.cs_prompt_attention(q, empty[:, :1], empty[:, :1], out, starts([3, 7]), ws, k_start=starts([0, 0]))
+    assert (out == 0).all() and cs.cs_get_device_error(ws) == 0
+
+
+def test_heads_of_every_group_up_to_128():
+    for group in (2, 3, 4, 6, 9, 10, 11, 13, 24, 31, 33, 43, 64, 100):
+        check(*make([6, 70], [6, 70], group, 1, 64, torch.bfloat16, seed=group), [6, 70])

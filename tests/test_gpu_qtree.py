@@ -227,3 +227,44 @@ def test_a_chain_sees_what_appended_tokens_see():
     cs.cs_qcache_attention(cache, q.cuda(), ints([154]), out, ws, q_pos=ints([150]))
     _, bound = ref.tree(*cpu[:4], None, q, k, v, [150])
     assert ((tree.double() - out.double()).abs().cpu() <= 3 * bound).all()
+
+
+@pytest.mark.parametrize("H,kv,n", [(8, 8, 16), (8, 8, 17), (8, 1, 2), (8, 1, 3), (16, 1, 1), (17, 1, 1), (6, 2, 5), (6, 2, 6)])
+@pytest.mark.parametrize("dt", DTS)
+def test_on_both_sides_of_few_rows(H, kv, n, dt):
+    """Rows of a cache head up to and past what the kernels of single tokens take, over a ragged batch with an empty sequence."""
+    g = gen(H, kv, n, 18)
+    cache, cpu = filled(4, kv, 700, 128, g)
+    cpu[5][torch.rand(4, kv, 700, generator=g) < 0.05] = -1
+    cache.pos.copy_(cpu[5])
+    check(cpu, cache, *drafts(4, n, H, kv, 128, dt, g), torch.tensor([700, 0, 129, 1]), parents(4, n, g), torch.tensor([n, n, max(n - 1, 0), n]))
+
+
+def test_a_workspace_of_larger_sizes_serves_smaller_calls():
+    g = gen(19)
+    cache, cpu = filled(2, 2, 300, 64, g)
+    ws = cs.QCacheTreeWorkspace(cache, 16, 64)
+    for H, n in ((16, 64), (2, 1), (4, 8), (16, 2), (2, 64), (8, 4), (4, 5)):
+        q, k, v = drafts(2, n, H, 2, 64, torch.float16, g)
+        out, _ = run(cache, q, k, v, [300, 77], ws=ws)
+        want, bound = ref.tree(*cpu[:4], cpu[5], q, k, v, [300, 77])
+        assert ((out.cpu().double() - want).abs() <= bound).all()
+    assert cs.cs_get_device_error(ws) == 0
+
+
+def test_long_chains_and_deep_trees():
+    g = gen(20)
+    cache, cpu = filled(1, 1, 40, 64, g)
+    q, k, v = drafts(1, 128, 2, 1, 64, torch.bfloat16, g)
+    check(cpu, cache, q, k, v, torch.tensor([40]))
+    check(cpu, cache, q, k, v, torch.tensor([40]), torch.arange(-1, 127, dtype=torch.int32)[None])
+    check(cpu, cache, q, k, v, torch.tensor([0]), torch.full((1, 128), -1, dtype=torch.int32))
+
+
+def test_scales_and_negative_scales():
+    g = gen(21)
+    cache, cpu = filled(1, 2, 200, 128, g)
+    for H, n in ((4, 2), (4, 20)):
+        q, k, v = drafts(1, n, H, 2, 128, torch.float16, g)
+        for scale in (0.03, -0.05):
+            check(cpu, cache, q, k, v, torch.tensor([200]), parents(1, n, g), scale=scale)
