@@ -207,7 +207,7 @@ __device__ __forceinline__ Work load_work(const Work *w) {
     return r;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;   // (1,024 took 1.3 us longer, for their barriers)
 constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in records than they win
 
 // Lists the works of `pairs` pairs of row tiles for kv heads: those of many key tiles first, cut along the keys so that no
