@@ -681,7 +681,7 @@ __device__ __forceinline__ int last_piece(Bars<STAGES> &b, unsigned *arrived, in
     return last;
 }
 
-// A row's sums over its pieces: 1 / l in l, and put(i, o) for every 32 channels.
+// A row's outputs from its pieces (0: zeros), put(i, o) for every 32 channels.
 template <int D, typename Put>
 __device__ __forceinline__ void join_pieces(const float *rec, int pieces, int row, float c, Put put) {
     float m = -INFINITY, l = 0.f;
@@ -708,14 +708,40 @@ __device__ __forceinline__ void join_pieces(const float *rec, int pieces, int ro
     }
 }
 
-// 32 values of a row as 16 bits, its start on a 16-byte boundary.
+// Rows of 16-bit outputs, a thread's row in 32 channels at a time, written by the warp in lines: 64 channels of its 32 rows
+// go through 4 KB of shared memory.  (Threads that store their own rows take a line for every 16 bytes: 5,000 cycles a
+// work, and as many until the loads behind them come through.)
 template <bool BF16>
-__device__ __forceinline__ void store32(char *at, const float *v) {
+struct RowWriter {
+    uint32_t at;       // the warp's shared memory
+    char *row;         // where this thread's row goes
+    uint32_t valid;    // the warp's rows that are written
+
+    __device__ __forceinline__ RowWriter(uint32_t at, char *row, bool valid) : at(at), row(row), valid(__ballot_sync(kFull, valid)) {}
+
+    // Channels 32 i .. of all rows; the whole warp.
+    __device__ __forceinline__ void put(int i, const float *v) {
+        const int lane = threadIdx.x & 31, c0 = (i & 1) * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<uint4 *>(at)[i] = make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]), pack2<BF16>(v[8 * i + 2], v[8 * i + 3]),
-                                                      pack2<BF16>(v[8 * i + 4], v[8 * i + 5]), pack2<BF16>(v[8 * i + 6], v[8 * i + 7]));
-}
+        for (int c = 0; c < 4; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4)),
+                         "r"(pack2<BF16>(v[8 * c], v[8 * c + 1])), "r"(pack2<BF16>(v[8 * c + 2], v[8 * c + 3])),
+                         "r"(pack2<BF16>(v[8 * c + 4], v[8 * c + 5])), "r"(pack2<BF16>(v[8 * c + 6], v[8 * c + 7]))
+                         : "memory");
+        if (!(i & 1)) return;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + lane / 8, c = lane & 7;
+            char *to = reinterpret_cast<char *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(row), r));
+            uint4 x;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                         : "r"(at + r * 128 + ((c ^ (r & 7)) << 4)) : "memory");
+            if (valid >> r & 1u) *reinterpret_cast<uint4 *>(to + 64 * (i - 1) + 16 * c) = x;
+        }
+        __syncwarp();
+    }
+};
 
 }  // namespace
 

@@ -121,8 +121,9 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Pl
 template <int D>
 struct PromptCfg {
     static constexpr int DB = D / 64;
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr size_t smem = (size_t)(2 + STAGES) * DB * kBlock + 1024;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int OUT = 4096;   // of each row warp, for its outputs
+    static constexpr size_t smem = (size_t)(2 + STAGES) * DB * kBlock + 8 * OUT + 1024;
 };
 
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int c, int h, int row, uint64_t *bar) {
@@ -230,6 +231,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     __stcg(my, r.m);
                     __stcg(my + kPair, r.l);
                 }
+                RowWriter<BF16> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
                 float odd = r.l * 0.f;   // NaN, if anything is not finite
 #pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
@@ -242,10 +244,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
 #pragma unroll
                             for (int e = 0; e < 32; ++e) __stcg(my + (2 + 32 * b + e) * kPair, o[e]);
                         }
-                    } else if (valid) {
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= inv;
-                        store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o);
+                        writer.put(b, o);
                     }
                 }
                 uint32_t again = __ballot_sync(kFull, valid && sums.some && !(odd == 0.f));
@@ -272,9 +274,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             if (rec) {
                 const int last = last_piece(bars, plan.arrived + h * recs + w.rec, w.pieces, &flag, r.n_rec++, a.err);
                 if (last < 0) break;
-                if (last && valid && mine)
-                    join_pieces<D>(rec, w.pieces, rt * kTile + row, c,
-                                   [&](int b, const float *o) { store32<BF16>(reinterpret_cast<char *>(out + 32 * b), o); });
+                if (last && mine) {
+                    RowWriter<BF16> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
+                    join_pieces<D>(rec, valid ? w.pieces : 0, rt * kTile + row, c, [&](int b, const float *o) { writer.put(b, o); });
+                }
             }
         }
     } else if (warp == 8) {

@@ -243,16 +243,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
             Sums sums;
             if (!join_streams(r, st, t, sh.bars, sh.stat, c, sums, a.err)) break;
             const bool mine = !(w.narrow && t == 1);   // whose rows these are
+            // a row tile's q has been read when its outputs are there: its memory takes them on their way
+            const int64_t to = w.seq * a.out.ldb + token * a.out.ldt + (int64_t)head * a.out.ldh;
+            RowWriter<BF16> writer(q_at + rt * C::DB * kBlock + (warp & 3) * 4096, a.out.p + 2 * to, there);
             auto put = [&](int b, const float *o) {
-                const int64_t to = w.seq * a.out.ldb + token * a.out.ldt + (int64_t)head * a.out.ldh + 32 * b;
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = o[(e & ~7) + (e & 3) * 2 + (e >> 2 & 1)];
                 if (a.out.vec) {
-                    store32<BF16>(a.out.p + 2 * to, v);
-                } else {
+                    writer.put(b, v);
+                } else if (there) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) q_store1(a.out, to + e, v[e]);
+                    for (int e = 0; e < 32; ++e) q_store1(a.out, to + 32 * b + e, v[e]);
                 }
             };
             float *rec = w.pieces > 1 ? plan.rec + (int64_t)(h * recs + w.rec) * rec_floats(D) : nullptr;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
 #pragma unroll
                             for (int e = 0; e < 32; ++e) __stcg(my + (2 + 32 * b + e) * kPair, o[e]);
                         }
-                    } else if (there) {
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = valid ? o[e] * inv : 0.f;
                         put(b, o);
@@ -288,14 +290,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
             if (rec) {
                 const int last = last_piece(sh.bars, plan.arrived + h * recs + w.rec, w.pieces, &sh.flag, r.n_rec++, a.err);
                 if (last < 0) break;
-                if (last && mine && there) {
-                    if (valid) {
-                        join_pieces<D>(rec, w.pieces, rt * kTile + row, c, put);
-                    } else {
-                        const float zero[32] = {};
-                        for (int b = 0; b < D / 32; ++b) put(b, zero);
-                    }
-                }
+                if (last && mine)
+                    join_pieces<D>(rec, valid ? w.pieces : 0, rt * kTile + row, c, put);
             }
         }
     } else if (warp < 8 + kMakers) {
