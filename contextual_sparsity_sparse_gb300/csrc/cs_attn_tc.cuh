@@ -708,10 +708,20 @@ __device__ __forceinline__ void join_pieces(const float *rec, int pieces, int ro
     }
 }
 
-// Rows of 16-bit outputs, a thread's row in 32 channels at a time, written by the warp in lines: 64 channels of its 32 rows
-// go through 4 KB of shared memory.  (Threads that store their own rows take a line for every 16 bytes: 5,000 cycles a
-// work, and as many until the loads behind them come through.)
+// 32 values of a row as 16 bits, its start on a 16-byte boundary.
 template <bool BF16>
+__device__ __forceinline__ void store32(char *at, const float *v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4 *>(at)[i] = make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]), pack2<BF16>(v[8 * i + 2], v[8 * i + 3]),
+                                                      pack2<BF16>(v[8 * i + 4], v[8 * i + 5]), pack2<BF16>(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// Rows of 16-bit outputs, a thread's row in 32 channels at a time.  Written by the warp in lines: 64 channels of its 32 rows
+// go through 4 KB of shared memory (threads that store rows of 128 channels themselves take a line for every 16 bytes: 5,000
+// cycles a work, and as many until the loads behind them come through).  Few rows, or rows of 64 channels (LINES false; 8,192
+// tokens of 16 heads 156 us, 165 in lines), are stored as they are.
+template <bool BF16, bool LINES>
 struct RowWriter {
     uint32_t at;       // the warp's shared memory
     char *row;         // where this thread's row goes
@@ -722,6 +732,10 @@ struct RowWriter {
     // Channels 32 i .. of all rows; the whole warp.
     __device__ __forceinline__ void put(int i, const float *v) {
         const int lane = threadIdx.x & 31, c0 = (i & 1) * 4;
+        if (!LINES || __popc(valid) <= 8) {
+            if (valid >> lane & 1u) store32<BF16>(row + 64 * i, v);
+            return;
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4)),

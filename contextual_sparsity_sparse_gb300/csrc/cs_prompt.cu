@@ -122,7 +122,7 @@ template <int D>
 struct PromptCfg {
     static constexpr int DB = D / 64;
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int OUT = 4096;   // of each row warp, for its outputs
+    static constexpr int OUT = D == 128 ? 4096 : 0;   // of each row warp, for its outputs
     static constexpr size_t smem = (size_t)(2 + STAGES) * DB * kBlock + 8 * OUT + 1024;
 };
 
@@ -231,7 +231,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     __stcg(my, r.m);
                     __stcg(my + kPair, r.l);
                 }
-                RowWriter<BF16> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
+                RowWriter<BF16, D == 128> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
                 float odd = r.l * 0.f;   // NaN, if anything is not finite
 #pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
@@ -275,7 +275,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const int last = last_piece(bars, plan.arrived + h * recs + w.rec, w.pieces, &flag, r.n_rec++, a.err);
                 if (last < 0) break;
                 if (last && mine) {
-                    RowWriter<BF16> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
+                    RowWriter<BF16, D == 128> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
                     join_pieces<D>(rec, valid ? w.pieces : 0, rt * kTile + row, c, [&](int b, const float *o) { writer.put(b, o); });
                 }
             }

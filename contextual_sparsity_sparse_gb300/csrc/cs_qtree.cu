@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
             const bool mine = !(w.narrow && t == 1);   // whose rows these are
             // a row tile's q has been read when its outputs are there: its memory takes them on their way
             const int64_t to = w.seq * a.out.ldb + token * a.out.ldt + (int64_t)head * a.out.ldh;
-            RowWriter<BF16> writer(q_at + rt * C::DB * kBlock + (warp & 3) * 4096, a.out.p + 2 * to, there);
+            RowWriter<BF16, D == 128> writer(q_at + rt * C::DB * kBlock + (warp & 3) * 4096, a.out.p + 2 * to, there);
             auto put = [&](int b, const float *o) {
                 float v[32];
 #pragma unroll
