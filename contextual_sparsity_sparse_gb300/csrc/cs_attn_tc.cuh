@@ -25,6 +25,17 @@
 // Work that is cut along the keys leaves records (each row's m, sum of p and
 // sums of p v, in 32 bits); the CTA that finishes the last piece of a work
 // adds them up in the pieces' order, whoever comes last.
+//
+// Bound (8,192 tokens, 64 over 8 heads of 128, causal, bf16: 690 us, 1,590
+// TFLOP/s): a pair of key tile and row tiles takes 2,800 cycles, of which the products need 2,048.  A
+// stream's next scores come 1,000 to 1,300 cycles after its last P (the product with V 512, the scores 512, barriers),
+// and a row's work on 128 scores takes 1,450 (the maximum 480, P 900; exponentials at 4 cycles a warp 512).  Products with both
+// operands in shared memory take all of its bandwidth, so every barrier and load costs 100 to 200 cycles beside them.
+// Tried and not kept (packed prompts of up to 5,000 tokens, 64 over 8 heads, about 1,590 us then): a warp for
+// each stream's products 2,111 instead of 1,708; P in one or four parts 1,764 and 1,957 instead of 1,718;
+// a warpgroup of its own for the outputs, with 128 registers for the rows, 1,668 instead of 1,582; masked
+// tiles 32 keys at a time 1,668 instead of 1,590; works placed by half a tile's cost for narrow ones, no gain;
+// outputs' loads from tensor memory ahead of their use 1,597 instead of 1,574.
 #pragma once
 
 #include <cuda.h>
@@ -242,7 +253,7 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
     }
     __syncthreads();
     // with a pair's pieces fewer than twice its tiles / chunk, all pieces of cut pairs are fewer than 2 SMs' number
-    const int chunk = (int)max((unsigned long long)kLeastPiece, (units * kv + sms - 1) / sms);
+    const int chunk = (int)min((unsigned long long)INT_MAX, max((unsigned long long)kLeastPiece, (units * kv + sms - 1) / sms));
     const int big = min(longest, chunk);
     auto pieces_of = [&](int tiles) { return tiles > chunk && plan.recs > 0 ? (tiles + chunk - 1) / chunk : 1; };
     auto bin_of = [&](int tiles, int pieces) {
