@@ -132,3 +132,68 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert torch.equal(po, want[0]) and torch.equal(to, want[1])
     assert cs.cs_get_device_error(pws) == 0 and cs.cs_get_device_error(tws) == 0
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_offsets_past_32_bits(n):
+    """A cache of more than 2^31 bytes of keys: the last head's slots as they are in a small cache; forks and rows there, too."""
+    g = torch.Generator("cuda").manual_seed(3)
+    kv, d, cap, used = 4, 128, 5_200_000, 300
+    big = cs.QCache.empty(2, kv, cap, d)
+    small = cs.QCache.empty(1, kv, used, d)
+    for t in (small.k, small.v):
+        t.random_(0, 256, generator=g)
+    small.k_scale.uniform_(0.01, 0.1, generator=g)
+    small.v_scale.uniform_(0.01, 0.1, generator=g)
+    small.weight.uniform_(0, 1, generator=g)
+    small.pos.copy_(torch.arange(used, device="cuda"))
+    parts = ("k", "v", "k_scale", "v_scale", "weight", "pos")
+    for name in parts:
+        getattr(big, name)[1, :, :used] = getattr(small, name)[0]
+    q, k, v = (torch.randn(2, n, h, d, generator=g, device="cuda").half() for h in (2 * kv, kv, kv))
+    out, one = torch.empty_like(q), torch.empty_like(q[1:])
+    tws = cs.QCacheTreeWorkspace(big, 2 * kv, n)
+    cs.cs_qcache_tree_attention(big, q, k, v, ints([0, used]), out, tws)
+    cs.cs_qcache_tree_attention(small, q[1:], k[1:], v[1:], ints([used]), one, cs.QCacheTreeWorkspace(small, 2 * kv, n))
+    # the cut along the keys goes by the lengths, which are alike but for an empty sequence
+    assert torch.equal(out[1:], one) and cs.cs_get_device_error(tws) == 0
+    ws = cs.QCacheWorkspace(big, n_heads=0)
+    cs.cs_qcache_fork(big, ints([1, -1]), ints([0, used]), ws)
+    for name in parts:
+        assert torch.equal(getattr(big, name)[0, :, :used], getattr(small, name)[0])
+    last = cap - 2 * n
+    cs.cs_qcache_append_rows(big, k.flatten(0, 1), v.flatten(0, 1), ints([list(range(n)), list(range(n, 2 * n))]), ws,
+                             start=ints([last, last]), pos=ints([7, 9]))
+    (kc, ks), (vc, vs) = qref.quantise(k.cpu().transpose(1, 2)), qref.quantise(v.cpu().transpose(1, 2))
+    for got, want in zip((big.k, big.k_scale, big.v, big.v_scale), (kc, ks, vc, vs)):
+        assert torch.equal(got[:, :, last:last + n].cpu(), want)
+    assert (big.pos[:, :, last] == ints([7, 9])[:, None]).all() and cs.cs_get_device_error(ws) == 0
+
+
+def test_prompts_whose_rows_lie_far_apart():
+    g = torch.Generator("cuda").manual_seed(4)
+    n, kv, d, wide = 4000, 2, 64, 300_000
+    buf = torch.empty(n, wide, dtype=torch.bfloat16, device="cuda")      # 2.4 GB, of which few columns are used
+    cut = lambda h, at: buf[:, at:at + h * d].unflatten(1, (h, d))  # noqa: E731
+    q, k, v, out = cut(4, 0), cut(kv, 1024), cut(kv, wide - 1024), cut(4, 4096)
+    for t in (q, k, v):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    pws = cs.PromptWorkspace(1, 4, kv, d, n)
+    cs.cs_prompt_attention(q, k, v, out, ints([0, n]), pws)
+    dense = torch.empty(n, 4, d, dtype=torch.bfloat16, device="cuda")
+    cs.cs_prompt_attention(q.contiguous(), k.contiguous(), v.contiguous(), dense, ints([0, n]), pws)
+    assert torch.equal(out, dense) and cs.cs_get_device_error(pws) == 0
+
+
+def test_wide_groups_of_drafted_trees():
+    g = torch.Generator().manual_seed(5)
+    for heads, n in ((127, 8), (100, 10), (65, 3), (128, 1), (33, 31)):
+        x = torch.randn(1, 1, 140, 64, generator=g)
+        (kc, ks), (vc, vs) = qref.quantise(x), qref.quantise(torch.randn(1, 1, 140, 64, generator=g))
+        cache = cs.QCache(kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda())
+        q, k, v = (torch.randn(1, n, h, 64, generator=g).half() for h in (heads, 1, 1))
+        out = torch.empty_like(q, device="cuda")
+        ws = cs.QCacheTreeWorkspace(cache, heads, n)
+        cs.cs_qcache_tree_attention(cache, q.cuda(), k.cuda(), v.cuda(), ints([140]), out, ws)
+        want, bound = ref.tree(kc, ks, vc, vs, None, q, k, v, [140])
+        assert ((out.cpu().double() - want).abs() <= bound).all() and cs.cs_get_device_error(ws) == 0
