@@ -495,6 +495,42 @@ constexpr float kShift = BF16 ? 0.f : 7.f;
 // What the rows of a warp see of a key tile: all of it, all the same keys, or each row keys of its own.
 enum Sight { SEE_ALL, SEE_SAME, SEE_OWN };
 
+// What is done to some tiles' scores in tensor memory stands out of the loop over tiles, whose code the warps of two streams
+// and of the other roles fetch side by side.
+//
+// Keys that nobody sees are columns, most often few: written over one by one (128 selections in the loop and their way back
+// to tensor memory took 1,400 cycles of a tile's 5,300).  w: the keys that are seen.
+__device__ __noinline__ void hide_columns(uint32_t s_at, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t out = ~(i == 0 ? w0 : i == 1 ? w1 : i == 2 ? w2 : w3);
+        if (out == kFull) {
+            float none[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) none[e] = -INFINITY;
+            tm_st32(s_at + 32 * i, none);
+        } else {
+            for (uint32_t b = out; b; b &= b - 1) tm_st1(s_at + 32 * i + __ffs(b) - 1, -INFINITY);
+        }
+    }
+    tm_wait_st();
+}
+// What this row does not see becomes -inf; for a negative scale, all scores are negated.
+__device__ __noinline__ void hide_scores(uint32_t s_at, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, bool all, bool neg) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mine = all ? kFull : i == 0 ? w0 : i == 1 ? w1 : i == 2 ? w2 : w3;
+        if (!neg && __all_sync(kFull, mine == kFull)) continue;
+        float x[32];
+        tm_ld32(s_at + 32 * i, x);
+        tm_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = mine >> e & 1u ? (neg ? -x[e] : x[e]) : -INFINITY;
+        tm_st32(s_at + 32 * i, x);
+    }
+    tm_wait_st();
+}
+
 // Stream t's key tiles first, first + step, ... below end: its rows' statistics in r, their sums of p v in tensor memory.
 // mask(j, w): what the warp's rows see of tile j, and unless it is all the bits of those keys.
 // CK: scores read at a time (16: fewer registers).
@@ -512,23 +548,8 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
         if (!wait_warp(&b.s_full[t], r.n_s & 1, err)) return false;
         ++r.n_s;
         tc_after();
-        if (sight == SEE_SAME && !neg) {
-            // keys that nobody sees are columns, most often few: written over one by one (128 selections and their way back to
-            // tensor memory took 1,400 cycles of a tile's 5,300)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t out = ~w[i];
-                if (out == kFull) {
-                    float none[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) none[e] = -INFINITY;
-                    tm_st32(s_at + 32 * i, none);
-                } else {
-                    for (uint32_t b = out; b; b &= b - 1) tm_st1(s_at + 32 * i + __ffs(b) - 1, -INFINITY);
-                }
-            }
-            tm_wait_st();
-        }
+        if (sight == SEE_SAME && !neg) hide_columns(s_at, w[0], w[1], w[2], w[3]);
+        else if (sight != SEE_ALL || neg) hide_scores(s_at, w[0], w[1], w[2], w[3], sight == SEE_ALL, neg);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < kTile; i += 64) {
@@ -536,18 +557,11 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
             tm_ld32(s_at + i, x);
             tm_ld32(s_at + i + 32, x + 32);
             tm_wait_ld();
-            if (sight == SEE_OWN || neg) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] = sight != SEE_ALL && !(w[(i + e) / 32] >> e % 32 & 1u) ? -INFINITY : neg ? -x[e] : x[e];
-                tm_st32(s_at + i, x);
-                tm_st32(s_at + i + 32, x + 32);
-            }
 #pragma unroll
             for (int e = 0; e < 64; e += 8)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], x[e + 4 + q]);
         }
-        if (sight == SEE_OWN || neg) tm_wait_st();
         constexpr int N = kTile / CK;
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (__any_sync(kFull, top > lead)) {
