@@ -201,7 +201,7 @@ struct Work {
 static_assert(sizeof(Work) == 48, "three 16-byte loads");
 
 struct Plan {
-    int *count;          // [0] works, [1] records of a head, [2] records that are planned so far
+    int *count;          // [0] works, [1] records of a head
     Work *work;
     unsigned *arrived;   // [records] finished pieces, by the first record's place
     float *rec;          // [records] per row m and l, then [d][256] sums of p v
@@ -755,12 +755,19 @@ struct RowWriter {
     __device__ __forceinline__ RowWriter(uint32_t at, char *row, bool valid) : at(at), row(row), valid(__ballot_sync(kFull, valid)) {}
 
     // Channels 32 i .. of all rows; the whole warp.
-    __device__ __forceinline__ void put(int i, const float *v) {
-        const int lane = threadIdx.x & 31, c0 = (i & 1) * 4;
-        if (!LINES || __popc(valid) <= 8) {
-            if (valid >> lane & 1u) store32<BF16>(row + 64 * i, v);
-            return;
+    __device__ __forceinline__ void put(int i, const float *v) const {
+        if constexpr (LINES) {
+            if (__popc(valid) > 8) {
+                put_lines(i, v);
+                return;
+            }
         }
+        if (valid >> (threadIdx.x & 31) & 1u) store32<BF16>(row + 64 * i, v);
+    }
+
+private:
+    __device__ __forceinline__ void put_lines(int i, const float *v) const {
+        const int lane = threadIdx.x & 31, c0 = (i & 1) * 4;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4)),

@@ -575,11 +575,13 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
  * Attention for a tree of drafted tokens over the cache, before any of them is in
  * it.  Sequence b has n drafted tokens (its first n_new[b], if n_new is given);
  * parent[b, t] ([batch, n] int32 device) is the token that token t continues, a
- * lower one, or -1: the last one in the cache.  Without parents (NULL) every token continues the one before it.
- * With keys and values of the slots and of the drafted tokens,
+ * lower one, or -1: the last one in the cache.  Without parents (NULL) every
+ * token continues the one before it.  With keys and values of the slots and of
+ * the drafted tokens,
  *     s_i = scale q . k_i,  p = softmax(s),  out = sum_i p_i v_i,
- * over the slots i < length[b] (clamped to [0, capacity], CS_DEVERR_COUNT) that are not
- * empty (pos < 0, if the cache has positions), the token's ancestors in the tree, and the token itself.
+ * over the slots i < length[b] (clamped to [0, capacity], CS_DEVERR_COUNT) that
+ * are not empty (pos < 0, if the cache has positions), the token's ancestors in
+ * the tree, and the token itself.
  *   q, out: n tokens of n_heads heads;  k, v: n tokens of cache->n_heads heads;
  *      all of one dtype, fp16 or bf16.  Query head h reads cache head
  *      h / (n_heads / cache->n_heads).  out is none of the inputs.
@@ -587,10 +589,13 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
  *      Tokens from n_new[b] on give zeros and are not seen.
  * A parent outside [-1, t) counts as -1 and sets CS_DEVERR_INDEX.  Drafted rows count
  * as fp16 values, as the cache would take them: clamped to +-65504, NaN as 0.
- * 1 <= n <= 128, n x n_heads / cache->n_heads <= 1024; d_head 64 or 128.  Slots'
- * values are rounded to fp16 for the products, q (by row and power of two) likewise; sums and softmax
- * statistics are fp32.  The cache, its weights among it, is not changed.
- * With the same arguments the results are the same bit for bit.
+ * 1 <= n <= 128, n_heads / cache->n_heads <= 128, n x n_heads / cache->n_heads
+ * <= 1024; d_head 64 or 128.  Slots' values go into the products as fp16, q
+ * likewise (by row, times a power of two), or finer; sums and softmax statistics
+ * are fp32.  The cache, its weights among it, is not changed.  With the same
+ * arguments the results are the same bit for bit.
+ * The workspace (on the current device; initialised once with cs_workspace_init)
+ * serves calls of up to these sizes.
  */
 size_t cs_qcache_tree_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n);
 cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q, const cs_head_rows *k,
@@ -616,9 +621,11 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
  *      q_start (then k_total must be q_total).  Values outside [0, total], and
  *      falling ones, are clamped and set CS_DEVERR_COUNT.
  *   scale: the factor on q . k; 0 means 1 / sqrt(d_head).
- * d_head is 64 or 128; batch <= 4096, n_heads <= 1024, n_heads / kv_heads <= 128.  Sums and softmax statistics are
- * fp32; the weights go into the value products in the inputs' type.  With the
- * same arguments the results are the same bit for bit.
+ * d_head is 64 or 128; batch <= 4096, n_heads <= 1024, n_heads / kv_heads <=
+ * 128, tokens <= 2^24.  Sums and softmax statistics are fp32; the weights go into
+ * the value products in the inputs' type.  With the same arguments the results
+ * are the same bit for bit.  The workspace (on the current device; initialised
+ * once with cs_workspace_init) serves calls of up to these sizes.
  */
 size_t cs_prompt_workspace_size(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total);
 cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, const cs_head_rows *v, int n_heads,
