@@ -488,9 +488,9 @@ struct RowState {
 };
 
 // fp16's p are taken 2^7 larger, so that those of 2^-31 of the largest are still there: with m following
-// the maximum by 2^8 they stay below 2^16.  bf16 has fp32's range.
+// the maximum by 2^8 they stay below 2^16.  bf16 has fp32's range: taken 2^32 smaller, 2^24 of them times any v stay in it.
 template <bool BF16>
-constexpr float kShift = BF16 ? 0.f : 7.f;
+constexpr float kShift = BF16 ? -32.f : 7.f;
 
 // What the rows of a warp see of a key tile: all of it, all the same keys, or each row keys of its own.
 enum Sight { SEE_ALL, SEE_SAME, SEE_OWN };

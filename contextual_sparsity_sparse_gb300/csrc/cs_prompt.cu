@@ -13,8 +13,8 @@
 //
 // A product with V adds p v for all 128 keys of a tile, and p = 0 does not undo a
 // NaN or infinity in a v that a row does not see.  Such rows end up not finite,
-// which is looked for when they are written: they are worked out again, key by
-// key, from what they see alone.
+// which is looked for when they are written: the channels that this can be the
+// reason for are worked out again, key by key, from what the row sees alone.
 #include "cs_attn_tc.cuh"
 
 namespace cs {
@@ -132,35 +132,63 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int
                  : "memory");
 }
 
-// One row by one warp, key by key, of keys [j0, j1): lane l has channels l + 32 i of o, the sums of p v.
+// One row by one warp, key by key: of the keys [j0, j1) the row sees those below lim, and m and l are its statistics.  Only
+// channels in which some value that it does not see is not finite are worked out: the products leave the others right, also
+// where what it does see is not finite.  Lane l has channels N l .. of o, the sums of p v; returns which of them these are
+// (bits), 0 if the warp has none.  The keys go backwards, until every such channel has met something that is not finite and
+// that the row does see: where values are bad throughout, that is at the first step.  (16,384 tokens of 8 heads of 128:
+// 0.4 ms, with values all NaN 1.6.)
 template <typename T, int D>
-__device__ __noinline__ void prompt_row(const PromptK &a, int token, int head, int64_t k0, int j0, int j1, float c, float shift, float &m,
-                                        float &l, float (&o)[D / 32]) {
-    const int lane = threadIdx.x & 31;
-    const T *q = reinterpret_cast<const T *>(a.q.p) + token * a.q.ldt + head * a.q.ldh;
-    const T *k = reinterpret_cast<const T *>(a.k.p) + k0 * a.k.ldt + head / a.group * a.k.ldh;
-    const T *v = reinterpret_cast<const T *>(a.v.p) + k0 * a.v.ldt + head / a.group * a.v.ldh;
-    float x[D / 32];
-    m = -INFINITY;
-    l = 0.f;
+__device__ __noinline__ uint32_t prompt_row(const PromptK &a, int token, int head, int64_t k0, int j0, int j1, int lim, float c, float m,
+                                            float shift, float (&o)[D / 32]) {
+    constexpr int N = D / 32, STEP = 8;
+    struct alignas(2 * N) Vec {
+        T x[N];
+    };
+    const int ch = N * (threadIdx.x & 31);
+    const T *q = reinterpret_cast<const T *>(a.q.p) + token * a.q.ldt + head * a.q.ldh + ch;
+    const T *k = reinterpret_cast<const T *>(a.k.p) + k0 * a.k.ldt + head / a.group * a.k.ldh + ch;
+    const T *v = reinterpret_cast<const T *>(a.v.p) + k0 * a.v.ldt + head / a.group * a.v.ldh + ch;
+    uint32_t bad = 0;
+    const int64_t stop = min((int64_t)j1, a.k_total - k0);   // behind it there are zeros
+    for (int64_t j = max(j0, lim); j < stop; ++j) {
+        const Vec y = *reinterpret_cast<const Vec *>(v + j * a.v.ldt);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        x[i] = a.scale < 0.f ? -(float)q[lane + 32 * i] : (float)q[lane + 32 * i];
+        for (int i = 0; i < N; ++i) bad |= (uint32_t)!isfinite((float)y.x[i]) << i;
+    }
+    if (!__any_sync(kFull, bad)) return 0;
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = a.scale < 0.f ? -(float)q[i] : (float)q[i];
         o[i] = 0.f;
     }
-#pragma unroll 4
-    for (int64_t j = j0; j < j1; ++j) {
-        float s = 0.f;
+    const float add = shift - (m == -INFINITY ? 0.f : m) * c;
+    for (int64_t end = min(j1, lim); end > j0; end -= STEP) {
+        Vec kk[STEP], vv[STEP];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) s = fmaf(x[i], (float)k[j * a.k.ldt + lane + 32 * i], s);
-        s = warp_sum(s);
-        const float up = fmaxf(m, s), base = up == -INFINITY ? 0.f : up;
-        const float keep = m == -INFINITY ? 0.f : exp2f((m - base) * c), p = exp2f((s - base) * c + shift);
-        m = up;
-        l = fmaf(l, keep, p);
+        for (int e = 0; e < STEP; ++e) {
+            const int64_t j = max(end - 1 - e, (int64_t)j0);
+            kk[e] = *reinterpret_cast<const Vec *>(k + j * a.k.ldt);
+            vv[e] = *reinterpret_cast<const Vec *>(v + j * a.v.ldt);
+        }
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], keep, p * (float)v[j * a.v.ldt + lane + 32 * i]);
+        for (int e = 0; e < STEP; ++e) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) s = fmaf(x[i], (float)kk[e].x[i], s);
+            const float p = exp2f(fmaf(warp_sum(s), c, add));
+            if (end - 1 - e >= j0) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) o[i] = fmaf(p, (float)vv[e].x[i], o[i]);
+            }
+        }
+        uint32_t left = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) left |= (uint32_t)(bad >> i & isfinite(o[i])) << i;
+        if (!__any_sync(kFull, left)) break;
     }
+    return bad;
 }
 
 template <int D, bool BF16>
@@ -232,7 +260,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                     __stcg(my + kPair, r.l);
                 }
                 RowWriter<BF16, D == 128> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
-                float odd = r.l * 0.f;   // NaN, if anything is not finite
+                float odd = 0.f;   // NaN, if anything is not finite
 #pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
                     float o[32];
@@ -250,23 +278,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                         writer.put(b, o);
                     }
                 }
-                uint32_t again = __ballot_sync(kFull, valid && sums.some && !(odd == 0.f));
+                // (with a sum of p that is not finite all of the row is NaN, as it should be)
+                uint32_t again = __ballot_sync(kFull, valid && sums.some && !(odd == 0.f) && isfinite(r.l));
+                __syncwarp();   // what is there has been written
                 while (again) {
                     const int from = __ffs(again) - 1;
                     again &= again - 1;
                     const int rt = __shfl_sync(kFull, token, from), rg = __shfl_sync(kFull, g, from), rl = __shfl_sync(kFull, lim, from);
-                    float m, l, o[D / 32];
-                    prompt_row<T, D>(a, rt, h * a.group + rg, w.k0, w.j0 * kTile, min(w.j1 * kTile, rl), c, kShift<BF16>, m, l, o);
+                    const float rm = __shfl_sync(kFull, r.m, from), rinv = __shfl_sync(kFull, inv, from);
+                    float o[D / 32];
+                    const uint32_t bad = prompt_row<T, D>(a, rt, h * a.group + rg, w.k0, w.j0 * kTile, st.end[t] * kTile, rl, c, rm,
+                                                          kShift<BF16>, o);
                     T *to = reinterpret_cast<T *>(a.out.p) + rt * a.out.ldt + (int64_t)(h * a.group + rg) * a.out.ldh;
                     float *ro = my ? my - lane + from : nullptr;
 #pragma unroll
                     for (int b = 0; b < D / 32; ++b) {
-                        if (my) __stcg(ro + (2 + 32 * b + lane) * kPair, o[b]);
-                        else to[32 * b + lane] = (T)(l == 0.f ? 0.f : o[b] / l);
-                    }
-                    if (my && lane == 0) {
-                        __stcg(ro, m);
-                        __stcg(ro + kPair, l);
+                        if (!(bad >> b & 1u)) continue;
+                        const int ch = D / 32 * lane + b;
+                        if (my) __stcg(ro + (2 + ch) * kPair, o[b]);
+                        else to[ch] = (T)(o[b] * rinv);
                     }
                 }
             }

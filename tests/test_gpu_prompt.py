@@ -240,3 +240,50 @@ def test_no_query_tokens_and_no_keys():
 def test_heads_of_every_group_up_to_128():
     for group in (2, 3, 4, 6, 9, 10, 11, 13, 24, 31, 33, 43, 64, 100):
         check(*make([6, 70], [6, 70], group, 1, 64, torch.bfloat16, seed=group), [6, 70])
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("q_lens,k_lens,d", [([300, 200], [300, 200], 64), ([400], [400], 128), ([6, 40], [20000, 200], 128),
+                                             ([100], [9000], 64)])
+def test_bad_values_of_some_channels(q_lens, k_lens, d, dt):
+    """Channels whose values are bad throughout, from a key on, or at one key: the other channels keep their bits, and rows
+    before a bad value theirs within the bound, whether the keys are cut or not."""
+    q, k, v = make(q_lens, k_lens, 8, 2, d, dt)
+    clean, _ = call(q, k, v, q_lens, k_lens)
+    want, bound = ref.prompt(q, k, v, q_lens, k_lens)
+    at = sum(k_lens) - 4      # a key of the last sequence that its last 4 rows see
+    bad = v.clone()
+    bad[..., 3] = float("inf")
+    bad[at:, :, 10] = float("nan")
+    bad[at, :, d - 1] = float("-inf")
+    out, ws = call(q, k, bad, q_lens, k_lens)
+    assert cs.cs_get_device_error(ws) == 0
+    rows = sum(q_lens) - 4
+    keep = [c for c in range(d) if c not in (3, 10, d - 1)]
+    assert torch.equal(out[..., keep], clean[..., keep])
+    assert not torch.isfinite(out[..., 3]).any()
+    for c in (10, d - 1):
+        off = (out[:rows, :, c].double() - want[:rows, :, c]).abs()
+        assert (off <= bound[:rows, :, c]).all()
+        assert not torch.isfinite(out[rows:, :, c]).any()
+
+
+def test_all_values_and_all_keys_bad():
+    """A prompt of NaN takes no longer than another: no wait runs out over it, and its neighbours are as they were."""
+    lens = [6000, 300]
+    q, k, v = make(lens, lens, 8, 2, 128, torch.bfloat16)
+    clean, _ = call(q, k, v, lens)
+    for t in (k, v):
+        poisoned = t.clone()
+        poisoned[:6000] = float("nan")
+        out, ws = call(q, poisoned if t is k else k, poisoned if t is v else v, lens)
+        assert cs.cs_get_device_error(ws) == 0
+        assert torch.isnan(out[:6000]).all() and torch.equal(out[6000:], clean[6000:])
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [([500], [500]), ([3], [20000])])
+def test_the_largest_values_of_bf16(q_lens, k_lens):
+    """Sums over many keys stay in range where the values are of the largest there are."""
+    q, k, v = make(q_lens, k_lens, 4, 1, 64, torch.bfloat16)
+    v = (v.sign() * 3e38 * (0.5 + 0.5 * torch.rand(v.shape, device="cuda"))).to(torch.bfloat16)
+    check(q, k, v, q_lens, k_lens)
