@@ -5,7 +5,8 @@
 // (cs_attn_tc.cuh) with the key tiles that they see, longest first, cut along
 // the keys where few rows see many.  In the second a CTA per SM goes through
 // the list for all key/value heads: one thread loads tiles by TMA, one issues
-// the products, two warpgroups have the rows.
+// the products, two warpgroups have the rows.  A few works that need not be cut
+// are listed by each CTA for itself, and there is no first kernel.
 //
 // The rows of a tile are whole tokens of one group of heads: 128 / group tokens.
 // A tile's box of q is [tokens][group][64 channels], so that it lands row by
@@ -22,6 +23,11 @@ namespace cs {
 namespace {
 
 constexpr int kMaxGroup = 128;         // query heads of one key/value head
+// Listed by every CTA itself are up to 32 pairs (a warp's lanes) of up to 31 sequences with up to kOwnTiles key tiles, which then
+// are not cut.  Without the first kernel, and without: 9 tokens of 8 heads 6.4 and 10.7 us, 2,048 of 40 heads 44.8 and 50, one
+// token over 2,048 keys 18 and 22 (two pieces a head); with twice the tiles 100 tokens of 8 heads to a key head over 4,096 keys
+// 52 instead of 34.
+constexpr int kOwnPairs = 32, kOwnTiles = 16;
 constexpr int kPromptThreads = 320;    // two warpgroups of rows, the products' warp, the loads' warp
 
 struct PromptK {
@@ -32,6 +38,7 @@ struct PromptK {
     uint32_t *err;
     int per;             // tokens of a row tile
     int sms;
+    int own;             // every CTA lists the works itself
 };
 
 // ------------------------------------------------------------------- the list
@@ -73,6 +80,20 @@ __device__ void plan_starts(const int32_t *start, int batch, int total, int *at,
     }
 }
 
+// Pair i of sequence b, whose tokens and keys are these rows: its key tiles, and in w all of its work but the piece.
+__device__ __forceinline__ int prompt_work(const PromptK &a, int b, int i, int q0, int q1, int k0, int k1, Work &w) {
+    const int pair = 2 * a.per, t = i * pair, n_q = q1 - q0, n_k = k1 - k0;
+    const int lim = a.causal ? min(max(n_k - n_q + min(t + pair, n_q), 0), n_k) : n_k;
+    w.tok0 = q0 + t;
+    w.toks = min(pair, n_q - t);
+    w.seq = b;
+    w.lim0 = a.causal ? n_k - n_q + t + 1 : n_k;
+    w.n_k = n_k;
+    w.k0 = k0;
+    w.narrow = w.toks <= a.per;
+    return (lim + kTile - 1) / kTile;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Plan plan) {
     extern __shared__ int starts[];
     __shared__ int scan[32];
@@ -103,17 +124,54 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Pl
             if (first[mid] <= i) lo = mid;
             else hi = mid;
         }
-        const int t = (i - first[lo]) * pair, n_q = qs[lo + 1] - qs[lo], n_k = ks[lo + 1] - ks[lo];
-        const int lim = a.causal ? min(max(n_k - n_q + min(t + pair, n_q), 0), n_k) : n_k;
-        w.tok0 = qs[lo] + t;
-        w.toks = min(pair, n_q - t);
-        w.seq = lo;
-        w.lim0 = a.causal ? n_k - n_q + t + 1 : n_k;
-        w.n_k = n_k;
-        w.k0 = ks[lo];
-        w.narrow = w.toks <= a.per;
-        return (lim + kTile - 1) / kTile;
+        return prompt_work(a, lo, i - first[lo], qs[lo], qs[lo + 1], ks[lo], ks[lo + 1], w);
     });
+}
+
+// The list of a few works that are not cut, by a warp: each CTA writes its own; returns their number.
+__device__ __forceinline__ int own_list(const PromptK &a, Work *list) {
+    const int lane = threadIdx.x & 31, pair = 2 * a.per;
+    // lane b: sequence b's starts
+    auto starts = [&](const int32_t *start, int total) {
+        const int x = lane <= a.batch ? ld_dep(start + lane) : INT_MIN;
+        int run = min(max(x, 0), total);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(kFull, run, o);
+            if (lane >= o) run = max(run, n);
+        }
+        if (lane <= a.batch && x != run) atomicOr(a.err, CS_DEVERR_COUNT);
+        return run;
+    };
+    const int q0 = starts(a.q_start, a.q_total), k0 = a.k_start == a.q_start ? q0 : starts(a.k_start, a.k_total);
+    const int q1 = __shfl_down_sync(kFull, q0, 1), k1 = __shfl_down_sync(kFull, k0, 1);
+    const int n = lane < a.batch ? (q1 - q0 + pair - 1) / pair : 0;
+    int behind = n;   // the pairs of sequences up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, behind, o);
+        if (lane >= o) behind += x;
+    }
+    const int total = __shfl_sync(kFull, behind, 31);
+    // lane i: pair i, of the first sequence that has more behind it
+    int b = 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (__shfl_sync(kFull, behind, b + o - 1) <= lane) b += o;
+    b = min(b, a.batch - 1);
+    Work w;
+    const int at = lane - __shfl_sync(kFull, behind - n, b), qb = __shfl_sync(kFull, q0, b), qe = __shfl_sync(kFull, q1, b);
+    const int kb = __shfl_sync(kFull, k0, b), ke = __shfl_sync(kFull, k1, b);
+    w.j1 = prompt_work(a, b, at, qb, qe, kb, ke, w);
+    w.j0 = w.p = w.rec = 0;
+    w.pieces = 1;
+    int place = 0;   // behind those of more tiles
+    for (int i = 0; i < total; ++i) {
+        const int x = __shfl_sync(kFull, w.j1, i);
+        place += x > w.j1 || (x == w.j1 && i < lane);
+    }
+    if (lane < total) list[place] = w;
+    return total;
 }
 
 // -------------------------------------------------------------- the attention
@@ -201,7 +259,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __shared__ Bars<C::STAGES> bars;
     __shared__ float2 stat[kTile];
     __shared__ uint32_t tmem_at;
-    __shared__ int flag;
+    __shared__ int flag, listed;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const uint32_t q_at = (smem_addr(dsm) + 1023u) & ~1023u, ring = q_at + 2 * C::DB * kBlock;
     if (warp == 8) tm_alloc(&tmem_at);
@@ -212,7 +270,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     const uint32_t tmem = uniform(tmem_at);
     pdl_wait();
     pdl_launch_dependents();
-    const int total = uniform(ld_dep(plan.count) * a.kv), recs = ld_dep(plan.count + 1), step = a.causal;
+    const Work *works = plan.work;
+    if (a.own) {
+        Work *list = plan.work + blockIdx.x * kOwnPairs;
+        if (warp == 0) {
+            const int n = own_list(a, list);
+            if (lane == 0) listed = n;
+        }
+        works = list;
+        __syncthreads();
+    }
+    const int total = uniform((a.own ? listed : ld_dep(plan.count)) * a.kv), recs = a.own ? 0 : ld_dep(plan.count + 1), step = a.causal;
 
     // where a row tile's keys end in a work
     auto end_of = [&](const Work &w, int t) {
@@ -229,7 +297,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         for (int i = 0;; ++i) {
             const int x = nth_work(i);
             if (x >= total) break;
-            const Work w = load_work(plan.work + x / a.kv);
+            const Work w = load_work(works + x / a.kv);
             const int h = x % a.kv, rt = w.narrow ? 0 : t, at = rt * a.per + tok;
             const Streams st = streams_of(w, end_of(w, 0), end_of(w, 1));
             const bool valid = tok < a.per && at < w.toks;
@@ -316,7 +384,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         for (int i = 0; ok; ++i) {
             const int x = nth_work(i);
             if (x >= total) break;
-            Work w = load_work(plan.work + x / a.kv);
+            Work w = load_work(works + x / a.kv);
             const int end0 = uniform(end_of(w, 0)), end1 = uniform(end_of(w, 1));
             w.j0 = uniform(w.j0);
             w.narrow = uniform(w.narrow);
@@ -333,7 +401,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
             for (int i = 0; ok; ++i) {
                 const int x = nth_work(i);
                 if (x >= total) break;
-                const Work w = load_work(plan.work + x / a.kv);
+                const Work w = load_work(works + x / a.kv);
                 const int h = x % a.kv;
                 const Streams st = streams_of(w, end_of(w, 0), end_of(w, 1));
                 if (st.last <= w.j0) continue;
@@ -385,7 +453,8 @@ bool prompt_sizes(int batch, int n_heads, int kv_heads, int d_head, int q_total,
 size_t prompt_scratch(int batch, int n_heads, int kv_heads, int d, int q_total, int k_total, int sms, char *at, Plan *plan) {
     const int per = kTile / (n_heads / kv_heads);
     const int recs = k_total > kLeastPiece * kTile ? 2 * sms : 0;
-    return plan_scratch((size_t)q_total / (2 * per) + batch, recs, d, at, plan);
+    const size_t works = (size_t)q_total / (2 * per) + batch, own = (size_t)kOwnPairs * sms;   // (calls of smaller sizes may list their own)
+    return plan_scratch(works > own ? works : own, recs, d, at, plan);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -417,10 +486,12 @@ bool head_map(CUtensorMap *m, const QRowsK &r, int d, int heads, int tokens, int
 template <int D, bool BF16>
 cudaError_t run_prompt(const PromptK &a, const Plan &plan, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                        cudaStream_t s) {
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&prompt_plan_kernel));
-    if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void *>(&prompt_kernel<D, BF16>));
-    if (e == cudaSuccess)
-        e = launch(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 3 * ((size_t)a.batch + 1) * sizeof(int), s, pdl_enabled(), a, plan);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&prompt_kernel<D, BF16>));
+    if (e == cudaSuccess && !a.own) {
+        e = allow_smem(reinterpret_cast<const void *>(&prompt_plan_kernel));
+        if (e == cudaSuccess)
+            e = launch(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 3 * ((size_t)a.batch + 1) * sizeof(int), s, pdl_enabled(), a, plan);
+    }
     if (e != cudaSuccess) return e;
     // no more CTAs than there can be works
     const int64_t most = ((int64_t)a.q_total / (2 * a.per) + a.batch + plan.recs) * a.kv;
@@ -492,6 +563,7 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)d_head);
     a.err = static_cast<uint32_t *>(ws);
     a.per = kTile / a.group;
+    a.own = batch < 32 && q_total / (2 * a.per) + batch <= kOwnPairs && k_total <= kOwnTiles * kTile;
     if (!encoder()) {
         set_error("%s: the driver has no tensor maps", who);
         return CS_ERR_CUDA;

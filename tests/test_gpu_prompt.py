@@ -287,3 +287,37 @@ def test_the_largest_values_of_bf16(q_lens, k_lens):
     q, k, v = make(q_lens, k_lens, 4, 1, 64, torch.bfloat16)
     v = (v.sign() * 3e38 * (0.5 + 0.5 * torch.rand(v.shape, device="cuda"))).to(torch.bfloat16)
     check(q, k, v, q_lens, k_lens)
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [
+    ([5] * 31, None), ([5] * 32, None), ([0, 300, 0, 0, 1] * 6, None), ([2048], None), ([2049], None), ([1] * 20 + [0] * 11, None),
+    ([1, 64, 65], [1000, 64, 984]), ([1, 64, 65], [1000, 64, 985]), ([0] * 30 + [129], [0] * 30 + [2048]), ([0, 0], [0, 0])])
+def test_about_the_limits_of_short_lists(q_lens, k_lens):
+    """As many sequences, works and keys as are listed without a kernel of their own, one less and one more."""
+    for heads, kv, d in ((2, 2, 64), (16, 1, 128)):
+        check(*make(q_lens, q_lens if k_lens is None else k_lens, heads, kv, d, torch.bfloat16), q_lens, k_lens)
+
+
+def test_lists_of_both_kinds_in_turn():
+    """Calls that share a workspace, with and without a kernel for the list, eager and captured."""
+    q, k, v = make([3000], [3000], 8, 2, 64, torch.float16)
+    ws = cs.PromptWorkspace(40, 8, 2, 64, 3000)
+    cases = [[100, 50], [2900, 30], [70] * 40, [1, 2, 3], [2048]]
+    views = [[t[:sum(lens)] for t in (q, k, v)] + [starts(lens)] for lens in cases]
+    want = [call(*x[:3], lens)[0] for x, lens in zip(views, cases)]
+    got = [torch.full_like(w, 7.0) for w in want]
+
+    def all_of_them():
+        for x, g in zip(views, got):
+            cs.cs_prompt_attention(*x[:3], g, x[3], ws)
+    all_of_them()
+    assert all(torch.equal(w, g) for w, g in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        all_of_them()
+    for g in got:
+        g.fill_(7.0)
+    graph.replay()
+    graph.replay()
+    assert all(torch.equal(w, g) for w, g in zip(want, got))
+    assert cs.cs_get_device_error(ws) == 0
