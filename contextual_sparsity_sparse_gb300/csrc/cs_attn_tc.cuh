@@ -22,9 +22,9 @@
 // then the thread scales its row of O, which the order above leaves alone: S_t's
 // commit covers the product with V before it.
 //
-// Work that is cut along the keys leaves records (each row's m, sum of p and
-// sums of p v, in 32 bits); the CTA that finishes the last piece of a work
-// adds them up in the pieces' order, whoever comes last.
+// Work that is cut along the keys leaves records (what each row's p are taken
+// against, the sum of p and the sums of p v, in 32 bits), which another kernel
+// adds up in the pieces' order.
 //
 // Bound (8,192 tokens, 64 over 8 heads of 128, causal, bf16: 690 us, 1,590
 // TFLOP/s): a pair of key tile and row tiles takes 2,800 cycles, of which the products need 2,048.  A
@@ -201,10 +201,10 @@ struct Work {
 static_assert(sizeof(Work) == 48, "three 16-byte loads");
 
 struct Plan {
-    int *count;          // [0] works, [1] records of a head
+    int *count;          // [0] works, [1] records of a head, [2] pairs that are cut
     Work *work;
-    unsigned *arrived;   // [records] finished pieces, by the first record's place
-    float *rec;          // [records] per row m and l, then [d][256] sums of p v
+    int *cut;            // [records / 2] their first pieces
+    float *rec;          // [records] per row the power of 2 that its p are taken against and l, then [d][256] sums of p v
     int recs;            // how many records there is room for
 };
 __host__ __device__ constexpr size_t rec_floats(int d) { return (size_t)kPair * (d + 2); }
@@ -227,15 +227,14 @@ constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in
 template <typename Find>
 __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find find) {
     constexpr int BINS = 256;
-    __shared__ int scan[32], hist[BINS], longest, recs, placed;
+    __shared__ int scan[32], hist[BINS], longest, recs, placed, cuts;
     __shared__ unsigned long long units;
     const int tid = threadIdx.x;
     if (tid == 0) {
-        longest = recs = placed = 0;
+        longest = recs = placed = cuts = 0;
         units = 0;
     }
     if (tid < BINS) hist[tid] = 0;
-    for (int i = tid; i < plan.recs; i += kPlanThreads) plan.arrived[i] = 0;
     __syncthreads();
     unsigned long long sum = 0;
     int most = 0;
@@ -262,7 +261,10 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
     for (int i = tid; i < pairs; i += kPlanThreads) {
         const int tiles = find(i, w), pieces = pieces_of(tiles);
         atomicAdd(&hist[bin_of(tiles, pieces)], pieces);
-        if (pieces > 1) atomicAdd(&recs, pieces);
+        if (pieces > 1) {
+            atomicAdd(&recs, pieces);
+            atomicAdd(&cuts, 1);
+        }
     }
     __syncthreads();
     const int mine = tid < BINS ? hist[tid] : 0;
@@ -272,6 +274,8 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
     if (tid == 0) {
         plan.count[0] = all;
         plan.count[1] = recs;
+        plan.count[2] = cuts;
+        cuts = 0;
     }
     __syncthreads();
     for (int i = tid; i < pairs; i += kPlanThreads) {
@@ -279,6 +283,7 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
         w.pieces = pieces;
         w.rec = pieces > 1 ? atomicAdd(&placed, pieces) : 0;
         const int to = atomicAdd(&hist[bin_of(tiles, pieces)], pieces);
+        if (pieces > 1) plan.cut[atomicAdd(&cuts, 1)] = to;
         for (int p = 0; p < pieces; ++p) {
             w.j0 = (int)((long long)tiles * p / pieces);
             w.j1 = (int)((long long)tiles * (p + 1) / pieces);
@@ -290,15 +295,15 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
 
 // A list's place: its works' number and how many records there are; returns the bytes.
 inline size_t plan_scratch(size_t works, int recs, int d, char *at, Plan *plan) {
-    const size_t list = align256((works + recs) * sizeof(Work)), arrived = align256((size_t)recs * sizeof(unsigned));
+    const size_t list = align256((works + recs) * sizeof(Work)), cut = align256((size_t)recs / 2 * sizeof(int));
     if (plan) {
         plan->count = reinterpret_cast<int *>(at);
         plan->work = reinterpret_cast<Work *>(at + 256);
-        plan->arrived = reinterpret_cast<unsigned *>(at + 256 + list);
-        plan->rec = reinterpret_cast<float *>(at + 256 + list + arrived);
+        plan->cut = reinterpret_cast<int *>(at + 256 + list);
+        plan->rec = reinterpret_cast<float *>(at + 256 + list + cut);
         plan->recs = recs;
     }
-    return 256 + list + arrived + (size_t)recs * rec_floats(d) * sizeof(float);
+    return 256 + list + cut + (size_t)recs * rec_floats(d) * sizeof(float);
 }
 
 // This CTA's i-th work of `total`, which are in the order of falling size: there and back over the CTAs.
@@ -314,7 +319,6 @@ struct Bars {
     uint64_t full[STAGES], empty[STAGES];   // a stage holds one key or one value tile
     uint64_t s_full[2], p_full[2][kParts], o_full[2];
     uint64_t ready, taken;                  // narrow work: stream 1 is done; it has been added to stream 0
-    uint64_t written, told;                 // a record is written; whether it was the last
     uint64_t drain;
 };
 template <int STAGES>
@@ -332,8 +336,6 @@ __device__ __forceinline__ void init_bars(Bars<STAGES> &b, int q_writers, int wr
     }
     mbar_init(&b.ready, kTile);
     mbar_init(&b.taken, kTile);
-    mbar_init(&b.written, kPair);
-    mbar_init(&b.told, 1);
     mbar_init(&b.drain, 1);
     mbar_fence_init();
 }
@@ -484,7 +486,7 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
 
 struct RowState {
     float m, l;   // the maximum that p is taken against (-inf: none yet), the sum of p
-    uint32_t n_s = 0, n_o = 0, n_join = 0, n_rec = 0;   // waits so far
+    uint32_t n_s = 0, n_o = 0, n_join = 0;   // waits so far
 };
 
 // fp16's p are taken 2^7 larger, so that those of 2^-31 of the largest are still there: with m following
@@ -687,59 +689,72 @@ __device__ __forceinline__ void load_sums(uint32_t o_at, int i, const Sums &s, f
     }
 }
 
-// After a piece's record is written: whether this CTA's is the pair's last piece (-1: a wait gave up).  All 256 threads of
-// the row tiles; n: how often they have asked before.
-template <int STAGES>
-__device__ __forceinline__ int last_piece(Bars<STAGES> &b, unsigned *arrived, int pieces, volatile int *flag, uint32_t n, uint32_t *err) {
-    __threadfence();
-    mbar_arrive(&b.written);
-    if (threadIdx.x == 0) {
-        if (wait(&b.written, n & 1, err)) {
-            *flag = atomicAdd(arrived, 1u) == (unsigned)pieces - 1;
-            mbar_arrive(&b.told);
-        }
-    }
-    __syncwarp();
-    if (!wait_warp(&b.told, n & 1, err)) return -1;
-    const int last = *flag;
-    if (last) __threadfence();
-    return last;
+// A row's statistics in its record.  What p are taken against is left as softmax_rows rounds it, so that pieces fit together.
+template <bool BF16>
+__device__ __forceinline__ void put_stat(float *rec, const RowState &r, float c) {
+    __stcg(rec, r.m == -INFINITY ? -INFINITY : -fmaf(-r.m, c, kShift<BF16>));
+    __stcg(rec + kPair, r.l);
 }
 
-// A row's outputs from its pieces (0: zeros), put(i, o) for every 32 channels.
-template <int D, typename Put>
-__device__ __forceinline__ void join_pieces(const float *rec, int pieces, int row, float c, Put put) {
-    float m = -INFINITY, l = 0.f;
-    for (int p = 0; p < pieces; ++p) m = fmaxf(m, __ldcg(rec + p * rec_floats(D) + row));
-    if (m == -INFINITY) m = 0.f;
-    for (int p = 0; p < pieces; ++p) {
-        const float *r = rec + p * rec_floats(D) + row;
-        l = fmaf(ex2((__ldcg(r) - m) * c), __ldcg(r + kPair), l);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = 0; i < D / 32; ++i) {
-        float o[32];
+// What join_records has to know of a row: where its outputs are, whether it has any, whether they are not just zeros.
+struct RowPlace {
+    char *at;
+    bool there, valid;
+};
+
+// The outputs of the work that was cut, a warp for 8 channels of 32 rows: place(w, h, rt, row) tells of a row of row tile rt,
+// put(at, i, o) takes channels 8 i .. of it.  Four pieces' loads are under way together.
+template <int D, typename Place, typename Put>
+__device__ __forceinline__ void join_records(const Plan &plan, int kv, Place place, Put put) {
+    constexpr int G = D / 8, STEP = 4;
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x >> 5);
+    const int total = ld_dep(plan.count + 2) * kv * (kPair / 32) * G, recs = ld_dep(plan.count + 1);
+    for (int x = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); x < total; x += warps) {
+        const int i = x % G, rows = x / G % (kPair / 32), h = x / (G * kPair / 32) % kv;
+        const Work w = load_work(plan.work + ld_dep(plan.cut + x / (G * kPair / 32) / kv));
+        const RowPlace row = place(w, h, rows / 4, rows % 4 * 32 + lane);
+        if (!__any_sync(kFull, row.there)) continue;
+        const float *rec = plan.rec + (int64_t)(h * recs + w.rec) * rec_floats(D) + rows * 32 + lane;
+        float m = -INFINITY, l = 0.f, o[8] = {};
+        for (int p0 = 0; p0 < w.pieces; p0 += STEP) {
+            float pm[STEP], pl[STEP], v[STEP][8];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        for (int p = 0; p < pieces; ++p) {
-            const float *r = rec + p * rec_floats(D) + row;
-            const float mp = __ldcg(r);
-            if (mp == -INFINITY && __ldcg(r + kPair) == 0.f) continue;   // saw nothing, wrote nothing
-            const float f = ex2((mp - m) * c) * inv;
+            for (int p = 0; p < STEP; ++p) {
+                const bool some = row.valid && p0 + p < w.pieces;
+                const float *r = rec + (p0 + p) * rec_floats(D);
+                pm[p] = some ? __ldcg(r) : -INFINITY;
+                pl[p] = some ? __ldcg(r + kPair) : 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = fmaf(f, __ldcg(r + (2 + 32 * i + e) * kPair), o[e]);
+                for (int e = 0; e < 8; ++e) v[p][e] = some ? __ldcg(r + (2 + 8 * i + e) * kPair) : 0.f;
+            }
+#pragma unroll
+            for (int p = 0; p < STEP; ++p) {
+                if (pm[p] == -INFINITY && pl[p] == 0.f) continue;   // saw nothing, may have written nothing
+                const float up = fmaxf(m, pm[p]), base = up == -INFINITY ? 0.f : up;
+                const float keep = m == -INFINITY ? 0.f : ex2(m - base), f = ex2(pm[p] - base);
+                m = up;
+                l = fmaf(f, pl[p], l * keep);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = fmaf(f, v[p][e], o[e] * keep);
+            }
         }
-        put(i, o);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= inv;
+        if (row.there) put(row.at, i, o);
     }
 }
+constexpr int kJoinThreads = 256;
 
-// 32 values of a row as 16 bits, its start on a 16-byte boundary.
+// 8 or 32 values of a row as 16 bits, their place on a 16-byte boundary.
+template <bool BF16>
+__device__ __forceinline__ void store8(char *at, const float *v) {
+    *reinterpret_cast<uint4 *>(at) = make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]), pack2<BF16>(v[6], v[7]));
+}
 template <bool BF16>
 __device__ __forceinline__ void store32(char *at, const float *v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<uint4 *>(at)[i] = make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]), pack2<BF16>(v[8 * i + 2], v[8 * i + 3]),
-                                                      pack2<BF16>(v[8 * i + 4], v[8 * i + 5]), pack2<BF16>(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < 4; ++i) store8<BF16>(at + 16 * i, v + 8 * i);
 }
 
 // Rows of 16-bit outputs, a thread's row in 32 channels at a time.  Written by the warp in lines: 64 channels of its 32 rows

@@ -1,12 +1,12 @@
 // Attention of whole prompts, packed one behind the other: causal or not, with
 // grouped heads.
 //
-// Two kernels.  The first lists the work: for every sequence, pairs of row tiles
+// Three kernels.  The first lists the work: for every sequence, pairs of row tiles
 // (cs_attn_tc.cuh) with the key tiles that they see, longest first, cut along
 // the keys where few rows see many.  In the second a CTA per SM goes through
 // the list for all key/value heads: one thread loads tiles by TMA, one issues
-// the products, two warpgroups have the rows.  A few works that need not be cut
-// are listed by each CTA for itself, and there is no first kernel.
+// the products, two warpgroups have the rows.  The third adds up what was cut.  A few works that need not be cut
+// are listed by each CTA for itself, and there is only the second kernel.
 //
 // The rows of a tile are whole tokens of one group of heads: 128 / group tokens.
 // A tile's box of q is [tokens][group][64 channels], so that it lands row by
@@ -259,7 +259,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __shared__ Bars<C::STAGES> bars;
     __shared__ float2 stat[kTile];
     __shared__ uint32_t tmem_at;
-    __shared__ int flag, listed;
+    __shared__ int listed;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const uint32_t q_at = (smem_addr(dsm) + 1023u) & ~1023u, ring = q_at + 2 * C::DB * kBlock;
     if (warp == 8) tm_alloc(&tmem_at);
@@ -323,10 +323,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 const uint32_t o_at = tmem + (((uint32_t)row & ~31u) << 16) + 2 * kTile + t * D;
                 float *my = rec ? rec + w.p * rec_floats(D) + rt * kTile + row : nullptr;
                 const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-                if (my) {
-                    __stcg(my, r.m);
-                    __stcg(my + kPair, r.l);
-                }
+                if (my) put_stat<BF16>(my, r, c);
                 RowWriter<BF16, D == 128> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
                 float odd = 0.f;   // NaN, if anything is not finite
 #pragma unroll 1
@@ -369,14 +366,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
                 }
             }
             if (!leave_streams(r, st, t, bars, a.err)) break;
-            if (rec) {
-                const int last = last_piece(bars, plan.arrived + h * recs + w.rec, w.pieces, &flag, r.n_rec++, a.err);
-                if (last < 0) break;
-                if (last && mine) {
-                    RowWriter<BF16, D == 128> writer(ring + C::STAGES * C::DB * kBlock + warp * C::OUT, reinterpret_cast<char *>(out), valid);
-                    join_pieces<D>(rec, valid ? w.pieces : 0, rt * kTile + row, c, [&](int b, const float *o) { writer.put(b, o); });
-                }
-            }
         }
     } else if (warp == 8) {
         MmaState ms;
@@ -441,6 +430,21 @@ prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     if (warp == 8) tm_free(tmem);
 }
 
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptK a, Plan plan) {
+    pdl_wait();
+    pdl_launch_dependents();
+    join_records<D>(
+        plan, a.kv,
+        [&](const Work &w, int h, int rt, int row) {
+            const int tok = row / a.group, at = rt * a.per + tok;
+            const bool valid = tok < a.per && at < w.toks;
+            const int64_t to = (w.tok0 + at) * a.out.ldt + (int64_t)(h * a.group + row - tok * a.group) * a.out.ldh;
+            return RowPlace{a.out.p + 2 * to, valid, valid};
+        },
+        [](char *at, int i, const float *o) { store8<BF16>(at + 16 * i, o); });
+}
+
 // ------------------------------------------------------------------- host side
 
 bool prompt_sizes(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total) {
@@ -495,8 +499,11 @@ cudaError_t run_prompt(const PromptK &a, const Plan &plan, const CUtensorMap &mq
     if (e != cudaSuccess) return e;
     // no more CTAs than there can be works
     const int64_t most = ((int64_t)a.q_total / (2 * a.per) + a.batch + plan.recs) * a.kv;
-    return launch(prompt_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kPromptThreads), PromptCfg<D>::smem, s,
-                  pdl_enabled(), mq, mk, mv, a, plan);
+    e = launch(prompt_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kPromptThreads), PromptCfg<D>::smem, s,
+               pdl_enabled(), mq, mk, mv, a, plan);
+    if (e == cudaSuccess && plan.recs > 0 && !a.own)
+        e = launch(prompt_join_kernel<D, BF16>, dim3(4 * a.sms), dim3(kJoinThreads), 0, s, pdl_enabled(), a, plan);
+    return e;
 }
 
 }  // namespace

@@ -93,7 +93,6 @@ struct TreeShared {
     uint8_t parents[kParentRing][kMaxTree];     // parent + 1 of every drafted token of a work's sequence
     float2 stat[kTile];
     uint32_t tmem;
-    int flag;
 };
 
 static_assert(offsetof(TreeShared, seen) % 16 == 0, "read by 16 bytes");
@@ -269,10 +268,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 const uint32_t o_at = tmem + (((uint32_t)row & ~31u) << 16) + 2 * kTile + t * D;
                 float *my = rec ? rec + w.p * rec_floats(D) + rt * kTile + row : nullptr;
                 const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-                if (my) {
-                    __stcg(my, r.m);
-                    __stcg(my + kPair, r.l);
-                }
+                if (my) put_stat<false>(my, r, c);
 #pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
                     float o[32];
@@ -294,12 +290,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 for (int e = 0; e < D; ++e) q_store1(a.out, to + e, 0.f);
             }
             if (!leave_streams(r, st, t, sh.bars, a.err)) break;
-            if (rec) {
-                const int last = last_piece(sh.bars, plan.arrived + h * recs + w.rec, w.pieces, &sh.flag, r.n_rec++, a.err);
-                if (last < 0) break;
-                if (last && mine)
-                    join_pieces<D>(rec, valid ? w.pieces : 0, rt * kTile + row, c, put);
-            }
         }
     } else if (warp < 8 + kMakers) {
         // a thread's chunk and slot: 8 threads side by side, which store together, have chunks of the same 64 channels in 4 slots,
@@ -477,6 +467,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
     if (warp == kIssuer) tm_free(tmem);
 }
 
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeK a, Plan plan) {
+    pdl_wait();
+    pdl_launch_dependents();
+    join_records<D>(
+        plan, a.kv,
+        [&](const Work &w, int h, int rt, int row) {
+            const int tok = row / a.group, at = rt * a.per + tok, token = w.tok0 + at;
+            const int64_t to = w.seq * a.out.ldb + token * a.out.ldt + (int64_t)(h * a.group + row - tok * a.group) * a.out.ldh;
+            const bool mine = tok < a.per && !(w.narrow && rt == 1);
+            return RowPlace{a.out.p + 2 * to, mine && token < a.n, mine && at < w.toks};
+        },
+        [&](char *at, int i, const float *o) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = o[(e & 3) * 2 + (e >> 2)];
+            if (a.out.vec) {
+                store8<BF16>(at + 16 * i, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q_store1(a.out, (at - a.out.p) / 2 + 8 * i + e, v[e]);
+            }
+        });
+}
+
 // -------------------------------------------------------------------- few rows
 //
 // The products above work on 128 rows however few there are.  Up to kFewRows rows
@@ -599,8 +614,11 @@ cudaError_t run_tree(const TreeK &a, const Plan &plan, cudaStream_t s) {
     if (e == cudaSuccess) e = launch(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, pdl_enabled(), a, plan);
     if (e != cudaSuccess) return e;
     const int64_t most = ((int64_t)a.c.batch * ((a.n + 2 * a.per - 1) / (2 * a.per)) + plan.recs) * a.kv;
-    return launch(tree_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kTreeThreads), TreeCfg<D>::smem, s,
-                  pdl_enabled(), a, plan);
+    e = launch(tree_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kTreeThreads), TreeCfg<D>::smem, s,
+               pdl_enabled(), a, plan);
+    if (e == cudaSuccess && plan.recs > 0)
+        e = launch(tree_join_kernel<D, BF16>, dim3(4 * a.sms), dim3(kJoinThreads), 0, s, pdl_enabled(), a, plan);
+    return e;
 }
 
 }  // namespace
