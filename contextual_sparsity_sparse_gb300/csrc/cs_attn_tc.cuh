@@ -219,15 +219,16 @@ __device__ __forceinline__ Work load_work(const Work *w) {
 }
 
 constexpr int kPlanThreads = 256;   // (1,024 took 1.3 us longer, for their barriers)
-constexpr int kLeastPiece = 8;         // key tiles: shorter pieces cost more in records than they win
+constexpr int kLeastPiece = 4;      // key tiles of a piece (8: 100 tokens of 8 heads to a key head over 3,000 keys 26.7 us instead of 21.8)
+constexpr int kUncut = 8;           // up to as many nothing is cut, and no room for records is needed
 
 // Lists the works of `pairs` pairs of row tiles for kv heads: those of many key tiles first, cut along the keys so that no
-// piece is longer than an SM's share of all.  find(i, w): pair i's key tiles, and in w all of its work but the piece.  One
+// piece is longer than an SM's share of all, or where that makes more pieces than SMs, somewhat longer.  find(i, w): pair i's key tiles, and in w all of its work but the piece.  One
 // CTA of kPlanThreads; places within a size differ from run to run, what a work is does not.
 template <typename Find>
 __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find find) {
     constexpr int BINS = 256;
-    __shared__ int scan[32], hist[BINS], longest, recs, placed, cuts;
+    __shared__ int scan[32], hist[BINS], rounds[kPlanThreads / 32], longest, recs, placed, cuts;
     __shared__ unsigned long long units;
     const int tid = threadIdx.x;
     if (tid == 0) {
@@ -252,9 +253,40 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
     }
     __syncthreads();
     // with a pair's pieces fewer than twice its tiles / chunk, all pieces of cut pairs are fewer than 2 SMs' number
-    const int chunk = (int)min((unsigned long long)INT_MAX, max((unsigned long long)kLeastPiece, (units * kv + sms - 1) / sms));
-    const int big = min(longest, chunk);
+    int chunk = (int)min((unsigned long long)INT_MAX, max((unsigned long long)kLeastPiece, (units * kv + sms - 1) / sms));
     auto pieces_of = [&](int tiles) { return tiles > chunk && plan.recs > 0 ? (tiles + chunk - 1) / chunk : 1; };
+    if (pairs * kv <= sms && plan.recs > 0) {
+        // A piece more than there are SMs waits for a second round.  Each warp tries another length from here to twice that;
+        // taken is the one whose rounds are soonest over.  (40 heads' 32 tokens over 2,048 slots: 4 pieces a head are 160.)
+        const int c = chunk, warp = tid >> 5;
+        chunk += (int)((long long)c * warp / (kPlanThreads / 32));
+        int n = 0, top = 0, half = 0, most = 0;   // pieces, the longest, and how many are longer than half and 3/4 of that
+        for (int i = tid & 31; i < pairs; i += 32) {
+            const int tiles = find(i, w), pieces = pieces_of(tiles);
+            n += pieces;
+            top = max(top, (tiles + pieces - 1) / pieces);
+        }
+        n = __reduce_add_sync(kFull, n) * kv;
+        top = __reduce_max_sync(kFull, top);
+        if (n > sms) {
+            for (int i = tid & 31; i < pairs; i += 32) {
+                const int tiles = find(i, w), pieces = pieces_of(tiles), size = (tiles + pieces - 1) / pieces;
+                if (2 * size > top) half += pieces;
+                if (4 * size > 3 * top) most += pieces;
+            }
+            half = __reduce_add_sync(kFull, half) * kv;
+            most = __reduce_add_sync(kFull, most) * kv;
+        }
+        // in quarters of a tile; beside its tiles a piece costs some 3 more.  The shortest pieces are a CTA's second.
+        if ((tid & 31) == 0)
+            rounds[warp] = n <= sms ? 4 * top + 12 : n > 2 * sms ? 12 * top + 36 : (half <= sms ? 4 : most <= sms ? 6 : 8) * top + 24;
+        __syncthreads();
+        int best = 0;
+        for (int i = 1; i < kPlanThreads / 32; ++i)
+            if (rounds[i] < rounds[best]) best = i;
+        chunk = c + (int)((long long)c * best / (kPlanThreads / 32));
+    }
+    const int big = min(longest, chunk);
     auto bin_of = [&](int tiles, int pieces) {
         return BINS - 1 - (int)((long long)min((tiles + pieces - 1) / pieces, big) * (BINS - 1) / max(big, 1));
     };

@@ -456,7 +456,7 @@ bool prompt_sizes(int batch, int n_heads, int kv_heads, int d_head, int q_total,
 // The list's place behind the control words; returns the bytes.
 size_t prompt_scratch(int batch, int n_heads, int kv_heads, int d, int q_total, int k_total, int sms, char *at, Plan *plan) {
     const int per = kTile / (n_heads / kv_heads);
-    const int recs = k_total > kLeastPiece * kTile ? 2 * sms : 0;
+    const int recs = k_total > kUncut * kTile ? 2 * sms : 0;
     const size_t works = (size_t)q_total / (2 * per) + batch, own = (size_t)kOwnPairs * sms;   // (calls of smaller sizes may list their own)
     return plan_scratch(works > own ? works : own, recs, d, at, plan);
 }

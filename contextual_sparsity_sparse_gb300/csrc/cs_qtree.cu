@@ -578,7 +578,7 @@ size_t tree_scratch(int batch, int kv_heads, int capacity, int d, int n_heads, i
     // what calls of fewer heads and tokens need is in it: for few rows, of as many as there can be
     const int group = n_heads / kv_heads, few_rows = group * n < kFewRows ? group * n : kFewRows;
     const FewScratch few = few_scratch(batch, kv_heads, capacity, d, kv_heads * few_rows, 1, sms);
-    const int pair = 2 * (kTile / group), recs = capacity > (kLeastPiece - 1) * kTile ? 2 * sms : 0;
+    const int pair = 2 * (kTile / group), recs = capacity > (kUncut - 1) * kTile ? 2 * sms : 0;
     const size_t many = plan_scratch((size_t)batch * ((n + pair - 1) / pair), recs, d, at, plan), fewer = few.out + few.stat + few.attn;
     return many > fewer ? many : fewer;
 }
