@@ -288,7 +288,7 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
     }
     const int big = min(longest, chunk);
     auto bin_of = [&](int tiles, int pieces) {
-        return BINS - 1 - (int)((long long)min((tiles + pieces - 1) / pieces, big) * (BINS - 1) / max(big, 1));
+        return BINS - 1 - min((tiles + pieces - 1) / pieces, big) * (BINS - 1) / max(big, 1);   // tiles are at most 2^17 and one
     };
     for (int i = tid; i < pairs; i += kPlanThreads) {
         const int tiles = find(i, w), pieces = pieces_of(tiles);
@@ -310,17 +310,37 @@ __device__ void plan_list(int pairs, int kv, int sms, const Plan &plan, Find fin
         cuts = 0;
     }
     __syncthreads();
-    for (int i = tid; i < pairs; i += kPlanThreads) {
-        const int tiles = find(i, w), pieces = pieces_of(tiles);
-        w.pieces = pieces;
-        w.rec = pieces > 1 ? atomicAdd(&placed, pieces) : 0;
-        const int to = atomicAdd(&hist[bin_of(tiles, pieces)], pieces);
-        if (pieces > 1) plan.cut[atomicAdd(&cuts, 1)] = to;
-        for (int p = 0; p < pieces; ++p) {
-            w.j0 = (int)((long long)tiles * p / pieces);
-            w.j1 = (int)((long long)tiles * (p + 1) / pieces);
-            w.p = p;
-            plan.work[to + p] = w;
+    const int lane = tid & 31;
+    for (int i0 = tid - lane; i0 < pairs; i0 += kPlanThreads) {
+        int tiles = 0, pieces = 0, to = 0;
+        if (i0 + lane < pairs) {
+            tiles = find(i0 + lane, w);
+            pieces = pieces_of(tiles);
+            to = atomicAdd(&hist[bin_of(tiles, pieces)], pieces);
+            w.pieces = pieces;
+            w.rec = w.p = w.j0 = 0;
+            w.j1 = tiles;
+            if (pieces > 1) {
+                w.rec = atomicAdd(&placed, pieces);
+                plan.cut[atomicAdd(&cuts, 1)] = to;
+            } else {
+                plan.work[to] = w;
+            }
+        }
+        // a pair's pieces are written by the warp
+        for (uint32_t cut = __ballot_sync(kFull, pieces > 1); cut; cut &= cut - 1) {
+            const int from = __ffs(cut) - 1, n = __shfl_sync(kFull, pieces, from), at = __shfl_sync(kFull, to, from);
+            Work x;
+#pragma unroll
+            for (int e = 0; e < (int)(sizeof(Work) / 4); ++e)
+                reinterpret_cast<int *>(&x)[e] = __shfl_sync(kFull, reinterpret_cast<const int *>(&w)[e], from);
+            const uint32_t all = x.j1;
+            for (int p = lane; p < n; p += 32) {
+                x.p = p;
+                x.j0 = all * p / n;
+                x.j1 = all * (p + 1) / n;
+                plan.work[at + p] = x;
+            }
         }
     }
 }

@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeK a, Plan p
 // of a cache head, which are one pass of the kernels of cs_qcache_attention, these
 // go over the slots instead, and leave outputs in 32 bits with each row's
 // statistics; a warp to a row then adds the drafted tokens on its path.  With 16 rows
-// 131,001 slots of 8 heads take 75 us so and 164 with the products above, 32 ragged sequences of up to
-// 8,192 106 and 142, 40 heads of 2,048 28 and 37; with 32 rows, two passes, 148 and 153, 207 and 143, 52 and 38.
+// 131,001 slots of 8 heads take 75 us so and 110 with the products above, 32 ragged sequences of up to
+// 8,192 105 and 125, 40 heads of 2,048 28 and 31; with 32 rows, two passes, 148 and 108, 207 and 126, 52 and 31.
 
 constexpr int kFewRows = 16;
 
