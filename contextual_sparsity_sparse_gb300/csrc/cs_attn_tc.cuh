@@ -34,7 +34,7 @@
 // Tried and not kept (packed prompts of up to 5,000 tokens, 64 over 8 heads, about 1,590 us then): a warp for
 // each stream's products 2,111 instead of 1,708; P in one or four parts 1,764 and 1,957 instead of 1,718;
 // a warpgroup of its own for the outputs, with 128 registers for the rows, 1,668 instead of 1,582; masked
-// tiles 32 keys at a time 1,668 instead of 1,590; works placed by half a tile's cost for narrow ones, no gain;
+// tiles 32 keys at a time inside the loop 1,668 instead of 1,590; works placed by half a tile's cost for narrow ones, no gain;
 // outputs' loads from tensor memory ahead of their use 1,597 instead of 1,574.
 #pragma once
 
@@ -454,9 +454,10 @@ __device__ __forceinline__ bool tiles_in_order(const Streams &s, F tile) {
 struct MmaState {
     uint32_t stage = 0, parity = 0, n_q = 0, n_p[2] = {0, 0};   // the ring's next tile; works and P tiles so far
 };
-template <int D, bool BF16, int STAGES>
+// SPLIT: key tiles below `split` come as two, fp16 values and behind them what their rounding left.
+template <int D, bool BF16, int STAGES, bool SPLIT = false>
 __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, uint32_t tmem, uint32_t q_at, uint32_t ring, MmaState &st,
-                                           uint32_t *err) {
+                                           uint32_t *err, int split = 0) {
     constexpr uint32_t kS = mma_desc(BF16, false, kTile), kO = mma_desc(BF16, true, D);
     constexpr int DB = D / 64, STEPS = kTile / 16 / kParts;
     const int first = w.first[0];
@@ -472,13 +473,18 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
         }
         return wait_warp(&b.full[stage], parity, err);
     };
-    auto scores = [&](int t, uint32_t stage) {
-        const uint64_t q = mat_desc(q_at + (narrow ? 0 : t) * DB * kBlock, 16, 1024), k = mat_desc(ring + stage * DB * kBlock, 16, 1024);
+    auto scores = [&](int t, uint32_t stage, bool more, uint32_t rest) {
+        const uint64_t q = mat_desc(q_at + (narrow ? 0 : t) * DB * kBlock, 16, 1024);
+        auto product = [&](uint32_t of, bool add) {
+            const uint64_t k = mat_desc(ring + of * DB * kBlock, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t in = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + t * kTile, q + in, k + in, kS, kk > 0);
-        }
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t in = ((kk >> 2) * kBlock + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + t * kTile, q + in, k + in, kS, add || kk > 0);
+            }
+        };
+        product(stage, false);
+        if (SPLIT && more) product(rest, true);
         mma_commit(&b.s_full[t]);
     };
     auto values = [&](int t, uint32_t stage, bool fresh, bool done) {
@@ -501,7 +507,7 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
     ++st.n_q;
     // The streams in turn, t known at compile time: the product with the value tile that lies a step back, then scores of
     // key tile j.
-    uint32_t vs = 0, ks = 0;
+    uint32_t vs = 0, ks = 0, kr = 0;
     auto turn = [&](auto stream, int j) {
         constexpr int t = decltype(stream)::value;
         const int jv = j - w.step, end = w.end[t];
@@ -513,6 +519,10 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
             if (j < w.last) {
                 if (!next()) return false;
                 ks = stage;
+                if (SPLIT && j < split) {
+                    if (!next()) return false;
+                    kr = stage;
+                }
             }
         }
         if (jv >= first && jv < end) {
@@ -520,10 +530,11 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
         } else {
             tc_after();
         }
-        if (j < end) scores(t, ks);
+        if (j < end) scores(t, ks, SPLIT && j < split, kr);
         if (narrow || t == 1) {
             if (jv >= first && jv < w.last) mma_commit(&b.empty[vs]);
             if (j < w.last) mma_commit(&b.empty[ks]);
+            if (SPLIT && j < w.last && j < split) mma_commit(&b.empty[kr]);
             if (j == w.last - 1) mma_commit(&b.q_empty);
         }
         return true;

@@ -131,12 +131,45 @@ __device__ __forceinline__ void load8(const QRowsK &r, int64_t i, float (&x)[8])
     }
 }
 
+// fp16 inputs over caches of up to so many slots: keys count with all their bits, as a tile of fp16 values and one of what their
+// rounding left (SPLIT).  Where a row has few keys nothing averages their roundings out: 24 tokens over 54 slots 3.2e-4 of the
+// output in the norm, of which the output's own rounding is 2.1e-4, and 2.7e-4 so; over 256 2.7e-4 and 2.3e-4.  (64 tokens
+// over 1,000 slots 67 us instead of 44; decided work by work, by lengths, in one kernel: trees without them 2 to 25% slower.)
+constexpr int kSplitSlots = 256;
+
+// What the rounding of a tile's values to fp16 left, by the same units as the values, into the tile at `to`.
+template <int D>
+__device__ __noinline__ void make_rest(uint32_t codes, uint32_t to, int unit, int chunk, int in_unit) {
+    using C = TreeCfg<D>;
+    for (; unit < C::UNITS; unit += kMakers)
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const int r = unit * C::ROWS + in_unit + (i >> 2) * (C::ROWS / 2), k = i & 3;
+            uint32_t sz, word, v[4];
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sz) : "r"(codes + C::CODES + (r * C::DB + chunk / 2) * 4));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(codes + r * (D / 2) + chunk * 16 + 4 * k));
+            const __half2 hz = u2h(sz);
+            float s, z;
+            half2x(sz, s, z);
+            decode8(word, __low2half2(hz), __high2half2(hz), v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                half2x(h2u(__hmin2(u2h(v[e]), __float2half2_rn(65504.f))), lo, hi);
+                lo = fminf(fmaf((float)(word >> 4 * e & 15u), s, z), 65504.f) - lo;
+                hi = fminf(fmaf((float)(word >> (4 * e + 16) & 15u), s, z), 65504.f) - hi;
+                v[e] = half2_of(lo, hi);
+            }
+            sts16(to + chunk_at(r, (chunk & 1) * 4 + k), v);
+        }
+}
+
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan plan) {
     using C = TreeCfg<D>;
     constexpr int CH = C::CH;
@@ -348,6 +381,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 } else {
                     ++cached;
                     const int left = w.n_k - j * kTile;
+                    const uint32_t first = units;
 #pragma unroll 1
                     for (; units < C::UNITS; units += kMakers) {
                         const int r0 = units * C::ROWS + in_unit, mine = units * C::ROWS + (lane & (C::ROWS - 1));
@@ -389,12 +423,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                             for (int k = 0; k < 4; ++k) sts16(at ^ (k << 4), v[k]);   // chunk c0 + k, as c0 is 0 or 4
                         }
                     }
+                    const uint32_t rest = it % kTreeStages;
+                    const bool more = SPLIT && !value;
+                    if (more) {
+                        if (!wait_warp(&sh.bars.empty[rest], (it / kTreeStages & 1) ^ 1, a.err)) return false;
+                        ++it;
+                        make_rest<D>(codes, ring + (rest * C::DB + chunk / 2) * kBlock, first, chunk, in_unit);
+                    }
                     fence_async();
                     __syncwarp();
                     if (lane == 0) {
                         if (!value) mbar_arrive(&sh.seen_full[slot]);
                         mbar_arrive(&sh.raw_empty[from]);
                         mbar_arrive(&sh.bars.full[stage]);
+                        if (more) mbar_arrive(&sh.bars.full[rest]);
                     }
                 }
                 units -= C::UNITS;
@@ -455,7 +497,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
             w.j0 = uniform(w.j0);
             w.j1 = uniform(w.j1);
             w.narrow = uniform(w.narrow);
-            ok = issue_work<D, false, kTreeStages>(streams(w), sh.bars, tmem, q_at, ring, ms, a.err);
+            ok = issue_work<D, false, kTreeStages, SPLIT>(streams(w), sh.bars, tmem, q_at, ring, ms, a.err,
+                                                          SPLIT ? (uniform(w.n_k) + kTile - 1) / kTile : 0);
         }
         if (!ok) {
             mma_commit(&sh.bars.drain);
@@ -608,13 +651,13 @@ cudaError_t run_few(const TreeK &a, char *scratch, cudaStream_t s) {
     return e;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 cudaError_t run_tree(const TreeK &a, const Plan &plan, cudaStream_t s) {
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&tree_kernel<D, BF16>));
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(&tree_kernel<D, BF16, SPLIT>));
     if (e == cudaSuccess) e = launch(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, pdl_enabled(), a, plan);
     if (e != cudaSuccess) return e;
     const int64_t most = ((int64_t)a.c.batch * ((a.n + 2 * a.per - 1) / (2 * a.per)) + plan.recs) * a.kv;
-    e = launch(tree_kernel<D, BF16>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kTreeThreads), TreeCfg<D>::smem, s,
+    e = launch(tree_kernel<D, BF16, SPLIT>, dim3((unsigned)(most < a.sms ? most : a.sms)), dim3(kTreeThreads), TreeCfg<D>::smem, s,
                pdl_enabled(), a, plan);
     if (e == cudaSuccess && plan.recs > 0)
         e = launch(tree_join_kernel<D, BF16>, dim3(4 * a.sms), dim3(kJoinThreads), 0, s, pdl_enabled(), a, plan);
@@ -687,9 +730,11 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
         return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
     }
     auto go = [&](auto run) { return run(a, plan, (cudaStream_t)stream); };
-    const bool h = q->dtype == CS_F16;
-    const cudaError_t e = a.c.d == 64 ? (h ? go(run_tree<64, false>) : go(run_tree<64, true>))
-                                      : (h ? go(run_tree<128, false>) : go(run_tree<128, true>));
+    auto by_type = [&](auto d) {
+        if (q->dtype == CS_BF16) return go(run_tree<d(), true, false>);
+        return a.c.cap <= kSplitSlots ? go(run_tree<d(), false, true>) : go(run_tree<d(), false, false>);
+    };
+    const cudaError_t e = a.c.d == 64 ? by_type(std::integral_constant<int, 64>()) : by_type(std::integral_constant<int, 128>());
     return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
 }
 

@@ -590,7 +590,8 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
  * A parent outside [-1, t) counts as -1 and sets CS_DEVERR_INDEX.  Drafted rows count
  * as fp16 values, as the cache would take them: clamped to +-65504, NaN as 0.
  * 1 <= n <= 128, n_heads / cache->n_heads <= 128, n x n_heads / cache->n_heads
- * <= 1024; d_head 64 or 128.  Slots' values go into the products as fp16, q
+ * <= 1024; d_head 64 or 128.  Slots' values go into the products as fp16 (keys, for
+ * fp16 inputs over at most 256 slots of capacity, with all their bits), q
  * likewise (by row, times a power of two), or finer; sums and softmax statistics
  * are fp32.  The cache, its weights among it, is not changed.  With the same
  * arguments the results are the same bit for bit.

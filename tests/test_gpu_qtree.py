@@ -268,3 +268,28 @@ def test_scales_and_negative_scales():
         q, k, v = drafts(1, n, H, 2, 128, torch.float16, g)
         for scale in (0.03, -0.05):
             check(cpu, cache, q, k, v, torch.tensor([200]), parents(1, n, g), scale=scale)
+
+
+@pytest.mark.parametrize("H,kv,d,S,n", [(8, 2, 128, 54, 24), (8, 8, 64, 1, 40), (16, 1, 128, 250, 30), (8, 1, 64, 256, 5), (5, 1, 128, 129, 100)])
+def test_keys_of_short_contexts_count_in_full(H, kv, d, S, n):
+    """fp16: over caches of up to 256 slots keys are not rounded to 16 bits, so that a logit is off by what fp32 sums are, also where
+    channels are far from zero."""
+    g = gen(H, kv, d, S, n)
+    cache, cpu = filled(1, kv, S, d, g)
+    scales = cpu[1].clone()
+    scales[..., 1] += 3.0                 # the groups' offsets
+    cache.k_scale.copy_(scales)
+    q, k, v = drafts(1, n, H, kv, d, torch.float16, g)
+    q = q - 0.5 * q.mean(-1, keepdim=True)
+    tree = parents(1, n, g)
+    out, ws = run(without_positions(cache), q, k, v, torch.tensor([S]), tree)
+    assert cs.cs_get_device_error(ws) == 0
+    own = ref.paths(tree[0], n)
+    for h in range(H):
+        i = h // (H // kv)
+        keys = torch.cat([qref.values(cpu[0][0, i], scales[0, i]), ref.drafted(k[0, :, i])])
+        vals = torch.cat([qref.values(cpu[2][0, i], cpu[3][0, i]), ref.drafted(v[0, :, i])])
+        seen = torch.cat([torch.ones(n, S, dtype=torch.bool), own], 1)
+        want, bound = ref.rows(q[0, :, h].double(), keys, vals, seen, d ** -0.5, torch.float16, 2.0 ** -18,
+                               ref.half_step(torch.float16), ref.half_step(torch.float16))
+        assert ((out[0, :, h].cpu().double() - want).abs() <= bound).all()
