@@ -14,9 +14,9 @@
 // bits of fp16 and bf16 inputs down to 2^-29 of a row's largest.
 //
 // Bound (32 ragged sequences of up to 8,192 slots, trees of 64 tokens, 64 over 8 heads
-// of 128, bf16: 328 us, 835 TFLOP/s): a key tile for a pair of row tiles takes 4,600 cycles.  Issue slots are half
+// of 128, bf16: 325 us, 845 TFLOP/s): a key tile for a pair of row tiles takes 4,600 cycles.  Issue slots are half
 // used: P is 2 x 600 instructions a warp, a tile's 32,768 values 2,600 (three and a quarter per pair of codes), beside
-// which the products' bandwidth in shared memory makes every store and barrier slow.  Narrow work (16 tokens: 147 us) waits for
+// which the products' bandwidth in shared memory makes every store and barrier slow.  Narrow work (16 tokens: 133 us) waits for
 // its tiles: 2,600 cycles for one.  Tried: 10, 8 or 14 makers instead of 6 370, 335 and 454 us instead of 363, narrow work 150 instead of 152;
 // makers in three groups with a tile each 445 and 229; codes by each thread's own loads, three tiles ahead, 506 and 282.
 #include <cstddef>
