@@ -34,6 +34,7 @@ struct PromptK {
     QRowsK q, k, v, out;
     int heads, kv, group, d, batch, q_total, k_total, causal;
     const int32_t *q_start, *k_start;
+    int one;             // both starts are the same, cut to the same total
     float scale;
     uint32_t *err;
     int per;             // tokens of a row tile
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptK a, Pl
     pdl_wait();
     pdl_launch_dependents();
     plan_starts(a.q_start, a.batch, a.q_total, qs, scan, a.err);
-    if (a.k_start == a.q_start) ks = qs;
+    if (a.one) ks = qs;
     else plan_starts(a.k_start, a.batch, a.k_total, ks, scan, a.err);
     __syncthreads();
     const int pair = 2 * a.per;
@@ -143,7 +144,7 @@ __device__ __forceinline__ int own_list(const PromptK &a, Work *list) {
         if (lane <= a.batch && x != run) atomicOr(a.err, CS_DEVERR_COUNT);
         return run;
     };
-    const int q0 = starts(a.q_start, a.q_total), k0 = a.k_start == a.q_start ? q0 : starts(a.k_start, a.k_total);
+    const int q0 = starts(a.q_start, a.q_total), k0 = a.one ? q0 : starts(a.k_start, a.k_total);
     const int q1 = __shfl_down_sync(kFull, q0, 1), k1 = __shfl_down_sync(kFull, k0, 1);
     const int n = lane < a.batch ? (q1 - q0 + pair - 1) / pair : 0;
     int behind = n;   // the pairs of sequences up to this one
@@ -567,6 +568,7 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     a.causal = causal != 0;
     a.q_start = q_start;
     a.k_start = k_start ? k_start : q_start;
+    a.one = a.k_start == q_start && q_total == k_total;
     a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)d_head);
     a.err = static_cast<uint32_t *>(ws);
     a.per = kTile / a.group;

@@ -321,3 +321,22 @@ def test_lists_of_both_kinds_in_turn():
     graph.replay()
     assert all(torch.equal(w, g) for w, g in zip(want, got))
     assert cs.cs_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("batch", [3, 40])
+@pytest.mark.parametrize("tq,tk", [(300, 100), (100, 300)])
+def test_one_tensor_for_both_starts_of_different_totals(batch, tq, tk):
+    """The same starts passed twice are cut to each total by itself, as two tensors of them are."""
+    q, k, v = make([tq], [tk], 4, 2, 64, torch.bfloat16)
+    at = starts([0] * (batch - 3) + [90, 110, 100])
+    ws = cs.PromptWorkspace(batch, 4, 2, 64, tq, tk)
+    out, other = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    cs.cs_prompt_attention(q, k, v, out, at, ws, k_start=at, causal=False)
+    assert cs.cs_get_device_error(ws, clear=True) == cs.CS_DEVERR_COUNT
+    cs.cs_prompt_attention(q, k, v, other, at, ws, k_start=at.clone(), causal=False)
+    assert cs.cs_get_device_error(ws) == cs.CS_DEVERR_COUNT
+    assert torch.equal(out, other)
+    cut = lambda total: [min(x, total) for x in (0, 90, 200, 300)]  # noqa: E731
+    q_lens, k_lens = ([b - a for a, b in zip(x, x[1:])] for x in (cut(tq), cut(tk)))
+    want, bound = ref.prompt(q, k, v, q_lens, k_lens, False)
+    assert ((out.double() - want).abs() <= bound).all()
