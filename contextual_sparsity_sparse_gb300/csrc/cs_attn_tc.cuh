@@ -448,6 +448,26 @@ __device__ __forceinline__ bool tiles_in_order(const Streams &s, F tile) {
 
 // ------------------------------------------------------------- the products' warp
 
+// What is not finite in a tile in shared memory becomes 0; a whole warp, whose products read it next.
+template <bool BF16>
+__device__ __noinline__ void clean_tile(uint32_t at, int bytes) {
+    constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+    for (uint32_t x = at + (threadIdx.x & 31) * 16; x < at + bytes; x += 512) {
+        uint32_t v[4], bad = 0;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(x) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t out = ((v[i] & kExp) == kExp ? 0xffffu : 0u) | ((v[i] >> 16 & kExp) == kExp ? 0xffff0000u : 0u);
+            v[i] &= ~out;
+            bad |= out;
+        }
+        if (bad)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(x), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    }
+    fence_async();
+    __syncwarp();
+}
+
 // Issues a work's products; a whole warp, whose arguments are the same in all threads.  (With a warp for each stream both
 // streams' products share the tensor cores, and each stream waits twice as long for its own: 8,192 tokens of 16 heads 541 us
 // instead of 412.)
@@ -455,9 +475,10 @@ struct MmaState {
     uint32_t stage = 0, parity = 0, n_q = 0, n_p[2] = {0, 0};   // the ring's next tile; works and P tiles so far
 };
 // SPLIT: key tiles below `split` come as two, fp16 values and behind them what their rounding left.
-template <int D, bool BF16, int STAGES, bool SPLIT = false>
+// CLEAN: of value tiles from `clean` on, values that are not finite count as 0.
+template <int D, bool BF16, int STAGES, bool SPLIT = false, bool CLEAN = false>
 __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, uint32_t tmem, uint32_t q_at, uint32_t ring, MmaState &st,
-                                           uint32_t *err, int split = 0) {
+                                           uint32_t *err, int split = 0, int clean = 0) {
     constexpr uint32_t kS = mma_desc(BF16, false, kTile), kO = mma_desc(BF16, true, D);
     constexpr int DB = D / 64, STEPS = kTile / 16 / kParts;
     const int first = w.first[0];
@@ -515,6 +536,7 @@ __device__ __forceinline__ bool issue_work(const Streams &w, Bars<STAGES> &b, ui
             if (jv >= first && jv < w.last) {
                 if (!next()) return false;
                 vs = stage;
+                if (CLEAN && jv >= clean) clean_tile<BF16>(ring + vs * DB * kBlock, DB * kBlock);
             }
             if (j < w.last) {
                 if (!next()) return false;

@@ -614,7 +614,8 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
  * j <= i + (its keys - its query tokens): the last query token sees all, and
  * keys that lie before the queries (an earlier part of the prompt) may be given.
  * A row that sees no key gives zeros; what a row does not see has no influence
- * on it, NaN and infinities included.  Rows of out in no sequence are not written.
+ * on it, NaN and infinities included (rows beside such values are worked out
+ * twice).  Rows of out in no sequence are not written.
  *   q, out: [q_total, n_heads, d_head];  k, v: [k_total, kv_heads, d_head]; one
  *      dtype, fp16 or bf16, every row on a 16-byte boundary (else
  *      CS_ERR_INVALID); their ld_batch is not used.  out is none of the inputs.

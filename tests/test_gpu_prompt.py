@@ -340,3 +340,94 @@ def test_one_tensor_for_both_starts_of_different_totals(batch, tq, tk):
     q_lens, k_lens = ([b - a for a, b in zip(x, x[1:])] for x in (cut(tq), cut(tk)))
     want, bound = ref.prompt(q, k, v, q_lens, k_lens, False)
     assert ((out.double() - want).abs() <= bound).all()
+
+
+def fastest(f, n=5):
+    """The shortest of n runs, in ms."""
+    best = float("inf")
+    for _ in range(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("causal,lens,heads,kv,d,dt,bad", [
+    (False, [4090, 6], 8, 8, 128, torch.bfloat16, [4090]),           # the first value behind a sequence
+    (False, [4090, 6], 32, 4, 64, torch.float16, list(range(4090, 4096))),
+    (True, [4090, 6], 16, 2, 128, torch.bfloat16, [4091]),
+    (True, [4096], 8, 8, 64, torch.float16, list(range(127, 4096, 128)))])
+def test_values_that_are_not_seen_cost_no_more_than_the_works_again(causal, lens, heads, kv, d, dt, bad):
+    """Rows beside values that are not finite keep their bits, and the call its time within a small factor, although every key
+    that they see themselves is finite, or many are."""
+    q, k, v = make(lens, lens, heads, kv, d, dt)
+    clean, ws = call(q, k, v, lens, causal=causal)
+    out, s = torch.empty_like(q), starts(lens)
+    run = lambda: cs.cs_prompt_attention(q, k, v, out, s, ws, causal=causal)  # noqa: E731
+    before = fastest(run)
+    v[bad] = float("nan")
+    out.fill_(7.0)
+    after = fastest(run)
+    first = bad[0] if causal else lens[0]
+    assert torch.equal(out[:first], clean[:first])
+    assert torch.isnan(out[first:]).all() if causal else torch.isnan(out[lens[0]:]).all()
+    assert cs.cs_get_device_error(ws) == 0
+    assert after < 10 * before + 0.1, (before, after)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("d,group,keys", [(64, 1, 300), (128, 4, 300), (128, 1, 9000)])
+def test_seen_infinities_keep_their_sign(d, group, keys, dt):
+    """Infinities among the last keys, which some rows see and others do not: with their sign, and NaN where both are seen."""
+    n = 300
+    q, k, v = make([n], [keys], group, 1, d, dt)
+    q *= 0.1        # no weight far from the others
+    at = keys - n   # key at + i is query token i's own
+    v[at + 200, 0, 3], v[at + 250, 0, 7], v[at + 270, 0, 7], v[at + 280, 0, 9] = (float(x) for x in ("inf", "-inf", "inf", "nan"))
+    out, ws = call(q, k, v, [n], [keys])
+    clean = v.clone()
+    clean[~torch.isfinite(clean)] = 0.0
+    want, _ = call(q, k, clean, [n], [keys])
+    mended = out.clone()
+    for c, first, what in ((3, 200, torch.isposinf), (7, 250, lambda x: ~torch.isfinite(x)), (9, 280, torch.isnan)):
+        assert what(out[first:, :, c]).all() and torch.isfinite(out[:first, :, c]).all()
+        mended[first:, :, c] = want[first:, :, c]
+    assert torch.isneginf(out[250:270, :, 7]).all()
+    keep = torch.ones(d, dtype=torch.bool)
+    keep[[3, 7, 9]] = False
+    assert torch.equal(mended[..., keep], want[..., keep]) and torch.equal(mended[:200], want[:200])
+    assert cs.cs_get_device_error(ws) == 0
+
+
+def test_spoilt_works_of_a_long_list():
+    """More works to a CTA than have a mark of their own; sequences of one token, whose outputs are their values."""
+    batch, heads, d = 4096, 64, 64
+    lens = [1] * batch
+    q, k, v = make(lens, lens, heads, heads, d, torch.float16)
+    bad = torch.arange(batch, device="cuda") % 97 == 5
+    v[bad] = float("nan")
+    out, ws = call(q, k, v, lens)
+    assert torch.equal(out[~bad], v[~bad]) and torch.isnan(out[bad]).all()
+    assert cs.cs_get_device_error(ws) == 0
+
+
+def test_a_captured_call_beside_bad_values():
+    q, k, v = make([500, 200], [500, 200], 8, 2, 128, torch.bfloat16)
+    s = starts([500, 200])
+    clean, ws = call(q, k, v, [500, 200])
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cs.cs_prompt_attention(q, k, v, out, s, ws)
+    good = v[500].clone()
+    for _ in range(3):
+        v[500] = float("inf")
+        graph.replay()
+        assert torch.equal(out[:500], clean[:500]) and not torch.isfinite(out[500:]).any()
+        v[500] = good
+        graph.replay()
+        assert torch.equal(out, clean)
+    assert cs.cs_get_device_error(ws) == 0
