@@ -515,9 +515,9 @@ bool prompt_sizes(int batch, int n_heads, int kv_heads, int d_head, int q_total,
            q_total <= kMaxTokens && k_total >= 0 && k_total <= kMaxTokens;
 }
 
-// The list's place behind the control words; returns the bytes.
-size_t prompt_scratch(int batch, int n_heads, int kv_heads, int d, int q_total, int k_total, int sms, char *at, Plan *plan) {
-    const int per = kTile / (n_heads / kv_heads);
+// The list's place behind the control words, with groups of `group` heads; returns the bytes.
+size_t prompt_scratch(int batch, int group, int d, int q_total, int k_total, int sms, char *at, Plan *plan) {
+    const int per = kTile / group;
     const int recs = k_total > kUncut * kTile ? 2 * sms : 0;
     const size_t works = (size_t)q_total / (2 * per) + batch, own = (size_t)kOwnPairs * sms;   // (calls of smaller sizes may list their own)
     return plan_scratch(works > own ? works : own, recs, d, at, plan);
@@ -578,7 +578,9 @@ extern "C" {
 
 size_t cs_prompt_workspace_size(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total) {
     if (!prompt_sizes(batch, n_heads, kv_heads, d_head, q_total, k_total)) return 0;
-    return kControlBytes + prompt_scratch(batch, n_heads, kv_heads, d_head, q_total, k_total, device_sm_count(), nullptr, nullptr);
+    // calls of fewer key/value heads have larger groups, and so more works
+    const int group = n_heads < kMaxGroup ? n_heads : kMaxGroup;
+    return kControlBytes + prompt_scratch(batch, group, d_head, q_total, k_total, device_sm_count(), nullptr, nullptr);
 }
 
 cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, const cs_head_rows *v, int n_heads,
@@ -614,7 +616,7 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     CS_CHECK(scale == scale && scale - scale == 0.f, "%s: scale must be finite", who);
     a.sms = device_sm_count();
     Plan plan;
-    const size_t need = kControlBytes + prompt_scratch(batch, n_heads, kv_heads, d_head, q_total, k_total, a.sms,
+    const size_t need = kControlBytes + prompt_scratch(batch, n_heads / kv_heads, d_head, q_total, k_total, a.sms,
                                                        static_cast<char *>(ws) + kControlBytes, &plan);
     st = check_qws(ws, ws_bytes, need, who);
     if (st != CS_OK) return st;

@@ -606,28 +606,36 @@ bool tree_sizes(int batch, int kv_heads, int capacity, int d_head, int n_heads, 
            n_heads / kv_heads <= kTile && (int64_t)n_heads / kv_heads * n <= kQMaxRows;
 }
 
-// For few rows: the slots' outputs, the rows' statistics, and the other kernels' own.
+// For few rows, `rows` of them in all and `each` of a cache head: the slots' outputs, the rows' statistics, and the other kernels' own.
 struct FewScratch {
     size_t out, stat, attn;
+    size_t all() const { return out + stat + attn; }
 };
-FewScratch few_scratch(int batch, int kv_heads, int capacity, int d, int n_heads, int n, int sms) {
-    const size_t rows = (size_t)batch * n * n_heads;
+FewScratch few_scratch(int batch, int cap, int d, size_t rows, int each, int sms) {
     return FewScratch{align256(rows * d * sizeof(float)), align256(rows * sizeof(float2)),
-                      qattn_scratch(batch, kv_heads, capacity, d, n_heads, n, false, sms)};
+                      qattn_scratch(batch, 1, cap, d, each, 1, false, sms)};
+}
+// For more: the list's place behind the control words, with `pairs` pairs of row tiles; returns the bytes.
+size_t many_scratch(size_t pairs, int cap, int d, int sms, char *at, Plan *plan) {
+    return plan_scratch(pairs, cap > (kUncut - 1) * kTile ? 2 * sms : 0, d, at, plan);
+}
+int tree_pairs(int group, int n) { return (n + 2 * (kTile / group) - 1) / (2 * (kTile / group)); }
+
+// What calls of up to these sizes need: of fewer heads, tokens, or cache heads, and so of larger groups.
+size_t tree_scratch(int batch, int kv_heads, int cap, int d, int n_heads, int n, int sms) {
+    const int most = n_heads < kTile ? n_heads : kTile;
+    int pairs = 0;
+    for (int group = 1; group <= most; ++group) {
+        const int p = tree_pairs(group, n < kQMaxRows / group ? n : kQMaxRows / group);
+        pairs = p > pairs ? p : pairs;
+    }
+    const int rows = n_heads * n < kFewRows * kv_heads ? n_heads * n : kFewRows * kv_heads, each = most * n < kFewRows ? most * n : kFewRows;
+    const size_t many = many_scratch((size_t)batch * pairs, cap, d, sms, nullptr, nullptr);
+    const size_t few = few_scratch(batch, cap, d, (size_t)batch * rows, each, sms).all();
+    return many > few ? many : few;
 }
 
-// The list's place behind the control words; returns the bytes.
-size_t tree_scratch(int batch, int kv_heads, int capacity, int d, int n_heads, int n, int sms, char *at, Plan *plan) {
-    // what calls of fewer heads and tokens need is in it: for few rows, of as many as there can be
-    const int group = n_heads / kv_heads, few_rows = group * n < kFewRows ? group * n : kFewRows;
-    const FewScratch few = few_scratch(batch, kv_heads, capacity, d, kv_heads * few_rows, 1, sms);
-    const int pair = 2 * (kTile / group), recs = capacity > (kUncut - 1) * kTile ? 2 * sms : 0;
-    const size_t many = plan_scratch((size_t)batch * ((n + pair - 1) / pair), recs, d, at, plan), fewer = few.out + few.stat + few.attn;
-    return many > fewer ? many : fewer;
-}
-
-cudaError_t run_few(const TreeK &a, char *scratch, cudaStream_t s) {
-    const FewScratch need = few_scratch(a.c.batch, a.c.heads, a.c.cap, a.c.d, a.heads, a.n, a.sms);
+cudaError_t run_few(const TreeK &a, const FewScratch &need, char *scratch, cudaStream_t s) {
     float *out = reinterpret_cast<float *>(scratch);
     float2 *stat = reinterpret_cast<float2 *>(scratch + need.out);
     QAttnArgs q{};
@@ -674,7 +682,7 @@ extern "C" {
 
 size_t cs_qcache_tree_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n) {
     if (!tree_sizes(batch, kv_heads, capacity, d_head, n_heads, n)) return 0;
-    return kControlBytes + tree_scratch(batch, kv_heads, capacity, d_head, n_heads, n, device_sm_count(), nullptr, nullptr);
+    return kControlBytes + tree_scratch(batch, kv_heads, capacity, d_head, n_heads, n, device_sm_count());
 }
 
 cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q, const cs_head_rows *k,
@@ -709,9 +717,12 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
     a.heads = n_heads;
     a.group = n_heads / cache->n_heads;
     a.sms = device_sm_count();
+    char *scratch = static_cast<char *>(ws) + kControlBytes;
+    const bool few = a.group * n <= kFewRows;
     Plan plan;
-    const size_t need = kControlBytes + tree_scratch(a.c.batch, a.c.heads, a.c.cap, a.c.d, n_heads, n, a.sms, static_cast<char *>(ws) + kControlBytes, &plan);
-    st = check_qws(ws, ws_bytes, need, who);
+    const FewScratch parts = few_scratch(a.c.batch, a.c.cap, a.c.d, (size_t)a.c.batch * n * n_heads, few ? a.group * n : 1, a.sms);
+    const size_t need = few ? parts.all() : many_scratch((size_t)a.c.batch * tree_pairs(a.group, n), a.c.cap, a.c.d, a.sms, scratch, &plan);
+    st = check_qws(ws, ws_bytes, kControlBytes + need, who);
     if (st != CS_OK) return st;
     a.n = n;
     a.per = kTile / a.group;
@@ -721,12 +732,12 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
     a.n_new = n_new;
     a.scale = scale != 0.f ? scale : 1.f / sqrtf((float)cache->d_head);
     a.err = static_cast<uint32_t *>(ws);
-    if (a.group * n <= kFewRows) {
+    if (few) {
         if ((int64_t)cache->batch * cache->n_heads * ((cache->capacity + 15) / 16 + 32) >= INT32_MAX) {
             set_error("%s: batch x n_heads x capacity is too large", who);
             return CS_ERR_UNSUPPORTED;
         }
-        const cudaError_t e = run_few(a, static_cast<char *>(ws) + kControlBytes, (cudaStream_t)stream);
+        const cudaError_t e = run_few(a, parts, scratch, (cudaStream_t)stream);
         return e == cudaSuccess ? CS_OK : cuda_fail(e, who);
     }
     auto go = [&](auto run) { return run(a, plan, (cudaStream_t)stream); };

@@ -596,7 +596,8 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
  * are fp32.  The cache, its weights among it, is not changed.  With the same
  * arguments the results are the same bit for bit.
  * The workspace (on the current device; initialised once with cs_workspace_init)
- * serves calls of up to these sizes.
+ * serves calls of up to these sizes, also of fewer cache heads under as many
+ * query heads.
  */
 size_t cs_qcache_tree_workspace_size(int batch, int kv_heads, int capacity, int d_head, int n_heads, int n);
 cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q, const cs_head_rows *k,
@@ -627,7 +628,8 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
  * 128, tokens <= 2^24.  Sums and softmax statistics are fp32; the weights go into
  * the value products in the inputs' type.  With the same arguments the results
  * are the same bit for bit.  The workspace (on the current device; initialised
- * once with cs_workspace_init) serves calls of up to these sizes.
+ * once with cs_workspace_init) serves calls of up to these sizes, also of fewer
+ * key/value heads under as many query heads.
  */
 size_t cs_prompt_workspace_size(int batch, int n_heads, int kv_heads, int d_head, int q_total, int k_total);
 cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, const cs_head_rows *v, int n_heads,

@@ -431,3 +431,14 @@ def test_a_captured_call_beside_bad_values():
         graph.replay()
         assert torch.equal(out, clean)
     assert cs.cs_get_device_error(ws) == 0
+
+
+def test_a_workspace_serves_fewer_key_heads():
+    """More works than a workspace for as many key/value heads as query heads would list: 12,000 tokens, two to a pair."""
+    lens = [100] * 120
+    q, k, v = make(lens, lens, 128, 4, 64, torch.float16)
+    ws = cs.PromptWorkspace(120, 128, 128, 64, 12000)
+    for kv in (1, 2, 4):
+        out, _ = call(q, k[:, :kv], v[:, :kv], lens, ws=ws)
+        want, _ = call(q, k[:, :kv], v[:, :kv], lens)
+        assert torch.equal(out, want) and cs.cs_get_device_error(ws) == 0

@@ -293,3 +293,16 @@ def test_keys_of_short_contexts_count_in_full(H, kv, d, S, n):
         want, bound = ref.rows(q[0, :, h].double(), keys, vals, seen, d ** -0.5, torch.float16, 2.0 ** -18,
                                ref.half_step(torch.float16), ref.half_step(torch.float16))
         assert ((out[0, :, h].cpu().double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("H,n", [(8, 1), (16, 1), (8, 2), (64, 16)])
+def test_a_workspace_serves_caches_of_fewer_heads(H, n):
+    """Fewer cache heads under as many query heads: more rows of each, on one path or the other."""
+    g = gen(22, H, n)
+    ws = cs.QCacheTreeWorkspace(filled(3, H, 100, 128, g)[0], H, n)
+    for kv in (1, 2, H):
+        cache, cpu = filled(3, kv, 100, 128, g)
+        q, k, v = drafts(3, n, H, kv, 128, torch.bfloat16, g)
+        out, _ = run(cache, q, k, v, [100, 0, 57], ws=ws)
+        want, _ = run(cache, q, k, v, [100, 0, 57])
+        assert torch.equal(out, want) and cs.cs_get_device_error(ws) == 0

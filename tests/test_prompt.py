@@ -150,3 +150,19 @@ def test_plain_paths():
     p = ref.paths(torch.tensor([-1, 0, 0, 2, -1]), 5)
     assert [set(torch.nonzero(r).flatten().tolist()) for r in p] == [{0}, {0, 1}, {0, 2}, {0, 2, 3}, {4}]
     assert torch.equal(ref.paths(None, 4), torch.ones(4, 4, dtype=torch.bool).tril())
+
+
+def test_workspaces_of_larger_sizes_have_room_for_smaller_calls():
+    """Fewer key/value heads make larger groups, and so more works: sizes do not fall with any argument."""
+    lib_ = cs.lib()
+    heads = [(h, k) for k in (1, 2, 8, 64) for h in (1, 2, 8, 16, 64, 128) if h % k == 0 and h >= k]
+    sizes = {(b, h, k, d, t): lib_.cs_prompt_workspace_size(b, h, k, d, t, t)
+             for b in (1, 300) for h, k in heads for d in (64, 128) for t in (1, 500, 1025, 100000)}
+    trees = {(b, h, k, d, s, n): lib_.cs_qcache_tree_workspace_size(b, k, s, d, h, n)
+             for b in (1, 300) for h, k in heads for d in (64, 128) for s in (100, 5000) for n in (1, 3, 8)}
+    for table in (sizes, trees):
+        assert all(table.values())
+        for small, x in table.items():
+            for large, y in table.items():
+                if all(a <= b for a, b in zip(small, large)):
+                    assert x <= y, (small, large)
