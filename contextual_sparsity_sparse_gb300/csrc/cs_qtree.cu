@@ -132,9 +132,10 @@ __device__ __forceinline__ void load8(const QRowsK &r, int64_t i, float (&x)[8])
 }
 
 // fp16 inputs over caches of up to so many slots: keys count with all their bits, as a tile of fp16 values and one of what their
-// rounding left (SPLIT).  Where a row has few keys nothing averages their roundings out: 24 tokens over 54 slots 3.2e-4 of the
-// output in the norm, of which the output's own rounding is 2.1e-4, and 2.7e-4 so; over 256 2.7e-4 and 2.3e-4.  (64 tokens
-// over 1,000 slots 67 us instead of 44; decided work by work, by lengths, in one kernel: trees without them 2 to 25% slower.)
+// rounding left (SPLIT).  Where a row has few keys nothing averages their roundings out: 24 tokens over 54 slots 3.2e-4 to 3.7e-4 of
+// the output in the norm, of which the output's own rounding is 2.1e-4, and 2.7e-4 so; over 250 2.7e-4 to 3.6e-4, and 2.3e-4 to 2.5e-4.
+// The host knows a cache's capacity, not the lengths: few slots of a larger cache are rounded.  (64 tokens over 1,000 slots 67 us
+// instead of 44; decided work by work, by lengths, in one kernel: trees without them 2 to 25% slower.)
 constexpr int kSplitSlots = 256;
 
 // What the rounding of a tile's values to fp16 left, by the same units as the values, into the tile at `to`.

@@ -590,11 +590,15 @@ cs_status cs_qcache_fork(const cs_qcache *src, const int32_t *source, const int3
  * A parent outside [-1, t) counts as -1 and sets CS_DEVERR_INDEX.  Drafted rows count
  * as fp16 values, as the cache would take them: clamped to +-65504, NaN as 0.
  * 1 <= n <= 128, n_heads / cache->n_heads <= 128, n x n_heads / cache->n_heads
- * <= 1024; d_head 64 or 128.  Slots' values go into the products as fp16 (keys, for
- * fp16 inputs over at most 256 slots of capacity, with all their bits), q
- * likewise (by row, times a power of two), or finer; sums and softmax statistics
- * are fp32.  The cache, its weights among it, is not changed.  With the same
- * arguments the results are the same bit for bit.
+ * <= 1024; d_head 64 or 128.  Slots' values go into the products as fp16, q
+ * likewise (by row, times a power of two); sums and softmax statistics are fp32.
+ * Two forms are finer, chosen by the call's sizes alone, so that a row's last bits
+ * go by them too: up to 16 rows, n x n_heads / cache->n_heads, take the slots as
+ * cs_qcache_attention does, and fp16 inputs over a cache of at most 256 slots of
+ * capacity take keys with all their bits.  (Outputs of 24 tokens over 54 slots,
+ * in the norm: off by 2.7e-4 in a cache of 256 slots, by 3.7e-4 in one of 5,000; their
+ * rounding to fp16 alone is 2.1e-4.)  The cache, its weights among it, is not
+ * changed.  With the same arguments the results are the same bit for bit.
  * The workspace (on the current device; initialised once with cs_workspace_init)
  * serves calls of up to these sizes, also of fewer cache heads under as many
  * query heads.

@@ -306,3 +306,24 @@ def test_a_workspace_serves_caches_of_fewer_heads(H, n):
         out, _ = run(cache, q, k, v, [100, 0, 57], ws=ws)
         want, _ = run(cache, q, k, v, [100, 0, 57])
         assert torch.equal(out, want) and cs.cs_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("S", [256, 257, 5000])
+@pytest.mark.parametrize("H,kv,d,L,n", [(8, 2, 128, 54, 24), (16, 1, 64, 9, 40), (8, 1, 128, 250, 5)])
+def test_short_contexts_in_caches_of_any_capacity(H, kv, d, L, n, S):
+    """fp16: a context of few slots, in a cache that keys are rounded over and in one that they are not; within the bound of
+    rounded keys, and with the same contents the same bits but for that."""
+    g = gen(23, H, kv, d, L, n)
+    small, cpu = filled(2, kv, L, d, g)
+    cache = cs.QCache.empty(2, kv, S, d)
+    for name in ("k", "v", "k_scale", "v_scale", "weight", "pos"):
+        getattr(cache, name)[:, :, :L] = getattr(small, name)
+    q, k, v = drafts(2, n, H, kv, d, torch.float16, g)
+    tree, length = parents(2, n, g), torch.tensor([L, L - 4])
+    out = check(cpu, cache, q, k, v, length, tree)
+    alike, _ = run(small, q, k, v, length, tree)
+    if S <= 256 or H // kv * n <= 16:
+        assert torch.equal(out, alike)
+    else:
+        want, bound = ref.tree(*cpu[:4], cpu[5], q, k, v, length, tree)
+        assert ((alike.cpu().double() - want).abs() <= bound).all()
