@@ -122,36 +122,8 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *r) {
                  "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
                  : "memory");
 }
-__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t)
-                 : "memory");
-}
-__device__ __forceinline__ void tm_ld16(uint32_t t, float *v) {
-    uint32_t *r = reinterpret_cast<uint32_t *>(v);
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(t));
-}
 __device__ __forceinline__ void tm_st1(uint32_t t, float v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "f"(v) : "memory");
-}
-// N fp32 columns, or N / 2 of pairs.
-template <int N>
-__device__ __forceinline__ void tm_ld(uint32_t t, float *v) {
-    if (N == 32) tm_ld32(t, v);
-    else tm_ld16(t, v);
-}
-template <int N>
-__device__ __forceinline__ void tm_st(uint32_t t, const float *v) {
-    if (N == 32) tm_st32(t, v);
-    else tm_st16(t, reinterpret_cast<const uint32_t *>(v));
-}
-template <int N>
-__device__ __forceinline__ void tm_st_pairs(uint32_t t, const uint32_t *v) {
-    if (N == 32) tm_st16(t, v);
-    else tm_st8(t, v);
 }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -620,8 +592,7 @@ __device__ __noinline__ void hide_scores(uint32_t s_at, uint32_t w0, uint32_t w1
 
 // Stream t's key tiles first, first + step, ... below end: its rows' statistics in r, their sums of p v in tensor memory.
 // mask(j, w): what the warp's rows see of tile j, and unless it is all the bits of those keys.
-// CK: scores read at a time (16: fewer registers).
-template <int D, bool BF16, int CK, int STAGES, typename Mask>
+template <int D, bool BF16, int STAGES, typename Mask>
 __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, int step, int t, Bars<STAGES> &b, uint32_t tmem, float c,
                                              bool neg, uint32_t *err, Mask mask) {
     const uint32_t lane = ((threadIdx.x & 127) & ~31u) << 16;
@@ -649,7 +620,7 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], x[e + 4 + q]);
         }
-        constexpr int N = kTile / CK;
+        constexpr int CK = 32, N = kTile / CK;   // scores read at a time
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (__any_sync(kFull, top > lead)) {
             const float m = top > lead ? top : r.m;
@@ -673,12 +644,12 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
         const float add = fmaf(-base, c, kShift<BF16>);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         float s[2][CK];
-        tm_ld<CK>(s_at, s[0]);
+        tm_ld32(s_at, s[0]);
         tm_wait_ld();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float (&v)[CK] = s[i & 1];
-            if (i < N - 1) tm_ld<CK>(s_at + CK * (i + 1), s[(i + 1) & 1]);
+            if (i < N - 1) tm_ld32(s_at + CK * (i + 1), s[(i + 1) & 1]);
             uint32_t p[CK / 2];
 #pragma unroll
             for (int e = 0; e < CK / 2; ++e) {
@@ -691,7 +662,7 @@ __device__ __forceinline__ bool softmax_rows(RowState &r, int first, int end, in
             }
             // P's columns are half as many: they are of scores that have been read
             if (i < N - 1) tm_wait_ld();
-            tm_st_pairs<CK>(s_at + CK / 2 * i, p);
+            tm_st16(s_at + CK / 2 * i, p);
             if ((i + 1) % (N / kParts) == 0) {
                 tm_wait_st();
                 tc_before();

@@ -37,7 +37,7 @@ constexpr int kPromptThreads = 320;    // two warpgroups of rows, the products' 
 
 struct PromptK {
     QRowsK q, k, v, out;
-    int heads, kv, group, d, batch, q_total, k_total, causal;
+    int kv, group, batch, q_total, k_total, causal;
     const int32_t *q_start, *k_start;
     int one;             // both starts are the same, cut to the same total
     float scale;
@@ -304,7 +304,7 @@ __device__ __forceinline__ void prompt_works(const CUtensorMap *mq, const CUtens
             const int token = w.tok0 + at;
             const int lim = valid ? min(max(w.lim0 + step * at, 0), w.n_k) : 0;
             const int all = __reduce_min_sync(kFull, valid ? lim : INT_MAX);   // keys that all of the warp's rows see
-            if (!softmax_rows<D, BF16, 32>(r, st.first[t], st.end[t], st.step, t, bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
+            if (!softmax_rows<D, BF16>(r, st.first[t], st.end[t], st.step, t, bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
                     if (all >= (j + 1) * kTile) return SEE_ALL;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -621,10 +621,8 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     st = check_qws(ws, ws_bytes, need, who);
     if (st != CS_OK) return st;
     if (q_total == 0) return CS_OK;
-    a.heads = n_heads;
     a.kv = kv_heads;
     a.group = n_heads / kv_heads;
-    a.d = d_head;
     a.batch = batch;
     a.q_total = q_total;
     a.k_total = k_total;

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(TreeK a, Plan pla
                 mbar_arrive(&sh.bars.q_full);
             }
             const int drafted = (w.n_k + kTile - 1) / kTile;   // the tile of the drafted tokens
-            if (!softmax_rows<D, false, 32>(r, st.first[t], st.end[t], st.step, t, sh.bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
+            if (!softmax_rows<D, false>(r, st.first[t], st.end[t], st.step, t, sh.bars, tmem, c, neg, a.err, [&](int j, uint32_t (&m)[4]) {
                     const uint32_t n = tiles + (j - w.j0), s = n % kSeenRing;
                     wait_warp(&sh.seen_full[s], n / kSeenRing & 1, a.err);
                     if (j < drafted) {
