@@ -442,3 +442,12 @@ def test_a_workspace_serves_fewer_key_heads():
         out, _ = call(q, k[:, :kv], v[:, :kv], lens, ws=ws)
         want, _ = call(q, k[:, :kv], v[:, :kv], lens)
         assert torch.equal(out, want) and cs.cs_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("batch", [255, 256, 257, 700])
+def test_more_sequences_than_listing_threads(batch):
+    """Several sequences' starts to a thread of the list's kernel, empty ones and those with an earlier part among them."""
+    g = torch.Generator().manual_seed(batch)
+    q_lens = torch.randint(0, 6, (batch,), generator=g).tolist()
+    k_lens = [n + int(x) for n, x in zip(q_lens, torch.randint(0, 20, (batch,), generator=g))]
+    check(*make(q_lens, k_lens, 4, 2, 64, torch.bfloat16), q_lens, k_lens)

@@ -179,3 +179,27 @@ def test_replayed_forks_read_their_sources_anew():
         graph.replay()
         torch.cuda.synchronize()
         assert same(arrays(cache), want)
+
+
+@pytest.mark.parametrize("B,H,S,d,step", [(600, 1, 5, 128, 1), (300, 2, 70, 64, 7), (1792, 1, 3, 256, 5), (4096, 1, 2, 64, 1)])
+@pytest.mark.parametrize("how", ["in place", "in place, from a few", "into another"])
+def test_many_sequences(B, H, S, d, step, how):
+    """More sequences than a CTA has threads, up to as many as can change places (batch x d_head 458,752)."""
+    g = gen(B, H, S, d, step)
+    cache, _ = filled(B, H, S, d, g)
+    if how == "in place, from a few":      # that nobody writes
+        few = torch.randperm(B, generator=g)[:B // 2]
+        source = torch.full((B,), -1)
+        others = torch.ones(B, dtype=torch.bool)
+        others[few] = False
+        source[others] = few[torch.randint(0, len(few), (int(others.sum()),), generator=g)]
+        source = source.tolist()
+    else:
+        source = [(i + step) % B for i in range(B)]
+    length = torch.randint(0, S + 1, (B,), generator=g)
+    to = filled(B, H, S, d, gen(98))[0] if how == "into another" else cache
+    want = forked([t.clone() for t in arrays(cache)], arrays(to), source, length)
+    ws = cs.QCacheWorkspace(cache, n_heads=0)
+    cs.cs_qcache_fork(cache, ints(source), ints(length), ws, dst=to)
+    assert cs.cs_get_device_error(ws) == 0
+    assert same(arrays(to), want)

@@ -327,3 +327,20 @@ def test_short_contexts_in_caches_of_any_capacity(H, kv, d, L, n, S):
     else:
         want, bound = ref.tree(*cpu[:4], cpu[5], q, k, v, length, tree)
         assert ((alike.cpu().double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("H,kv,n,S", [(8, 1, 24, 200), (2, 1, 40, 300), (8, 1, 24, 5000)])
+def test_a_bad_row_among_many_stays_alone(H, kv, n, S, bad, dt):
+    """One query row of NaN or with an infinity, beside others of its row tile: it is not finite, they keep their bits."""
+    g = gen(24, H, n, S)
+    cache, cpu = filled(1, kv, S, 64, g)
+    q, k, v = drafts(1, n, H, kv, 64, dt, g)
+    clean, _ = run(cache, q, k, v, [S])
+    q[0, n - 7, H - 1, 9] = bad
+    out, ws = run(cache, q, k, v, [S])
+    keep = torch.ones(1, n, H, dtype=torch.bool)
+    keep[0, n - 7, H - 1] = False
+    assert not torch.isfinite(out[~keep]).any() and torch.equal(out[keep], clean[keep])
+    assert cs.cs_get_device_error(ws) == 0

@@ -166,3 +166,9 @@ def test_workspaces_of_larger_sizes_have_room_for_smaller_calls():
             for large, y in table.items():
                 if all(a <= b for a, b in zip(small, large)):
                     assert x <= y, (small, large)
+
+
+def test_more_than_can_change_places_is_refused(lib):
+    for batch, d in ((1793, 256), (3585, 128)):
+        c = cache(batch=batch, d_head=d, n_heads=1)
+        assert lib.cs_qcache_fork(ref_(c), P, P, None, P, 1 << 20, None) == UNSUPPORTED and lib.cs_last_error()
