@@ -590,10 +590,10 @@ cs_status cs_prompt_attention(const cs_head_rows *q, const cs_head_rows *k, cons
     const char *who = "cs_prompt_attention";
     PromptK a;
     CS_CHECK(q_total >= 0 && k_total >= 0, "%s: q_total and k_total must be >= 0 (%d, %d)", who, q_total, k_total);
-    cs_status st = check_rows(q, q_total == 0, "q", who, &a.q);
-    if (st == CS_OK) st = check_rows(k, k_total == 0, "k", who, &a.k);
-    if (st == CS_OK) st = check_rows(v, k_total == 0, "v", who, &a.v);
-    if (st == CS_OK) st = check_rows(out, q_total == 0, "out", who, &a.out);
+    cs_status st = check_packed(q, q_total, n_heads, q_total == 0, "q", who, &a.q);
+    if (st == CS_OK) st = check_packed(k, k_total, kv_heads, k_total == 0, "k", who, &a.k);
+    if (st == CS_OK) st = check_packed(v, k_total, kv_heads, k_total == 0, "v", who, &a.v);
+    if (st == CS_OK) st = check_packed(out, q_total, n_heads, q_total == 0, "out", who, &a.out);
     if (st != CS_OK) return st;
     CS_CHECK(q->dtype == k->dtype && q->dtype == v->dtype && q->dtype == out->dtype, "%s: q, k, v and out differ in dtype", who);
     CS_CHECK(batch >= 1 && n_heads >= 1 && kv_heads >= 1 && n_heads % kv_heads == 0,

@@ -861,6 +861,15 @@ cs_status check_rows(const cs_head_rows *r, bool empty, const char *name, const 
     return CS_OK;
 }
 
+cs_status check_packed(const cs_head_rows *r, int tokens, int heads, bool empty, const char *name, const char *who, QRowsK *out) {
+    if (!r) return check_rows(r, empty, name, who, out);
+    cs_head_rows packed = *r;
+    packed.ld_batch = 0;
+    if (tokens <= 1) packed.ld_token = 0;
+    if (heads == 1) packed.ld_head = 0;
+    return check_rows(&packed, empty, name, who, out);
+}
+
 cs_status check_qws(void *ws, size_t ws_bytes, size_t need, const char *who) {
     if (!ws || !aligned(ws, 256)) {
         set_error("%s: workspace is null or not 256-byte aligned", who);
@@ -915,10 +924,15 @@ cudaError_t launch_append(const QRowsCall &a, cudaStream_t s) {
 }
 
 cs_status rows_call(const cs_qcache *cache, const cs_head_rows *k, const cs_head_rows *v, int n, const int32_t *start,
-                    const int32_t *slots, void *ws, size_t ws_bytes, const char *who, QRowsCall *a, bool empty = false) {
+                    const int32_t *slots, void *ws, size_t ws_bytes, const char *who, QRowsCall *a, int n_rows = -1) {
     cs_status st = check_cache(cache, true, who, &a->c);
-    if (st == CS_OK) st = check_rows(k, n == 0 || empty, "k", who, &a->k);
-    if (st == CS_OK) st = check_rows(v, n == 0 || empty, "v", who, &a->v);
+    // n_rows: packed rows, or -1.  Without tokens, or rows that they could come from, k and v have no data
+    auto check = [&](const cs_head_rows *r, const char *name, QRowsK *out) {
+        return n_rows < 0 ? check_rows(r, n == 0, name, who, out)
+                          : check_packed(r, n_rows, cache->n_heads, n == 0 || n_rows == 0, name, who, out);
+    };
+    if (st == CS_OK) st = check(k, "k", &a->k);
+    if (st == CS_OK) st = check(v, "v", &a->v);
     if (st != CS_OK) return st;
     CS_CHECK(k->dtype == v->dtype, "%s: k and v differ in dtype", who);
     CS_CHECK(n >= 0 && n <= kMaxTokens, "%s: n=%d outside [0, %d]", who, n, kMaxTokens);
@@ -981,8 +995,7 @@ cs_status cs_qcache_append_rows(const cs_qcache *cache, const cs_head_rows *k, c
                                 const int32_t *pos, void *ws, size_t ws_bytes, cs_stream_t stream) {
     const char *who = "cs_qcache_append_rows";
     QRowsCall a;
-    // no rows at all: tokens have nothing to come from, and k and v no data
-    const cs_status st = rows_call(cache, k, v, n, start, slots, ws, ws_bytes, who, &a, n_rows == 0);
+    const cs_status st = rows_call(cache, k, v, n, start, slots, ws, ws_bytes, who, &a, n_rows);
     if (st != CS_OK) return st;
     CS_CHECK(n_rows >= 0 && n_rows <= kMaxTokens, "%s: n_rows=%d outside [0, %d]", who, n_rows, kMaxTokens);
     CS_CHECK(n == 0 || (rows && aligned(rows, 4)), "%s: rows is null or misaligned", who);

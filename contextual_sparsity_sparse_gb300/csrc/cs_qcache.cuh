@@ -46,6 +46,8 @@ inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintp
 cs_status check_cache(const cs_qcache *q, bool codes, const char *who, QCacheK *out);
 // empty: no tokens, so no data
 cs_status check_rows(const cs_head_rows *r, bool empty, const char *name, const char *who, QRowsK *out);
+// The same for [tokens, heads, d] rows, of whose strides those count that lead from one row to another.
+cs_status check_packed(const cs_head_rows *r, int tokens, int heads, bool empty, const char *name, const char *who, QRowsK *out);
 cs_status check_qws(void *ws, size_t ws_bytes, size_t need, const char *who);
 
 struct QAttnArgs {

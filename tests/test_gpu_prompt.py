@@ -451,3 +451,16 @@ def test_more_sequences_than_listing_threads(batch):
     q_lens = torch.randint(0, 6, (batch,), generator=g).tolist()
     k_lens = [n + int(x) for n, x in zip(q_lens, torch.randint(0, 20, (batch,), generator=g))]
     check(*make(q_lens, k_lens, 4, 2, 64, torch.bfloat16), q_lens, k_lens)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_token_and_one_head_of_any_stride(d):
+    """The only row there is starts on a 16-byte boundary, whatever the strides that lead to others."""
+    g = torch.Generator("cuda").manual_seed(6)
+    x = torch.randn(4, 1, d + 1, generator=g, device="cuda").half()
+    x = [torch.empty(d + 9, dtype=torch.float16, device="cuda")[:d + 1].copy_(t[0]).unsqueeze(0) for t in x]
+    q, k, v, out = (t[:, :d].unsqueeze(1) for t in x)
+    assert q.stride(0) % 8
+    ws = cs.PromptWorkspace(1, 1, 1, d, 1)
+    cs.cs_prompt_attention(q, k, v, out, starts([1]), ws)
+    assert torch.equal(out, v) and cs.cs_get_device_error(ws) == 0

@@ -172,3 +172,16 @@ def test_more_than_can_change_places_is_refused(lib):
     for batch, d in ((1793, 256), (3585, 128)):
         c = cache(batch=batch, d_head=d, n_heads=1)
         assert lib.cs_qcache_fork(ref_(c), P, P, None, P, 1 << 20, None) == UNSUPPORTED and lib.cs_last_error()
+
+
+def test_strides_that_no_row_is_reached_by_may_be_anything(lib):
+    """Between sequences, where rows are packed; between tokens or heads, where there is one."""
+    odd = dict(ldb=-5, ldt=512, ldh=128)
+    none = dict(tq=0, q=r16(None, **odd), out=r16(None, **odd))     # so that nothing is launched
+    assert prompt(lib, k=r16(2 * P, **odd), v=r16(3 * P, ldb=3, ldt=512, ldh=128), **none) == 0
+    one = dict(ldb=1, ldt=129, ldh=-3)
+    assert prompt(lib, heads=1, kv=1, tk=1, k=r16(2 * P, **one), v=r16(3 * P, **one), **none) == 0
+    assert prompt(lib, heads=1, kv=1, tk=2, k=r16(2 * P, **one), v=r16(3 * P, **one), **none) == INVALID
+    assert prompt(lib, heads=4, kv=2, tk=1, k=r16(2 * P, **one), v=r16(3 * P, **one), **none) == INVALID
+    append = lambda r: lib.cs_qcache_append_rows(ref_(cache()), ref_(r), ref_(r), 7, P, 0, P, None, P, P, 1 << 20, None)  # noqa: E731
+    assert append(rows(ldb=-1)) == 0 and append(rows(ldt=-1)) == INVALID
