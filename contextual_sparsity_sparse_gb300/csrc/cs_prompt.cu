@@ -29,9 +29,11 @@ namespace {
 
 constexpr int kMaxGroup = 128;         // query heads of one key/value head
 // Listed by every CTA itself are up to 32 pairs (a warp's lanes) of up to 31 sequences with up to kOwnTiles key tiles, which then
-// are not cut.  Without the first kernel, and without: 9 tokens of 8 heads 6.4 and 10.7 us, 2,048 of 40 heads 44.8 and 50, one
-// token over 2,048 keys 18 and 22 (two pieces a head); with twice the tiles 100 tokens of 8 heads to a key head over 4,096 keys
-// 52 instead of 34.
+// are not cut.  Without the first and third kernels, and with them: 9 tokens of 8 heads 6.4 and 10.7 us, 10 prompts of 200 of 32 heads
+// 24 and 29, 2,048 tokens of 40 heads 45 and 50; but where few works see many keys, cutting them is worth more: 100 tokens of 8 heads to
+// a key head over 2,000 keys 30 and 22, one token over 2,048 18 and 17.  The tiles are those of all sequences together, which is all
+// that the host knows.  With room for 32 of them 16 prompts of 200 tokens of 8 heads 12 us instead of 18, one of 2,304 of 40 heads 55
+// instead of 61, but 100 tokens over 2,500 keys 35 instead of 23, over 4,096 52 instead of 24.
 constexpr int kOwnPairs = 32, kOwnTiles = 16;
 constexpr int kPromptThreads = 320;    // two warpgroups of rows, the products' warp, the loads' warp
 

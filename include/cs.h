@@ -630,8 +630,9 @@ cs_status cs_qcache_tree_attention(const cs_qcache *cache, const cs_head_rows *q
  *   scale: the factor on q . k; 0 means 1 / sqrt(d_head).
  * d_head is 64 or 128; batch <= 4096, n_heads <= 1024, n_heads / kv_heads <=
  * 128, tokens <= 2^24.  Sums and softmax statistics are fp32; the weights go into
- * the value products in the inputs' type.  With the same arguments the results
- * are the same bit for bit.  The workspace (on the current device; initialised
+ * the value products in the inputs' type (bf16: values below 2^-106 lose bits,
+ * below 2^-120 all).  With the same arguments the results are the same bit for
+ * bit.  The workspace (on the current device; initialised
  * once with cs_workspace_init) serves calls of up to these sizes, also of fewer
  * key/value heads under as many query heads.
  */

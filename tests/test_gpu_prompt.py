@@ -464,3 +464,11 @@ def test_one_token_and_one_head_of_any_stride(d):
     ws = cs.PromptWorkspace(1, 1, 1, d, 1)
     cs.cs_prompt_attention(q, k, v, out, starts([1]), ws)
     assert torch.equal(out, v) and cs.cs_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [([300], [300]), ([5], [20000])])
+def test_small_values_of_bf16(q_lens, k_lens):
+    """Values near 2^-96: a key's p v is off by at most 2^-150 more, and the largest alone is 2^-128 (p of it 2^-32), of which
+    300 keys' are 2^-14 at most; 20,000 with logits of a width of 1 to 2 have sums of 100 times that."""
+    q, k, v = make(q_lens, k_lens, 4, 1, 64, torch.bfloat16)
+    check(q, k, (v.double() * 2.0 ** -96).to(torch.bfloat16), q_lens, k_lens)
