@@ -204,8 +204,8 @@ __device__ __forceinline__ int first_masked(const Work &w) { return min(max(w.li
 // What a warp's rows see of values that are not finite, in a work done without them, whose key `from` is the first of a tile
 // that they may have been taken out of.  A thread has a row and its place: `to`, behind the last key that it sees (not falling
 // from row to row; 0: not to be looked at), add, what p = 2^(c s + add) is taken against, and inv, the factor of its sums, or rec, where
-// they are.  Per row and channel one such value is added, the last: with it the sum is not finite either way.  Lane l has
-// channels N l ..; a key's values are read once for all rows, and a row's scores with keys of such values alone worked out.
+// they are.  Per row and channel one such value is added, the last, or NaN where there are infinities of both signs, or a NaN.
+// Lane l has channels N l ..; a key's values are read once for all rows, and a row's scores with those last keys alone worked out.
 template <typename T, int D>
 __device__ __noinline__ void add_seen(const PromptK &a, int64_t k0, int h, int from, int token, int head, int to, float c, float add,
                                       float inv, float *rec) {
@@ -217,8 +217,12 @@ __device__ __noinline__ void add_seen(const PromptK &a, int64_t k0, int h, int f
     const T *k = reinterpret_cast<const T *>(a.k.p) + k0 * a.k.ldt + h * a.k.ldh + ch;
     const T *v = reinterpret_cast<const T *>(a.v.p) + k0 * a.v.ldt + h * a.v.ldh + ch;
     int last[N], done = from;   // the last key before `done` with such a value, or -1
+    bool up[N], down[N];        // whether there was one above 0 (or NaN), below 0 (or NaN)
 #pragma unroll
-    for (int i = 0; i < N; ++i) last[i] = -1;
+    for (int i = 0; i < N; ++i) {
+        last[i] = -1;
+        up[i] = down[i] = false;
+    }
     for (uint32_t rows = __ballot_sync(kFull, to > from); rows; rows &= rows - 1) {
         const int row = __ffs(rows) - 1, end = __shfl_sync(kFull, to, row);
         for (int j = done; j < end; j += STEP) {
@@ -228,8 +232,13 @@ __device__ __noinline__ void add_seen(const PromptK &a, int64_t k0, int h, int f
 #pragma unroll
             for (int e = 0; e < STEP; ++e)
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (!isfinite((float)y[e].x[i])) last[i] = min(j + e, end - 1);
+                for (int i = 0; i < N; ++i) {
+                    const float x = (float)y[e].x[i];
+                    if (isfinite(x)) continue;
+                    last[i] = min(j + e, end - 1);
+                    up[i] |= !(x < 0.f);
+                    down[i] |= !(x > 0.f);
+                }
         }
         done = max(done, end);
         int left[N], key = -1;
@@ -253,7 +262,7 @@ __device__ __noinline__ void add_seen(const PromptK &a, int64_t k0, int h, int f
             for (int i = 0; i < N; ++i) {
                 if (left[i] == key) {
                     left[i] = -1;
-                    const float o = p * (float)vv.x[i];
+                    const float o = up[i] && down[i] ? NAN : p * (float)vv.x[i];
                     if (to_rec) __stcg(to_rec + (2 + ch + i) * kPair, __ldcg(to_rec + (2 + ch + i) * kPair) + o);
                     else to_out[i] = (T)((float)to_out[i] + o * f);
                 }

@@ -472,3 +472,20 @@ def test_small_values_of_bf16(q_lens, k_lens):
     300 keys' are 2^-14 at most; 20,000 with logits of a width of 1 to 2 have sums of 100 times that."""
     q, k, v = make(q_lens, k_lens, 4, 1, 64, torch.bfloat16)
     check(q, k, (v.double() * 2.0 ** -96).to(torch.bfloat16), q_lens, k_lens)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("d,group,keys", [(64, 1, 300), (128, 4, 300), (128, 1, 9000)])
+def test_infinities_of_both_signs_are_nan(d, group, keys, dt):
+    """Both among the keys that not all rows of a work see; and NaN before an infinity."""
+    n = 300
+    q, k, v = make([n], [keys], group, 1, d, dt)
+    q *= 0.1
+    at = keys - n
+    for i, c, x in ((258, 3, "-inf"), (264, 3, "inf"), (258, 5, "nan"), (264, 5, "inf"), (258, 6, "inf"), (264, 6, "inf")):
+        v[at + i, 0, c] = float(x)
+    out, ws = call(q, k, v, [n], [keys])
+    assert torch.isfinite(out[:258]).all()
+    assert torch.isneginf(out[258:264, :, 3]).all() and torch.isnan(out[264:, :, 3]).all()
+    assert torch.isnan(out[258:, :, 5]).all() and torch.isposinf(out[258:, :, 6]).all()
+    assert cs.cs_get_device_error(ws) == 0
